@@ -8,12 +8,20 @@
 #include <cstdint>
 #include <cstdlib>
 
+#include "api_checks.hpp"
 #include "ssm.h"
 #include "ssm_kernels.hpp"
 
 namespace {
 
+using ssm::aligned;
 using ssm::Dtype;
+using ssm::elem_bytes;
+using ssm::round256;
+using ssm::shapes_fit;
+using ssm::Span;
+using ssm::span;
+using ssm::writes_overlap;
 
 // The forward scan's workgroups are sized so that five fit on a CU (20
 // waves); the planner splits a sequence into segments only as far as needed
@@ -70,8 +78,6 @@ bool use_wave_kernel(int dstate, bool conv) {
 
 bool dstate_ok(int n) { return n == 1 || n == 2 || n == 4 || n == 8 || n == 16; }
 
-int elem_bytes(int dtype) { return dtype == SSM_BF16 ? 2 : 4; }
-
 bool flags_ok(int flags) { return (flags & ~(SSM_DELTA_SOFTPLUS | SSM_BBAR_ZOH)) == 0; }
 
 // Segments of the sequence for the forward scan.  A chosen segment length is
@@ -114,8 +120,6 @@ SegPlan plan_segments(int batch, int dim, int dstate, int64_t L, int dtype) {
 struct WsLayout {
   size_t bc, hend, sumdt, total;
 };
-
-size_t round256(size_t x) { return (x + 255) / 256 * 256; }
 
 WsLayout workspace_layout(int batch, int dim, int dstate, int64_t L, int dtype, const SegPlan& sp) {
   WsLayout w{};
@@ -175,39 +179,6 @@ BwdWsLayout bwd_workspace_layout(int batch, int dim, int dstate, int64_t L, int 
   return w;
 }
 
-bool aligned(const void* p, size_t a) { return p == nullptr || (reinterpret_cast<uintptr_t>(p) % a) == 0; }
-
-// The byte range [lo, hi) a buffer occupies; a null pointer or zero bytes
-// occupies none.  Aliasing is judged on these ranges, not on pointer
-// equality, so an output that starts inside an input (or ends inside one) is
-// rejected too.
-struct Span {
-  uintptr_t lo, hi;
-};
-
-Span span(const void* p, size_t bytes) {
-  const uintptr_t lo = reinterpret_cast<uintptr_t>(p);
-  if (p == nullptr || bytes == 0) return Span{0, 0};
-  return Span{lo, lo + bytes};
-}
-
-bool overlap(const Span& a, const Span& b) {
-  return a.hi > a.lo && b.hi > b.lo && a.lo < b.hi && b.lo < a.hi;
-}
-
-// Whether a buffer the call writes overlaps another buffer the call writes,
-// or one it reads.  Inputs may overlap each other (they are only read).
-template <size_t NO, size_t NI>
-bool writes_overlap(const Span (&outs)[NO], const Span (&ins)[NI]) {
-  for (size_t i = 0; i < NO; ++i) {
-    for (size_t j = i + 1; j < NO; ++j)
-      if (overlap(outs[i], outs[j])) return true;
-    for (size_t j = 0; j < NI; ++j)
-      if (overlap(outs[i], ins[j])) return true;
-  }
-  return false;
-}
-
 // The scan kernels' vectorised paths address the rows of a 64-channel group
 // through buffer descriptors with a 32-bit per-lane offset (channel * L +
 // step) * element bytes.  Every lane of the group forms one, also the lanes
@@ -217,15 +188,6 @@ bool writes_overlap(const Span (&outs)[NO], const Span (&ins)[NI]) {
 // element-wise path.
 bool group_rows_fit(int64_t seqlen, size_t es) {
   return (long double)64 * (long double)seqlen * (long double)es < (long double)INT32_MAX;
-}
-
-// The scan kernels keep step positions in 32 bits.
-constexpr int64_t kMaxSeqlen = INT32_MAX - 4096;
-
-bool shapes_fit(int batch, int dim, int64_t seqlen) {
-  if (batch < 0 || dim < 0 || seqlen < 0 || seqlen > kMaxSeqlen) return false;
-  const long double total = (long double)batch * (long double)dim * (long double)(seqlen > 0 ? seqlen : 1);
-  return total < (long double)(INT64_C(1) << 60);
 }
 
 }  // namespace
