@@ -1,4 +1,4 @@
-"""ctypes view of libssm.so (include/ssm.h).  Loading fails loudly when the
+"""ctypes view of libssm.so (include/ssm.h, ssm_gated.h, ssm_norm.h).  Loading fails loudly when the
 library has not been built: there is no other implementation to fall back to."""
 from __future__ import annotations
 
@@ -10,6 +10,7 @@ from .build import LIB, INCLUDE
 
 SSM_F32, SSM_BF16 = 0, 1
 SSM_DELTA_SOFTPLUS, SSM_BBAR_ZOH = 1, 2
+SSM_GATE_SOFTPLUS, SSM_GATE_UNIT = 1, 2
 _lib = None
 
 
@@ -19,9 +20,9 @@ class SsmError(RuntimeError):
         super().__init__(f"{where}: {status_string(status)} ({status})")
 
 
-def header_functions() -> list[str]:
-    """Names of the functions include/ssm.h declares."""
-    with open(os.path.join(INCLUDE, "ssm.h")) as f:
+def header_functions(header: str = "ssm.h") -> list[str]:
+    """Names of the functions that a header of include/ declares."""
+    with open(os.path.join(INCLUDE, header)) as f:
         text = f.read()
     text = re.sub(r"/\*.*?\*/", "", text, flags=re.S)
     return re.findall(r"\b(ssm_\w+)\s*\(", text)
@@ -76,6 +77,27 @@ def load():
         lib.ssm_scan_fwd_noalloc.argtypes = [vp, vp, fp, vp, vp, fp, vp, fp, i32, fp, vp, fp,
                                              i32, i32, i32, i64, i32, vp]
         lib.ssm_scan_fwd_noalloc.restype = i32
+    lib.ssm_gated_scan_ckpt_bytes.argtypes = [i32, i32, i64]
+    lib.ssm_gated_scan_ckpt_bytes.restype = sz
+    lib.ssm_gated_scan_fwd_workspace_bytes.argtypes = [i32, i32, i64, i32]
+    lib.ssm_gated_scan_fwd_workspace_bytes.restype = sz
+    lib.ssm_gated_scan_bwd_workspace_bytes.argtypes = [i32, i32, i64, i32]
+    lib.ssm_gated_scan_bwd_workspace_bytes.restype = sz
+    lib.ssm_gated_scan_fwd.argtypes = [vp, vp, fp, fp, vp, fp, vp, i32, vp, fp, vp, fp, fp, sz,
+                                       i32, i32, i64, i32, vp, sz, vp]
+    lib.ssm_gated_scan_fwd.restype = i32
+    lib.ssm_gated_scan_bwd.argtypes = [vp, vp, fp, fp, vp, fp, vp, i32, vp, fp, sz, vp, fp, vp, vp, fp,
+                                       fp, vp, fp, vp, fp, i32, i32, i64, i32, vp, sz, vp]
+    lib.ssm_gated_scan_bwd.restype = i32
+    lib.ssm_gated_state_update.argtypes = [fp, vp, vp, fp, fp, vp, fp, vp, i32, vp, vp, fp, i32, i32,
+                                           i32, vp]
+    lib.ssm_gated_state_update.restype = i32
+    lib.ssm_layer_norm_fwd.argtypes = [vp, vp, fp, fp, ctypes.c_float, vp, vp, fp, fp, i32, i32, i64, i32, vp]
+    lib.ssm_layer_norm_fwd.restype = i32
+    lib.ssm_layer_norm_bwd_workspace_bytes.argtypes = [i32, i32, i64, i32]
+    lib.ssm_layer_norm_bwd_workspace_bytes.restype = sz
+    lib.ssm_layer_norm_bwd.argtypes = [vp, fp, fp, fp, vp, vp, vp, fp, fp, i32, i32, i64, i32, vp, sz, vp]
+    lib.ssm_layer_norm_bwd.restype = i32
     lib.ssm_status_string.argtypes = [i32]
     lib.ssm_status_string.restype = ctypes.c_char_p
     _lib = lib

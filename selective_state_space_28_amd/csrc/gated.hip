@@ -1,0 +1,442 @@
+// gated.hip -- the gated linear recurrence over whole sequences, its backward
+// pass and its one-token step, for gfx950 (include/ssm_gated.h states it).
+//
+// Per channel h_t = a_t h_{t-1} + v_t with a_t = exp(A g_t), v_t = w_t u_t.
+// There is one state per channel, so nothing is gained by giving a lane a
+// channel as the selective scan does: a wave walks one row (b, d) in blocks of
+// 512 steps, each lane holding 8 consecutive ones (16 bytes of bf16), so every
+// access of a wave is 1 KiB in one piece.  A lane composes its 8 steps into
+// the map h -> P h + Q, the maps are composed over the wave by a prefix (six
+// DPP rounds), and each lane reruns its steps from the state entering them:
+// one pass over HBM, no LDS.  P = exp2 of the sum of the steps' exponents.
+//
+// The backward pass walks the blocks from last to first.  It forms the gates
+// again, the states from the block's kept entering state, and the adjoint
+// lambda_t = dh_t + a_{t+1} lambda_{t+1} by the same prefix over the mirrored
+// lanes (its map m -> P m + Q carries m_t = a_t lambda_t to the left).
+#include "gated_math.hpp"
+#include "ssm_kernels.hpp"
+
+namespace ssm {
+
+namespace {
+
+constexpr int kRowsPerGroup = 4;  // rows (waves) of a workgroup
+
+struct GatedSizes {
+  int rows, dim;
+  int seqlen, nblk;
+};
+
+}  // namespace
+
+template <typename T, int RULE, bool IG, bool ZG>
+__global__ __launch_bounds__(64 * kRowsPerGroup) void gated_fwd_kernel(
+    const T* __restrict__ x, const T* __restrict__ r, const float* __restrict__ A,
+    const float* __restrict__ r_bias, const T* __restrict__ ig, const float* __restrict__ i_bias,
+    const T* __restrict__ z, const uint8_t* __restrict__ starts, const float* __restrict__ h0,
+    T* __restrict__ y, float* __restrict__ last_state, float* __restrict__ ckpt, const GatedSizes p) {
+  const int lane = threadIdx.x & 63;
+  const int row = blockIdx.x * kRowsPerGroup + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  if (row >= p.rows) return;
+  const int b = row / p.dim, d = row - b * p.dim;
+  const float Ad = A[d];
+  const float A2 = Ad * kLog2e;
+  const float An = (RULE & kGateUnit) != 0 ? 2.0f * Ad : Ad;
+  const float rb = r_bias != nullptr ? r_bias[d] : 0.0f;
+  const float ib = IG && i_bias != nullptr ? i_bias[d] : 0.0f;
+  const int64_t base = (int64_t)row * p.seqlen;
+  float H = h0 != nullptr ? h0[row] : 0.0f;
+
+  for (int blk = 0; blk < p.nblk; ++blk) {
+    const int t0 = blk * kGatedBlock + lane * kRun;
+    const int valid = p.seqlen - t0;  // steps of this lane's run inside the row (may be <= 0)
+    const bool whole = (blk + 1) * kGatedBlock <= p.seqlen;
+    const int v = whole ? kRun : valid;
+    const RunWords<T> wr = load_run(r + base + t0, v), wx = load_run(x + base + t0, v);
+    RunWords<T> wi, wz;
+    if constexpr (IG) wi = load_run(ig + base + t0, v);
+    if constexpr (ZG) wz = load_run(z + base + t0, v);
+    uint32_t cut = 0;
+    if (starts != nullptr) cut = load_starts(starts + (int64_t)b * p.seqlen + t0, v);
+    if (ckpt != nullptr && lane == 0) ckpt[((int64_t)b * p.nblk + blk) * p.dim + d] = H;
+
+    float fr[kRun], fx[kRun], fi[kRun], a[kRun], q[kRun];
+    run_floats<T>(wr, fr);
+    run_floats<T>(wx, fx);
+    if constexpr (IG) run_floats<T>(wi, fi);
+    float S = 0.0f;  // exponent of the run's decay
+#pragma unroll
+    for (int k = 0; k < kRun; ++k) {
+      const float pre = fr[k] + rb;
+      const float g = (RULE & kGateSoftplus) != 0 ? softplus_f32(pre) : sigmoid_f32(pre);
+      const float e2 = A2 * g;
+      a[k] = decay_of(e2);
+      q[k] = weight_of<RULE>(a[k], An, g) * fx[k];
+      if constexpr (IG) q[k] *= sigmoid_f32(fi[k] + ib);
+      if (!whole && k >= valid) {  // past the end: the identity
+        a[k] = 1.0f;
+        q[k] = 0.0f;
+      } else {
+        S += e2;
+      }
+    }
+    float P = __builtin_fmaxf(exp2_hw(S), kMinNormal), Q = 0.0f, h;
+    if (starts != nullptr) {
+#pragma unroll
+      for (int k = 0; k < kRun; ++k) {
+        if (cut & (1u << k)) a[k] = 0.0f;
+        Q = apply_map<true>(a[k], q[k], Q);
+      }
+      if (cut != 0) P = 0.0f;
+      wave_prefix<true>(P, Q);
+      const float end = apply_map<true>(P, Q, H);
+      h = lane_before(end, H);
+      H = lane_value(end, 63);
+#pragma unroll
+      for (int k = 0; k < kRun; ++k) q[k] = h = apply_map<true>(a[k], q[k], h);
+    } else {
+#pragma unroll
+      for (int k = 0; k < kRun; ++k) Q = __builtin_fmaf(a[k], Q, q[k]);
+      wave_prefix<false>(P, Q);
+      const float end = __builtin_fmaf(P, H, Q);
+      h = lane_before(end, H);
+      H = lane_value(end, 63);
+#pragma unroll
+      for (int k = 0; k < kRun; ++k) q[k] = h = __builtin_fmaf(a[k], h, q[k]);
+    }
+    if constexpr (ZG) {
+      float fz[kRun];
+      run_floats<T>(wz, fz);
+#pragma unroll
+      for (int k = 0; k < kRun; ++k) q[k] *= silu_f32(fz[k]);
+    }
+    store_run<T>(y + base + t0, v, q);
+  }
+  if (last_state != nullptr && lane == 0) last_state[row] = H;
+}
+
+template <typename T, int RULE, bool IG, bool ZG>
+__global__ __launch_bounds__(64 * kRowsPerGroup) void gated_bwd_kernel(
+    const T* __restrict__ x, const T* __restrict__ r, const float* __restrict__ A,
+    const float* __restrict__ r_bias, const T* __restrict__ ig, const float* __restrict__ i_bias,
+    const T* __restrict__ z, const uint8_t* __restrict__ starts, const float* __restrict__ ckpt,
+    const T* __restrict__ dy, const float* __restrict__ dlast, T* __restrict__ dx, T* __restrict__ dr,
+    T* __restrict__ di, T* __restrict__ dz, float* __restrict__ row_dA, float* __restrict__ row_drb,
+    float* __restrict__ row_dib, float* __restrict__ dh0, const GatedSizes p) {
+  const int lane = threadIdx.x & 63;
+  const int row = blockIdx.x * kRowsPerGroup + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  if (row >= p.rows) return;
+  const int b = row / p.dim, d = row - b * p.dim;
+  const float Ad = A[d];
+  const float A2 = Ad * kLog2e;
+  const float An = (RULE & kGateUnit) != 0 ? 2.0f * Ad : Ad;
+  const float rb = r_bias != nullptr ? r_bias[d] : 0.0f;
+  const float ib = IG && i_bias != nullptr ? i_bias[d] : 0.0f;
+  const int64_t base = (int64_t)row * p.seqlen;
+  float M = dlast != nullptr ? dlast[row] : 0.0f;  // a_{t+1} lambda_{t+1} entering from the right
+  // the row's sums, over up to 2^31 steps: in float64 across blocks
+  double sA = 0.0, srb = 0.0, sib = 0.0;
+
+  for (int blk = p.nblk - 1; blk >= 0; --blk) {
+    const int t0 = blk * kGatedBlock + lane * kRun;
+    const int valid = p.seqlen - t0;
+    const bool whole = (blk + 1) * kGatedBlock <= p.seqlen;
+    const int v = whole ? kRun : valid;
+    const RunWords<T> wr = load_run(r + base + t0, v), wx = load_run(x + base + t0, v);
+    const RunWords<T> wd = load_run(dy + base + t0, v);
+    RunWords<T> wi, wz;
+    if constexpr (IG) wi = load_run(ig + base + t0, v);
+    if constexpr (ZG) wz = load_run(z + base + t0, v);
+    const bool packed = starts != nullptr;
+    uint32_t cut = 0;
+    if (packed) cut = load_starts(starts + (int64_t)b * p.seqlen + t0, v);
+    const float H = ckpt[((int64_t)b * p.nblk + blk) * p.dim + d];
+
+    float fr[kRun], fx[kRun], fi[kRun], ad[kRun], w[kRun], q[kRun], gi[kRun], dh[kRun];
+    run_floats<T>(wr, fr);
+    run_floats<T>(wx, fx);
+    run_floats<T>(wd, dh);
+    if constexpr (IG) run_floats<T>(wi, fi);
+    float S = 0.0f;
+#pragma unroll
+    for (int k = 0; k < kRun; ++k) {
+      const float pre = fr[k] + rb;
+      const float g = (RULE & kGateSoftplus) != 0 ? softplus_f32(pre) : sigmoid_f32(pre);
+      const float e2 = A2 * g;
+      ad[k] = decay_of(e2);
+      w[k] = weight_of<RULE>(ad[k], An, g);
+      q[k] = w[k] * fx[k];
+      if constexpr (IG) {
+        gi[k] = sigmoid_f32(fi[k] + ib);
+        q[k] *= gi[k];
+      }
+      if (!whole && k >= valid) {
+        ad[k] = 1.0f;
+        q[k] = 0.0f;
+      } else {
+        S += e2;
+      }
+    }
+    const float P = cut != 0 ? 0.0f : __builtin_fmaxf(exp2_hw(S), kMinNormal);
+
+    // the states: hb[k] before step k (0 at a start), q[k] after it
+    float hb[kRun];
+    {
+      float Pf = P, Q = 0.0f, h;
+      if (packed) {
+#pragma unroll
+        for (int k = 0; k < kRun; ++k) Q = apply_map<true>((cut & (1u << k)) ? 0.0f : ad[k], q[k], Q);
+        wave_prefix<true>(Pf, Q);
+        h = lane_before(apply_map<true>(Pf, Q, H), H);
+#pragma unroll
+        for (int k = 0; k < kRun; ++k) {
+          hb[k] = (cut & (1u << k)) ? 0.0f : h;
+          q[k] = h = __builtin_fmaf(ad[k], hb[k], q[k]);
+        }
+      } else {
+#pragma unroll
+        for (int k = 0; k < kRun; ++k) Q = __builtin_fmaf(ad[k], Q, q[k]);
+        wave_prefix<false>(Pf, Q);
+        h = lane_before(__builtin_fmaf(Pf, H, Q), H);
+#pragma unroll
+        for (int k = 0; k < kRun; ++k) {
+          hb[k] = h;
+          q[k] = h = __builtin_fmaf(ad[k], h, q[k]);
+        }
+      }
+    }
+
+    // the output gate: dz, and dh = dy silu(z)
+    if constexpr (ZG) {
+      float fz[kRun], o[kRun];
+      run_floats<T>(wz, fz);
+#pragma unroll
+      for (int k = 0; k < kRun; ++k) {
+        float s, c;
+        sigmoid_pair(fz[k], s, c);
+        o[k] = dh[k] * q[k] * (s * __builtin_fmaf(fz[k], c, 1.0f));
+        dh[k] *= fz[k] * s;
+      }
+      store_run<T>(dz + base + t0, v, o);
+    }
+
+    // the adjoint entering the run from the right
+    float m = 0.0f;
+    {
+      float Q = 0.0f;
+      if (packed) {
+#pragma unroll
+        for (int k = kRun - 1; k >= 0; --k) Q = (cut & (1u << k)) ? 0.0f : ad[k] * (dh[k] + Q);
+      } else {
+#pragma unroll
+        for (int k = kRun - 1; k >= 0; --k) Q = ad[k] * (dh[k] + Q);
+      }
+      float Pr = lane_mirror(P, lane), Qr = lane_mirror(Q, lane), end;
+      if (packed) {
+        wave_prefix<true>(Pr, Qr);
+        end = apply_map<true>(Pr, Qr, M);
+      } else {
+        wave_prefix<false>(Pr, Qr);
+        end = __builtin_fmaf(Pr, M, Qr);
+      }
+      m = lane_mirror(lane_before(end, M), lane);
+      M = lane_value(end, 63);
+    }
+
+    // the gradients of each step, from the right
+    float odx[kRun], odr[kRun], odi[kRun];
+    float pA = 0.0f, prb = 0.0f, pib = 0.0f;
+#pragma unroll
+    for (int k = kRun - 1; k >= 0; --k) {
+      const float lam = dh[k] + m;
+      m = ad[k] * lam;
+      if (packed && (cut & (1u << k))) m = 0.0f;
+      const float pre = fr[k] + rb;
+      float g, slope, s, c;
+      sigmoid_pair(pre, s, c);
+      if constexpr ((RULE & kGateSoftplus) != 0) {
+        g = softplus_f32(pre);
+        slope = s;
+      } else {
+        g = s;
+        slope = s * c;
+      }
+      const float u = IG ? fx[k] * gi[k] : fx[k];
+      const float lw = lam * w[k];
+      odx[k] = IG ? lw * gi[k] : lw;
+      // dw/de: -a, or -a^2 / w (0 where w is 0)
+      float bend = ad[k];
+      if constexpr ((RULE & kGateUnit) != 0) bend = w[k] > 0.0f ? ad[k] * ad[k] * rcp_hw(w[k]) : 0.0f;
+      float de = lam * (ad[k] * hb[k] - u * bend);
+      if (!whole && k >= valid) de = 0.0f;
+      odr[k] = de * Ad * slope;
+      pA = __builtin_fmaf(de, g, pA);
+      prb += odr[k];
+      if constexpr (IG) {
+        float sg, cg;
+        sigmoid_pair(fi[k] + ib, sg, cg);
+        odi[k] = lw * fx[k] * sg * cg;
+        pib += odi[k];
+      }
+    }
+    store_run<T>(dx + base + t0, v, odx);
+    store_run<T>(dr + base + t0, v, odr);
+    if constexpr (IG) store_run<T>(di + base + t0, v, odi);
+    sA += (double)pA;
+    srb += (double)prb;
+    if constexpr (IG) sib += (double)pib;
+  }
+
+#pragma unroll
+  for (int off = 1; off < 64; off <<= 1) {
+    sA += __shfl_xor(sA, off);
+    srb += __shfl_xor(srb, off);
+    if constexpr (IG) sib += __shfl_xor(sib, off);
+  }
+  if (lane == 0) {
+    row_dA[row] = (float)sA;
+    if (row_drb != nullptr) row_drb[row] = (float)srb;
+    if (IG && row_dib != nullptr) row_dib[row] = (float)sib;
+    if (dh0 != nullptr) dh0[row] = M;
+  }
+}
+
+// The rows' sums over the batch: out[k][d] = sum_b part[k][b][d], in float64 in
+// the order of the batch.
+__global__ __launch_bounds__(256) void gated_sum_kernel(const float* __restrict__ part, float* __restrict__ dA,
+                                                        float* __restrict__ drb, float* __restrict__ dib,
+                                                        int batch, int dim) {
+  const int d = blockIdx.x * 256 + threadIdx.x;
+  float* out = blockIdx.y == 0 ? dA : blockIdx.y == 1 ? drb : dib;
+  if (d >= dim || out == nullptr) return;
+  const float* p = part + (int64_t)blockIdx.y * batch * dim + d;
+  double s = 0.0;
+  for (int b = 0; b < batch; ++b) s += (double)p[(int64_t)b * dim];
+  out[d] = (float)s;
+}
+
+// One token of every channel: a lane per channel.
+template <typename T, int RULE, bool IG, bool ZG>
+__global__ __launch_bounds__(256) void gated_step_kernel(
+    const float* state, const T* __restrict__ x, const T* __restrict__ r, const float* __restrict__ A,
+    const float* __restrict__ r_bias, const T* __restrict__ ig, const float* __restrict__ i_bias,
+    const T* __restrict__ z, const uint8_t* __restrict__ starts, T* __restrict__ y, float* state_out, int b0,
+    int dim) {
+  const int d = blockIdx.x * 256 + threadIdx.x;
+  if (d >= dim) return;
+  const int b = b0 + (int)blockIdx.y;
+  const int64_t at = (int64_t)b * dim + d;
+  const float Ad = A[d];
+  const float pre = Elem<T>::load(r + at) + (r_bias != nullptr ? r_bias[d] : 0.0f);
+  const float g = (RULE & kGateSoftplus) != 0 ? softplus_f32(pre) : sigmoid_f32(pre);
+  const float a = decay_of(Ad * kLog2e * g);
+  float h = weight_of<RULE>(a, (RULE & kGateUnit) != 0 ? 2.0f * Ad : Ad, g) * Elem<T>::load(x + at);
+  if constexpr (IG) h *= sigmoid_f32(Elem<T>::load(ig + at) + (i_bias != nullptr ? i_bias[d] : 0.0f));
+  if (starts == nullptr || starts[b] == 0) h = __builtin_fmaf(a, state[at], h);
+  state_out[at] = h;
+  if constexpr (ZG) h *= silu_f32(Elem<T>::load(z + at));
+  Elem<T>::store(y + at, h);
+}
+
+namespace {
+
+// Calls f<RULE, IG, ZG> with the launch's rule and gates as constants.
+template <typename F>
+hipError_t by_rule(const GatedLaunch& a, F&& f) {
+  auto gates = [&](auto rule) {
+    constexpr int R = decltype(rule)::value;
+    if (a.i != nullptr)
+      return a.z != nullptr ? f.template operator()<R, true, true>() : f.template operator()<R, true, false>();
+    return a.z != nullptr ? f.template operator()<R, false, true>() : f.template operator()<R, false, false>();
+  };
+  const int rule = (a.softplus ? kGateSoftplus : 0) | (a.unit ? kGateUnit : 0);
+  switch (rule) {
+    case 0: return gates(std::integral_constant<int, 0>{});
+    case 1: return gates(std::integral_constant<int, 1>{});
+    case 2: return gates(std::integral_constant<int, 2>{});
+    default: return gates(std::integral_constant<int, 3>{});
+  }
+}
+
+GatedSizes sizes_of(const GatedLaunch& a) {
+  return GatedSizes{a.batch * a.dim, a.dim, (int)a.seqlen, (int)((a.seqlen + kGatedBlock - 1) / kGatedBlock)};
+}
+
+template <typename T>
+struct FwdLaunch {
+  const GatedLaunch& a;
+  hipStream_t stream;
+  template <int RULE, bool IG, bool ZG>
+  hipError_t operator()() const {
+    const GatedSizes s = sizes_of(a);
+    const unsigned grid = (unsigned)((s.rows + kRowsPerGroup - 1) / kRowsPerGroup);
+    gated_fwd_kernel<T, RULE, IG, ZG><<<grid, 64 * kRowsPerGroup, 0, stream>>>(
+        static_cast<const T*>(a.x), static_cast<const T*>(a.r), a.A, a.r_bias, static_cast<const T*>(a.i),
+        a.i_bias, static_cast<const T*>(a.z), a.starts, a.h0, static_cast<T*>(a.y), a.last_state, a.ckpt, s);
+    return hipGetLastError();
+  }
+};
+
+template <typename T>
+struct BwdLaunchOf {
+  const GatedLaunch& a;
+  hipStream_t stream;
+  template <int RULE, bool IG, bool ZG>
+  hipError_t operator()() const {
+    const GatedSizes s = sizes_of(a);
+    const unsigned grid = (unsigned)((s.rows + kRowsPerGroup - 1) / kRowsPerGroup);
+    // one row per channel: its sums are the results
+    const bool direct = a.batch == 1;
+    const int64_t plane = (int64_t)a.batch * a.dim;
+    gated_bwd_kernel<T, RULE, IG, ZG><<<grid, 64 * kRowsPerGroup, 0, stream>>>(
+        static_cast<const T*>(a.x), static_cast<const T*>(a.r), a.A, a.r_bias, static_cast<const T*>(a.i),
+        a.i_bias, static_cast<const T*>(a.z), a.starts, a.ckpt, static_cast<const T*>(a.dy), a.dlast,
+        static_cast<T*>(a.dx), static_cast<T*>(a.dr), static_cast<T*>(a.di), static_cast<T*>(a.dz),
+        direct ? a.dA : a.part, direct ? a.dr_bias : a.part + plane, direct ? a.di_bias : a.part + 2 * plane,
+        a.dh0, s);
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess || direct) return e;
+    gated_sum_kernel<<<dim3((unsigned)((a.dim + 255) / 256), IG ? 3 : 2), 256, 0, stream>>>(
+        a.part, a.dA, a.dr_bias, a.di_bias, a.batch, a.dim);
+    return hipGetLastError();
+  }
+};
+
+template <typename T>
+struct StepLaunch {
+  const GatedLaunch& a;
+  hipStream_t stream;
+  template <int RULE, bool IG, bool ZG>
+  hipError_t operator()() const {
+    constexpr int kMaxRows = 65535;  // grid y per launch
+    for (int b0 = 0; b0 < a.batch; b0 += kMaxRows) {
+      const int nb = a.batch - b0 < kMaxRows ? a.batch - b0 : kMaxRows;
+      gated_step_kernel<T, RULE, IG, ZG><<<dim3((unsigned)((a.dim + 255) / 256), (unsigned)nb), 256, 0, stream>>>(
+          a.h0, static_cast<const T*>(a.x), static_cast<const T*>(a.r), a.A, a.r_bias,
+          static_cast<const T*>(a.i), a.i_bias, static_cast<const T*>(a.z), a.starts, static_cast<T*>(a.y),
+          a.last_state, b0, a.dim);
+      const hipError_t e = hipGetLastError();
+      if (e != hipSuccess) return e;
+    }
+    return hipSuccess;
+  }
+};
+
+}  // namespace
+
+hipError_t launch_gated_fwd(const GatedLaunch& a, hipStream_t stream) {
+  return a.dtype == Dtype::BF16 ? by_rule(a, FwdLaunch<uint16_t>{a, stream}) : by_rule(a, FwdLaunch<float>{a, stream});
+}
+
+hipError_t launch_gated_bwd(const GatedLaunch& a, hipStream_t stream) {
+  return a.dtype == Dtype::BF16 ? by_rule(a, BwdLaunchOf<uint16_t>{a, stream})
+                                : by_rule(a, BwdLaunchOf<float>{a, stream});
+}
+
+hipError_t launch_gated_step(const GatedLaunch& a, hipStream_t stream) {
+  return a.dtype == Dtype::BF16 ? by_rule(a, StepLaunch<uint16_t>{a, stream})
+                                : by_rule(a, StepLaunch<float>{a, stream});
+}
+
+}  // namespace ssm

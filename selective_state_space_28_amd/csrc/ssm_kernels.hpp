@@ -1,5 +1,5 @@
 // ssm_kernels.hpp -- host-side launch interface between the C ABI layer
-// (ssm_api.cpp) and the HIP kernels (scan_fwd.hip, state_update.hip).
+// (ssm_api.cpp, layers_api.cpp) and the HIP kernels.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -173,6 +173,72 @@ struct SsdLaunch {
   Dtype dtype;
 };
 
+// The gated recurrence (include/ssm_gated.h): whole sequences, their backward,
+// and one token.  A wave works on kGatedBlock consecutive steps of a row at a
+// time; the forward pass keeps the state entering each block for the backward.
+constexpr int kGatedBlock = 512;
+
+struct GatedLaunch {
+  const void* x;
+  const void* r;
+  const float* A;
+  const float* r_bias;    // nullable
+  const void* i;          // nullable
+  const float* i_bias;    // nullable
+  const void* z;          // nullable
+  const uint8_t* starts;  // nullable
+  const float* h0;        // nullable; the token's state for a step
+  void* y;
+  float* last_state;      // nullable; the state after the token for a step
+  float* ckpt;            // (batch, nblk, dim) nullable; read by the backward
+  int softplus, unit;     // the gate's and the input weight's rule
+  int batch, dim;
+  int64_t seqlen;
+  Dtype dtype;
+  // backward only
+  const void* dy;
+  const float* dlast;     // nullable
+  void* dx;
+  void* dr;
+  void* di;               // required when i is given
+  void* dz;               // required when z is given
+  float* dA;
+  float* dr_bias;         // nullable
+  float* di_bias;         // nullable
+  float* dh0;             // nullable
+  float* part;            // (3, batch, dim) sums of each row (batch > 1)
+};
+
+// Layer norm over the channels of (batch, dim, seqlen) (include/ssm_norm.h).
+struct NormLaunch {
+  const void* x;          // the backward: what was normalised
+  const void* residual;   // nullable
+  const float* weight;
+  const float* bias;      // nullable
+  float eps;
+  void* y;
+  void* sum_out;          // with residual
+  float* mean;            // nullable in the forward
+  float* rstd;            // nullable in the forward
+  int batch, dim;
+  int64_t seqlen;
+  Dtype dtype;
+  // backward only
+  const void* dy;
+  const void* dsum;       // nullable
+  void* dx;
+  float* dweight;
+  float* dbias;           // nullable
+  float* part;            // (norm_bwd_parts, 2, dim) partial sums
+};
+// Workgroups that each leave one partial sum of dweight and dbias.
+int norm_bwd_parts(int batch, int dim, int64_t seqlen);
+
+hipError_t launch_gated_fwd(const GatedLaunch& a, hipStream_t stream);
+hipError_t launch_gated_bwd(const GatedLaunch& a, hipStream_t stream);
+hipError_t launch_gated_step(const GatedLaunch& a, hipStream_t stream);
+hipError_t launch_norm_fwd(const NormLaunch& a, hipStream_t stream);
+hipError_t launch_norm_bwd(const NormLaunch& a, hipStream_t stream);
 hipError_t launch_scan_fwd(const ScanLaunch& a, hipStream_t stream);
 // Packs only the B, C records into a.ws_bc (a backward pass whose checkpoints
 // came from the forward pass needs them and nothing else of launch_scan_fwd).
