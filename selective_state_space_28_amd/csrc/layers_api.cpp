@@ -61,13 +61,13 @@ GatedLaunch gated_launch(const void* x, const void* r, const float* A, const flo
   return a;
 }
 
-// The norm numbers its tokens' workgroups in 32 bits (tiles of 32 steps).
+// The norm numbers its tiles in 32 bits (of 8 steps and more).
 bool norm_shape_ok(int batch, int dim, int64_t seqlen) {
-  return dim >= 1 && shapes_fit(batch, dim, seqlen) && (int64_t)batch * ((seqlen + 31) / 32) <= INT_MAX - 64;
+  return dim >= 1 && dim <= INT_MAX - 65536 && shapes_fit(batch, dim, seqlen) && (int64_t)batch * ((seqlen + 7) / 8) <= INT_MAX - 4096;
 }
 
-size_t norm_bwd_ws_bytes(int batch, int dim, int64_t seqlen) {
-  return round256((size_t)norm_bwd_parts(batch, dim, seqlen) * 2 * (size_t)dim * sizeof(float));
+size_t norm_bwd_ws_bytes(int batch, int dim, int64_t seqlen, int dtype) {
+  return round256((size_t)norm_bwd_parts(batch, dim, seqlen, elem_bytes(dtype)) * 2 * (size_t)dim * sizeof(float));
 }
 
 }  // namespace
@@ -253,7 +253,7 @@ int ssm_layer_norm_fwd(const void* x, const void* residual, const float* weight,
 
 size_t ssm_layer_norm_bwd_workspace_bytes(int batch, int dim, int64_t seqlen, int dtype) {
   if (!dtype_ok(dtype) || !norm_shape_ok(batch, dim, seqlen) || batch == 0 || seqlen == 0) return 0;
-  return norm_bwd_ws_bytes(batch, dim, seqlen);
+  return norm_bwd_ws_bytes(batch, dim, seqlen, dtype);
 }
 
 int ssm_layer_norm_bwd(const void* s, const float* weight, const float* mean, const float* rstd, const void* dy,
@@ -269,7 +269,7 @@ int ssm_layer_norm_bwd(const void* s, const float* weight, const float* mean, co
       !aligned(mean, 4) || !aligned(rstd, 4) || !aligned(dweight, 4) || !aligned(dbias, 4) ||
       !aligned(workspace, 256))
     return SSM_ERR_ALIGN;
-  const size_t need = empty ? 0 : norm_bwd_ws_bytes(batch, dim, seqlen);
+  const size_t need = empty ? 0 : norm_bwd_ws_bytes(batch, dim, seqlen, dtype);
   if (need > 0 && (workspace == nullptr || workspace_bytes < need)) return SSM_ERR_WORKSPACE;
   const size_t tokens = (size_t)batch * (size_t)seqlen, all = tokens * (size_t)dim * es, ch = (size_t)dim * 4;
   const Span outs[] = {span(dx, all), span(dweight, ch), span(dbias, ch), span(workspace, need)};

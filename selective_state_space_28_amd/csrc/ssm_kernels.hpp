@@ -232,7 +232,7 @@ struct NormLaunch {
   float* part;            // (norm_bwd_parts, 2, dim) partial sums
 };
 // Workgroups that each leave one partial sum of dweight and dbias.
-int norm_bwd_parts(int batch, int dim, int64_t seqlen);
+int norm_bwd_parts(int batch, int dim, int64_t seqlen, int elem_bytes);
 
 hipError_t launch_gated_fwd(const GatedLaunch& a, hipStream_t stream);
 hipError_t launch_gated_bwd(const GatedLaunch& a, hipStream_t stream);

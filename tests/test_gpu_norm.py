@@ -216,7 +216,9 @@ def test_nothing_is_written_beside_the_outputs(dev, dtype, shape, axis):
 
 
 def test_offsets_past_32_bits(dev):
-    """More than 2^31 elements in either layout: the last token is that of a call on it alone."""
+    """More than 2^31 elements in either layout: the last tokens are those of a call on them alone.  Another number of
+    tokens may add the channels in another order: two roundings to bf16 of values that agree to float32 are then at
+    most a step apart, 2^-7 of the value (a value near 0, of float32's error of the largest)."""
     import torch
     import selective_state_space_28_amd as ssm
     w = torch.linspace(0.5, 1.5, 4096, device=dev)
@@ -233,10 +235,12 @@ def test_offsets_past_32_bits(dev):
     x = x.view(1, 4096, 540000)
     y, m, r = ssm.ssm_layer_norm_fwd(x, w, axis=1, return_stats=True)
     end = x[:, :, -64:].contiguous()
-    assert torch.equal(y[:, :, -64:], ssm.ssm_layer_norm_fwd(end, w, axis=1))
+    near = lambda u, v: bool(((u.float() - v.float()).abs()  # noqa: E731
+                              <= 2.0 ** -7 * v.float().abs() + 4 * SLACK).all())
+    assert near(y[:, :, -64:], ssm.ssm_layer_norm_fwd(end, w, axis=1))
     g = ssm.ssm_layer_norm_bwd(x, w, m, r, y, axis=1)
     one = ssm.ssm_layer_norm_bwd(end, w, m[:, -64:].contiguous(), r[:, -64:].contiguous(), y[:, :, -64:].contiguous(), axis=1)
-    assert torch.equal(g["dx"][:, :, -64:], one["dx"])
+    assert near(g["dx"][:, :, -64:], one["dx"])
 
 
 def test_refusals(dev):
