@@ -8,7 +8,12 @@
 // access of a wave is 1 KiB in one piece.  A lane composes its 8 steps into
 // the map h -> P h + Q, the maps are composed over the wave by a prefix (six
 // DPP rounds), and each lane reruns its steps from the state entering them:
-// one pass over HBM, no LDS.  P = exp2 of the sum of the steps' exponents.
+// one pass over HBM.  P = exp2 of the sum of the steps' exponents.
+//
+// Where there are too few rows to fill the chip with a wave each, W waves take a
+// row's blocks in turn, W at a time: each wave's map over its block goes to the
+// others through LDS (a barrier for every W blocks), and each applies those before
+// its own to the row's state.
 //
 // The backward pass walks the blocks from last to first.  It forms the gates
 // again, the states from the block's kept entering state, and the adjoint
@@ -21,24 +26,60 @@ namespace ssm {
 
 namespace {
 
-constexpr int kRowsPerGroup = 4;  // rows (waves) of a workgroup
+// Waves of a workgroup with W waves to a row: 4 rows of one wave, else one row.
+constexpr int group_waves(int W) { return W == 1 ? 4 : W; }
 
 struct GatedSizes {
   int rows, dim;
   int seqlen, nblk;
 };
 
+// A wave's total map, for the other waves of its row; two buffers, so that one
+// barrier for every W blocks is enough.
+template <int W>
+struct RowMaps {
+  float P[2][W], Q[2][W];
+};
+
+// The value that enters wave `w` of a row's W, whose waves map it in the order
+// 0, 1, .. (the forward) or W-1, W-2, .. (the backward): `in` mapped by those
+// before it.  `in` becomes the value after all of them.
+template <bool CUT, int W, bool REVERSE>
+__device__ __forceinline__ float through_waves(RowMaps<W>& s, int turn, int w, float P, float Q, float& in) {
+  if constexpr (W == 1) {
+    return in;
+  } else {
+    // lane 63 of the prefix holds the wave's total
+    if ((threadIdx.x & 63) == 63) {
+      s.P[turn][w] = P;
+      s.Q[turn][w] = Q;
+    }
+    __syncthreads();
+    float mine = in;
+#pragma unroll
+    for (int j = 0; j < W; ++j) {
+      const int k = REVERSE ? W - 1 - j : j;
+      if (k == w) mine = in;
+      in = apply_map<CUT>(s.P[turn][k], s.Q[turn][k], in);
+    }
+    return mine;
+  }
+}
+
 }  // namespace
 
-template <typename T, int RULE, bool IG, bool ZG>
-__global__ __launch_bounds__(64 * kRowsPerGroup) void gated_fwd_kernel(
+template <typename T, int RULE, bool IG, bool ZG, int W>
+__global__ __launch_bounds__(64 * group_waves(W)) void gated_fwd_kernel(
     const T* __restrict__ x, const T* __restrict__ r, const float* __restrict__ A,
     const float* __restrict__ r_bias, const T* __restrict__ ig, const float* __restrict__ i_bias,
     const T* __restrict__ z, const uint8_t* __restrict__ starts, const float* __restrict__ h0,
     T* __restrict__ y, float* __restrict__ last_state, float* __restrict__ ckpt, const GatedSizes p) {
   const int lane = threadIdx.x & 63;
-  const int row = blockIdx.x * kRowsPerGroup + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  if (row >= p.rows) return;
+  [[maybe_unused]] __shared__ RowMaps<W> maps;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int row = W == 1 ? blockIdx.x * group_waves(W) + wave : blockIdx.x;
+  const int w0 = W == 1 ? 0 : wave;  // this wave's place among the row's
+  if (row >= p.rows) return;         // (with more waves to a row the grid is the rows)
   const int b = row / p.dim, d = row - b * p.dim;
   const float Ad = A[d];
   const float A2 = Ad * kLog2e;
@@ -48,10 +89,12 @@ __global__ __launch_bounds__(64 * kRowsPerGroup) void gated_fwd_kernel(
   const int64_t base = (int64_t)row * p.seqlen;
   float H = h0 != nullptr ? h0[row] : 0.0f;
 
-  for (int blk = 0; blk < p.nblk; ++blk) {
-    const int t0 = blk * kGatedBlock + lane * kRun;
-    const int valid = p.seqlen - t0;  // steps of this lane's run inside the row (may be <= 0)
-    const bool whole = (blk + 1) * kGatedBlock <= p.seqlen;
+  for (int b0 = 0, turn = 0; b0 < p.nblk; b0 += W, turn ^= 1) {
+    const int blk = b0 + w0;  // past the last block: no steps, the identity
+    const int64_t t0 = (int64_t)blk * kGatedBlock + lane * kRun;
+    const int64_t left = p.seqlen - t0;  // steps of this lane's run inside the row (may be <= 0)
+    const int valid = left < kRun ? (int)(left < 0 ? 0 : left) : kRun;
+    const bool whole = (int64_t)(blk + 1) * kGatedBlock <= p.seqlen;
     const int v = whole ? kRun : valid;
     const RunWords<T> wr = load_run(r + base + t0, v), wx = load_run(x + base + t0, v);
     RunWords<T> wi, wz;
@@ -59,7 +102,6 @@ __global__ __launch_bounds__(64 * kRowsPerGroup) void gated_fwd_kernel(
     if constexpr (ZG) wz = load_run(z + base + t0, v);
     uint32_t cut = 0;
     if (starts != nullptr) cut = load_starts(starts + (int64_t)b * p.seqlen + t0, v);
-    if (ckpt != nullptr && lane == 0) ckpt[((int64_t)b * p.nblk + blk) * p.dim + d] = H;
 
     float fr[kRun], fx[kRun], fi[kRun], a[kRun], q[kRun];
     run_floats<T>(wr, fr);
@@ -81,7 +123,7 @@ __global__ __launch_bounds__(64 * kRowsPerGroup) void gated_fwd_kernel(
         S += e2;
       }
     }
-    float P = __builtin_fmaxf(exp2_hw(S), kMinNormal), Q = 0.0f, h;
+    float P = __builtin_fmaxf(exp2_hw(S), kMinNormal), Q = 0.0f, h, h_in;
     if (starts != nullptr) {
 #pragma unroll
       for (int k = 0; k < kRun; ++k) {
@@ -90,21 +132,24 @@ __global__ __launch_bounds__(64 * kRowsPerGroup) void gated_fwd_kernel(
       }
       if (cut != 0) P = 0.0f;
       wave_prefix<true>(P, Q);
-      const float end = apply_map<true>(P, Q, H);
-      h = lane_before(end, H);
-      H = lane_value(end, 63);
+      h_in = through_waves<true, W, false>(maps, turn, w0, P, Q, H);
+      const float end = apply_map<true>(P, Q, h_in);
+      h = lane_before(end, h_in);
+      if constexpr (W == 1) H = lane_value(end, 63);
 #pragma unroll
       for (int k = 0; k < kRun; ++k) q[k] = h = apply_map<true>(a[k], q[k], h);
     } else {
 #pragma unroll
       for (int k = 0; k < kRun; ++k) Q = __builtin_fmaf(a[k], Q, q[k]);
       wave_prefix<false>(P, Q);
-      const float end = __builtin_fmaf(P, H, Q);
-      h = lane_before(end, H);
-      H = lane_value(end, 63);
+      h_in = through_waves<false, W, false>(maps, turn, w0, P, Q, H);
+      const float end = __builtin_fmaf(P, h_in, Q);
+      h = lane_before(end, h_in);
+      if constexpr (W == 1) H = lane_value(end, 63);
 #pragma unroll
       for (int k = 0; k < kRun; ++k) q[k] = h = __builtin_fmaf(a[k], h, q[k]);
     }
+    if (ckpt != nullptr && lane == 0 && blk < p.nblk) ckpt[((int64_t)b * p.nblk + blk) * p.dim + d] = h_in;
     if constexpr (ZG) {
       float fz[kRun];
       run_floats<T>(wz, fz);
@@ -113,11 +158,11 @@ __global__ __launch_bounds__(64 * kRowsPerGroup) void gated_fwd_kernel(
     }
     store_run<T>(y + base + t0, v, q);
   }
-  if (last_state != nullptr && lane == 0) last_state[row] = H;
+  if (last_state != nullptr && lane == 0 && w0 == 0) last_state[row] = H;
 }
 
-template <typename T, int RULE, bool IG, bool ZG>
-__global__ __launch_bounds__(64 * kRowsPerGroup) void gated_bwd_kernel(
+template <typename T, int RULE, bool IG, bool ZG, int W>
+__global__ __launch_bounds__(64 * group_waves(W)) void gated_bwd_kernel(
     const T* __restrict__ x, const T* __restrict__ r, const float* __restrict__ A,
     const float* __restrict__ r_bias, const T* __restrict__ ig, const float* __restrict__ i_bias,
     const T* __restrict__ z, const uint8_t* __restrict__ starts, const float* __restrict__ ckpt,
@@ -125,8 +170,11 @@ __global__ __launch_bounds__(64 * kRowsPerGroup) void gated_bwd_kernel(
     T* __restrict__ di, T* __restrict__ dz, float* __restrict__ row_dA, float* __restrict__ row_drb,
     float* __restrict__ row_dib, float* __restrict__ dh0, const GatedSizes p) {
   const int lane = threadIdx.x & 63;
-  const int row = blockIdx.x * kRowsPerGroup + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  if (row >= p.rows) return;
+  [[maybe_unused]] __shared__ RowMaps<W> maps;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int row = W == 1 ? blockIdx.x * group_waves(W) + wave : blockIdx.x;
+  const int w0 = W == 1 ? 0 : wave;  // this wave's place among the row's
+  if (row >= p.rows) return;         // (with more waves to a row the grid is the rows)
   const int b = row / p.dim, d = row - b * p.dim;
   const float Ad = A[d];
   const float A2 = Ad * kLog2e;
@@ -138,10 +186,12 @@ __global__ __launch_bounds__(64 * kRowsPerGroup) void gated_bwd_kernel(
   // the row's sums, over up to 2^31 steps: in float64 across blocks
   double sA = 0.0, srb = 0.0, sib = 0.0;
 
-  for (int blk = p.nblk - 1; blk >= 0; --blk) {
-    const int t0 = blk * kGatedBlock + lane * kRun;
-    const int valid = p.seqlen - t0;
-    const bool whole = (blk + 1) * kGatedBlock <= p.seqlen;
+  for (int b0 = (p.nblk - 1) / W * W, turn = 0; b0 >= 0; b0 -= W, turn ^= 1) {
+    const int blk = b0 + w0;  // past the last block: no steps, the identity
+    const int64_t t0 = (int64_t)blk * kGatedBlock + lane * kRun;
+    const int64_t left = p.seqlen - t0;
+    const int valid = left < kRun ? (int)(left < 0 ? 0 : left) : kRun;
+    const bool whole = (int64_t)(blk + 1) * kGatedBlock <= p.seqlen;
     const int v = whole ? kRun : valid;
     const RunWords<T> wr = load_run(r + base + t0, v), wx = load_run(x + base + t0, v);
     const RunWords<T> wd = load_run(dy + base + t0, v);
@@ -151,7 +201,7 @@ __global__ __launch_bounds__(64 * kRowsPerGroup) void gated_bwd_kernel(
     const bool packed = starts != nullptr;
     uint32_t cut = 0;
     if (packed) cut = load_starts(starts + (int64_t)b * p.seqlen + t0, v);
-    const float H = ckpt[((int64_t)b * p.nblk + blk) * p.dim + d];
+    const float H = blk < p.nblk ? ckpt[((int64_t)b * p.nblk + blk) * p.dim + d] : 0.0f;
 
     float fr[kRun], fx[kRun], fi[kRun], ad[kRun], w[kRun], q[kRun], gi[kRun], dh[kRun];
     run_floats<T>(wr, fr);
@@ -232,16 +282,18 @@ __global__ __launch_bounds__(64 * kRowsPerGroup) void gated_bwd_kernel(
 #pragma unroll
         for (int k = kRun - 1; k >= 0; --k) Q = ad[k] * (dh[k] + Q);
       }
-      float Pr = lane_mirror(P, lane), Qr = lane_mirror(Q, lane), end;
+      float Pr = lane_mirror(P, lane), Qr = lane_mirror(Q, lane), end, m_in;
       if (packed) {
         wave_prefix<true>(Pr, Qr);
-        end = apply_map<true>(Pr, Qr, M);
+        m_in = through_waves<true, W, true>(maps, turn, w0, Pr, Qr, M);
+        end = apply_map<true>(Pr, Qr, m_in);
       } else {
         wave_prefix<false>(Pr, Qr);
-        end = __builtin_fmaf(Pr, M, Qr);
+        m_in = through_waves<false, W, true>(maps, turn, w0, Pr, Qr, M);
+        end = __builtin_fmaf(Pr, m_in, Qr);
       }
-      m = lane_mirror(lane_before(end, M), lane);
-      M = lane_value(end, 63);
+      m = lane_mirror(lane_before(end, m_in), lane);
+      if constexpr (W == 1) M = lane_value(end, 63);
     }
 
     // the gradients of each step, from the right
@@ -294,7 +346,23 @@ __global__ __launch_bounds__(64 * kRowsPerGroup) void gated_bwd_kernel(
     srb += __shfl_xor(srb, off);
     if constexpr (IG) sib += __shfl_xor(sib, off);
   }
-  if (lane == 0) {
+  if constexpr (W > 1) {
+    __shared__ double s_sum[3][W];
+    if (lane == 0) {
+      s_sum[0][w0] = sA;
+      s_sum[1][w0] = srb;
+      s_sum[2][w0] = sib;
+    }
+    __syncthreads();
+    sA = srb = sib = 0.0;
+#pragma unroll
+    for (int j = 0; j < W; ++j) {
+      sA += s_sum[0][j];
+      srb += s_sum[1][j];
+      sib += s_sum[2][j];
+    }
+  }
+  if (lane == 0 && w0 == 0) {
     row_dA[row] = (float)sA;
     if (row_drb != nullptr) row_drb[row] = (float)srb;
     if (IG && row_dib != nullptr) row_dib[row] = (float)sib;
@@ -359,6 +427,16 @@ hipError_t by_rule(const GatedLaunch& a, F&& f) {
   }
 }
 
+// Waves to a row: one where the rows alone make the 8192 waves that fill the
+// chip, more where they do not and the sequence has blocks for them (batch 1,
+// dim 2048, L 65536 bf16: one 266 us, four 234, sixteen 238; batch 3, dim 1000,
+// L 1777 float32: 23.4, 22.6, 68; batch 8, dim 5120, L 2048, backward: 231, 257).
+int waves_of(const GatedLaunch& a) {
+  const int64_t rows = (int64_t)a.batch * a.dim, nblk = (a.seqlen + kGatedBlock - 1) / kGatedBlock;
+  if (rows >= 8192 || nblk == 1) return 1;
+  return rows >= 2048 || nblk <= 4 ? 4 : 16;
+}
+
 GatedSizes sizes_of(const GatedLaunch& a) {
   return GatedSizes{a.batch * a.dim, a.dim, (int)a.seqlen, (int)((a.seqlen + kGatedBlock - 1) / kGatedBlock)};
 }
@@ -369,9 +447,17 @@ struct FwdLaunch {
   hipStream_t stream;
   template <int RULE, bool IG, bool ZG>
   hipError_t operator()() const {
+    switch (waves_of(a)) {
+      case 1: return launch<RULE, IG, ZG, 1>();
+      case 4: return launch<RULE, IG, ZG, 4>();
+      default: return launch<RULE, IG, ZG, 16>();
+    }
+  }
+  template <int RULE, bool IG, bool ZG, int W>
+  hipError_t launch() const {
     const GatedSizes s = sizes_of(a);
-    const unsigned grid = (unsigned)((s.rows + kRowsPerGroup - 1) / kRowsPerGroup);
-    gated_fwd_kernel<T, RULE, IG, ZG><<<grid, 64 * kRowsPerGroup, 0, stream>>>(
+    const unsigned grid = (unsigned)(W == 1 ? (s.rows + group_waves(W) - 1) / group_waves(W) : s.rows);
+    gated_fwd_kernel<T, RULE, IG, ZG, W><<<grid, 64 * group_waves(W), 0, stream>>>(
         static_cast<const T*>(a.x), static_cast<const T*>(a.r), a.A, a.r_bias, static_cast<const T*>(a.i),
         a.i_bias, static_cast<const T*>(a.z), a.starts, a.h0, static_cast<T*>(a.y), a.last_state, a.ckpt, s);
     return hipGetLastError();
@@ -384,12 +470,20 @@ struct BwdLaunchOf {
   hipStream_t stream;
   template <int RULE, bool IG, bool ZG>
   hipError_t operator()() const {
+    switch (waves_of(a)) {
+      case 1: return launch<RULE, IG, ZG, 1>();
+      case 4: return launch<RULE, IG, ZG, 4>();
+      default: return launch<RULE, IG, ZG, 16>();
+    }
+  }
+  template <int RULE, bool IG, bool ZG, int W>
+  hipError_t launch() const {
     const GatedSizes s = sizes_of(a);
-    const unsigned grid = (unsigned)((s.rows + kRowsPerGroup - 1) / kRowsPerGroup);
+    const unsigned grid = (unsigned)(W == 1 ? (s.rows + group_waves(W) - 1) / group_waves(W) : s.rows);
     // one row per channel: its sums are the results
     const bool direct = a.batch == 1;
     const int64_t plane = (int64_t)a.batch * a.dim;
-    gated_bwd_kernel<T, RULE, IG, ZG><<<grid, 64 * kRowsPerGroup, 0, stream>>>(
+    gated_bwd_kernel<T, RULE, IG, ZG, W><<<grid, 64 * group_waves(W), 0, stream>>>(
         static_cast<const T*>(a.x), static_cast<const T*>(a.r), a.A, a.r_bias, static_cast<const T*>(a.i),
         a.i_bias, static_cast<const T*>(a.z), a.starts, a.ckpt, static_cast<const T*>(a.dy), a.dlast,
         static_cast<T*>(a.dx), static_cast<T*>(a.dr), static_cast<T*>(a.di), static_cast<T*>(a.dz),

@@ -2,8 +2,6 @@
 layer norm (include/ssm_norm.h): marshalling only, as in ops.py."""
 from __future__ import annotations
 
-import contextlib
-
 import torch
 
 from ._lib import SSM_GATE_SOFTPLUS, SSM_GATE_UNIT, SsmError, load
@@ -13,7 +11,7 @@ CKPT_STEPS = 512
 _GATES = {"sigmoid": 0, "softplus": SSM_GATE_SOFTPLUS}
 _WEIGHTS = {"convex": 0, "unit": SSM_GATE_UNIT}
 _INT_MAX = 2**31 - 1
-_HERE = contextlib.nullcontext()
+_F32 = torch.float32
 
 
 def _rule(gate, weight):
@@ -24,11 +22,46 @@ def _rule(gate, weight):
     return _GATES[gate] | _WEIGHTS[weight]
 
 
-def _on(dev):
-    """The context that makes `dev` the current device (launches go there)."""
+# The current stream's handle without making a torch.cuda.Stream of it (0.1
+# against 1.8 us of a single token's 12).
+_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
+def _call(fn, where, dev, *args):
+    """The entry point on the tensors' device and its current stream.  (A
+    launch goes to the current device, so another one is made current for it.)"""
+    if dev.index == torch.cuda.current_device():
+        rc = fn(*args, _stream(dev.index))
+    else:
+        with torch.cuda.device(dev):
+            rc = fn(*args, _stream(dev.index))
+    if rc != 0:
+        raise SsmError(rc, where)
+
+
+def _gpu(x):
+    dev = x.device
     if dev.type != "cuda":
         raise ValueError("libssm runs on the GPU: tensors must be on a cuda device")
-    return _HERE if dev.index == torch.cuda.current_device() else torch.cuda.device(dev)
+    return dev
+
+
+# A token's call is mostly host time, so its tensors are looked at quickly here;
+# what does not fit goes to _check, which says why.
+def _ok(t, shape, dtype, idx):
+    return t.dtype is dtype and t.shape == shape and t.get_device() == idx and t.is_contiguous()
+
+
+def _in(name, t, shape, dtype, dev, required=True):
+    """The address of a tensor that fits, None for None; else _check's error."""
+    if t is None:
+        if required:
+            raise ValueError(f"{name} is required")
+        return None
+    if not _ok(t, shape, dtype, dev.index):
+        _check(name, t, shape, dtype, dev)
+    return t.data_ptr()
 
 
 def _int32(what, n):
@@ -54,6 +87,18 @@ def _check_gates(x, r, A, r_bias, i, i_bias, z, starts, shape, dev):
         _check("starts", starts, shape[:1] + shape[2:], starts.dtype, dev)
 
 
+def _gates_in(x, r, A, r_bias, i, i_bias, z, starts, shape, dev):
+    """_check_gates, and the addresses: (x, r, A, r_bias, i, i_bias, z), starts."""
+    dt, idx, channels = x.dtype, dev.index, (shape[1],)
+    fits = (_ok(x, shape, dt, idx) and _ok(r, shape, dt, idx) and _ok(A, channels, _F32, idx)
+            and (r_bias is None or _ok(r_bias, channels, _F32, idx)) and (i is None or _ok(i, shape, dt, idx))
+            and (i_bias is None or (i is not None and _ok(i_bias, channels, _F32, idx)))
+            and (z is None or _ok(z, shape, dt, idx)) and starts is None) if r is not None and A is not None else False
+    if not fits:
+        _check_gates(x, r, A, r_bias, i, i_bias, z, starts, shape, dev)
+    return (x.data_ptr(), r.data_ptr(), A.data_ptr(), _ptr(r_bias), _ptr(i), _ptr(i_bias), _ptr(z)), _ptr(starts)
+
+
 def _workspace(workspace, need, dev):
     """(workspace tensor or None, its bytes): the caller's, or a new one where it is missing or too small."""
     if need == 0:
@@ -68,7 +113,10 @@ def _workspace(workspace, need, dev):
 def _sizes3(x, name="x"):
     if x.dim() != 3:
         raise ValueError(f"{name} must be (batch, dim, seqlen), not {tuple(x.shape)}")
-    return _int32("batch", x.shape[0]), _int32("dim", x.shape[1]), x.shape[2]
+    shape = tuple(x.shape)
+    _int32("batch", shape[0])
+    _int32("dim", shape[1])
+    return shape
 
 
 def ssm_gated_scan_fwd_workspace_bytes(batch: int, dim: int, seqlen: int, dtype: torch.dtype) -> int:
@@ -97,27 +145,19 @@ def ssm_gated_scan_fwd(x, r, A, r_bias=None, i=None, i_bias=None, z=None, *, gat
     return_last_state), then what ssm_gated_scan_bwd starts from (if
     return_ckpt): (batch, ceil(L/512), dim) float32."""
     lib = load()
-    dev = x.device
-    here = _on(dev)
+    dev = _gpu(x)
     code = _code(x)
-    batch, dim, L = _sizes3(x)
+    batch, dim, L = shape = _sizes3(x)
     flags = _rule(gate, weight)
-    _check_gates(x, r, A, r_bias, i, i_bias, z, starts, (batch, dim, L), dev)
-    _check("h0", h0, (batch, dim), torch.float32, dev, required=False)
+    ins, ps = _gates_in(x, r, A, r_bias, i, i_bias, z, starts, shape, dev)
+    p0 = _in("h0", h0, (batch, dim), _F32, dev, required=False)
     y = out if out is not None else torch.empty_like(x)
-    _check("out", y, (batch, dim, L), x.dtype, dev)
-    last = torch.empty((batch, dim), dtype=torch.float32, device=dev) if return_last_state else None
-    ckpt = None
-    if return_ckpt:
-        ckpt = torch.empty((batch, -(-L // CKPT_STEPS), dim), dtype=torch.float32, device=dev)
-    workspace, ws_bytes = _workspace(workspace, int(lib.ssm_gated_scan_fwd_workspace_bytes(batch, dim, L, code)), dev)
-    with here:
-        rc = lib.ssm_gated_scan_fwd(
-            _ptr(x), _ptr(r), _ptr(A), _ptr(r_bias), _ptr(i), _ptr(i_bias), _ptr(z), flags, _ptr(starts),
-            _ptr(h0), _ptr(y), _ptr(last), _ptr(ckpt), ckpt.numel() * 4 if return_ckpt else 0, batch, dim, L,
-            code, _ptr(workspace), ws_bytes, torch.cuda.current_stream(dev).cuda_stream)
-    if rc != 0:
-        raise SsmError(rc, "ssm_gated_scan_fwd")
+    py = _in("out", y, shape, x.dtype, dev)
+    last = torch.empty((batch, dim), dtype=_F32, device=dev) if return_last_state else None
+    ckpt = torch.empty((batch, -(-L // CKPT_STEPS), dim), dtype=_F32, device=dev) if return_ckpt else None
+    workspace, ws_bytes = _workspace(workspace, lib.ssm_gated_scan_fwd_workspace_bytes(batch, dim, L, code), dev)
+    _call(lib.ssm_gated_scan_fwd, "ssm_gated_scan_fwd", dev, *ins, flags, ps, p0, py, _ptr(last), _ptr(ckpt),
+          ckpt.numel() * 4 if return_ckpt else 0, batch, dim, L, code, _ptr(workspace), ws_bytes)
     res = (y,)
     if return_last_state:
         res += (last,)
@@ -134,30 +174,23 @@ def ssm_gated_scan_bwd(x, r, A, r_bias=None, i=None, i_bias=None, z=None, *, gat
     dz (None without z) in the input dtype; dA, dr_bias, di_bias (None without
     i), dh0 in float32."""
     lib = load()
-    dev = x.device
-    here = _on(dev)
+    dev = _gpu(x)
     code = _code(x)
-    batch, dim, L = _sizes3(x)
+    batch, dim, L = shape = _sizes3(x)
     flags = _rule(gate, weight)
-    _check_gates(x, r, A, r_bias, i, i_bias, z, starts, (batch, dim, L), dev)
-    _check("ckpt", ckpt, (batch, -(-L // CKPT_STEPS), dim), torch.float32, dev)
-    _check("dy", dy, (batch, dim, L), x.dtype, dev)
-    _check("dlast_state", dlast_state, (batch, dim), torch.float32, dev, required=False)
-    f32 = dict(dtype=torch.float32, device=dev)
+    ins, ps = _gates_in(x, r, A, r_bias, i, i_bias, z, starts, shape, dev)
+    pc = _in("ckpt", ckpt, (batch, -(-L // CKPT_STEPS), dim), _F32, dev)
+    pdy = _in("dy", dy, shape, x.dtype, dev)
+    pdl = _in("dlast_state", dlast_state, (batch, dim), _F32, dev, required=False)
+    f32 = dict(dtype=_F32, device=dev)
     g = dict(dx=torch.empty_like(x), dr=torch.empty_like(x), dA=torch.empty(dim, **f32),
              dr_bias=torch.empty(dim, **f32), di=torch.empty_like(x) if i is not None else None,
              di_bias=torch.empty(dim, **f32) if i is not None else None,
              dz=torch.empty_like(x) if z is not None else None, dh0=torch.empty((batch, dim), **f32))
-    workspace, ws_bytes = _workspace(workspace, int(lib.ssm_gated_scan_bwd_workspace_bytes(batch, dim, L, code)), dev)
-    with here:
-        rc = lib.ssm_gated_scan_bwd(
-            _ptr(x), _ptr(r), _ptr(A), _ptr(r_bias), _ptr(i), _ptr(i_bias), _ptr(z), flags, _ptr(starts),
-            _ptr(ckpt), ckpt.numel() * 4, _ptr(dy), _ptr(dlast_state), _ptr(g["dx"]), _ptr(g["dr"]),
-            _ptr(g["dA"]), _ptr(g["dr_bias"]), _ptr(g["di"]), _ptr(g["di_bias"]), _ptr(g["dz"]),
-            _ptr(g["dh0"]), batch, dim, L, code, _ptr(workspace), ws_bytes,
-            torch.cuda.current_stream(dev).cuda_stream)
-    if rc != 0:
-        raise SsmError(rc, "ssm_gated_scan_bwd")
+    workspace, ws_bytes = _workspace(workspace, lib.ssm_gated_scan_bwd_workspace_bytes(batch, dim, L, code), dev)
+    _call(lib.ssm_gated_scan_bwd, "ssm_gated_scan_bwd", dev, *ins, flags, ps, pc, ckpt.numel() * 4, pdy, pdl,
+          _ptr(g["dx"]), _ptr(g["dr"]), _ptr(g["dA"]), _ptr(g["dr_bias"]), _ptr(g["di"]), _ptr(g["di_bias"]),
+          _ptr(g["dz"]), _ptr(g["dh0"]), batch, dim, L, code, _ptr(workspace), ws_bytes)
     return g
 
 
@@ -168,25 +201,20 @@ def ssm_gated_state_update(state, x, r, A, r_bias=None, i=None, i_bias=None, z=N
     (batch, dim); starts: (batch,), set where the token is its sequence's
     first.  Returns y (batch, dim)."""
     lib = load()
-    dev = x.device
-    here = _on(dev)
+    dev = _gpu(x)
     code = _code(x)
     if x.dim() != 2:
         raise ValueError(f"x must be (batch, dim), not {tuple(x.shape)}")
-    batch, dim = shape = _int32("batch", x.shape[0]), _int32("dim", x.shape[1])
+    batch, dim = shape = x.shape
+    _int32("batch", batch)
+    _int32("dim", dim)
     flags = _rule(gate, weight)
-    _check("state", state, shape, torch.float32, dev)
-    _check_gates(x, r, A, r_bias, i, i_bias, z, starts, shape, dev)
+    p0 = _in("state", state, shape, _F32, dev)
+    ins, ps = _gates_in(x, r, A, r_bias, i, i_bias, z, starts, shape, dev)
     y = out if out is not None else torch.empty_like(x)
-    _check("out", y, shape, x.dtype, dev)
-    _check("state_out", state_out, shape, torch.float32, dev, required=False)
-    with here:
-        rc = lib.ssm_gated_state_update(
-            _ptr(state), _ptr(x), _ptr(r), _ptr(A), _ptr(r_bias), _ptr(i), _ptr(i_bias), _ptr(z), flags,
-            _ptr(starts), _ptr(y), _ptr(state_out), batch, dim, code,
-            torch.cuda.current_stream(dev).cuda_stream)
-    if rc != 0:
-        raise SsmError(rc, "ssm_gated_state_update")
+    py = y.data_ptr() if out is None else _in("out", y, shape, x.dtype, dev)
+    _call(lib.ssm_gated_state_update, "ssm_gated_state_update", dev, p0, *ins, flags, ps, py,
+          _in("state_out", state_out, shape, _F32, dev, required=False), batch, dim, code)
     return y
 
 
@@ -222,27 +250,23 @@ def ssm_layer_norm_fwd(x, weight, bias=None, residual=None, *, eps=1e-5, axis=-1
     residual the sum x + residual (what the norm was taken of), then mean and
     rstd (if return_stats), float32 in x's shape without the axis."""
     lib = load()
-    dev = x.device
-    here = _on(dev)
+    dev = _gpu(x)
     code = _code(x)
     batch, dim, L, stats = _norm_sizes(x, axis)
-    _check("x", x, x.shape, x.dtype, dev)
-    _check("residual", residual, x.shape, x.dtype, dev, required=False)
-    _check("weight", weight, (dim,), torch.float32, dev)
-    _check("bias", bias, (dim,), torch.float32, dev, required=False)
+    shape, dt = x.shape, x.dtype
+    px = _in("x", x, shape, dt, dev)
+    pr = _in("residual", residual, shape, dt, dev, required=False)
+    pw = _in("weight", weight, (dim,), _F32, dev)
+    pb = _in("bias", bias, (dim,), _F32, dev, required=False)
     y = out if out is not None else torch.empty_like(x)
-    _check("out", y, x.shape, x.dtype, dev)
+    py = y.data_ptr() if out is None else _in("out", y, shape, dt, dev)
     total = torch.empty_like(x) if residual is not None else None
     mean = rstd = None
     if return_stats:
-        mean = torch.empty(stats, dtype=torch.float32, device=dev)
-        rstd = torch.empty(stats, dtype=torch.float32, device=dev)
-    with here:
-        rc = lib.ssm_layer_norm_fwd(_ptr(x), _ptr(residual), _ptr(weight), _ptr(bias), eps, _ptr(y),
-                                    _ptr(total), _ptr(mean), _ptr(rstd), batch, dim, L, code,
-                                    torch.cuda.current_stream(dev).cuda_stream)
-    if rc != 0:
-        raise SsmError(rc, "ssm_layer_norm_fwd")
+        mean = torch.empty(stats, dtype=_F32, device=dev)
+        rstd = torch.empty(stats, dtype=_F32, device=dev)
+    _call(lib.ssm_layer_norm_fwd, "ssm_layer_norm_fwd", dev, px, pr, pw, pb, eps, py, _ptr(total), _ptr(mean),
+          _ptr(rstd), batch, dim, L, code)
     res = (y,)
     if residual is not None:
         res += (total,)
@@ -257,23 +281,19 @@ def ssm_layer_norm_bwd(x, weight, mean, rstd, dy, dsum=None, *, axis=-1, workspa
     pass returned, dsum the gradient arriving at the sum by its other way.
     Returns a dict: dx (of x and of the residual alike), dweight, dbias."""
     lib = load()
-    dev = x.device
-    here = _on(dev)
+    dev = _gpu(x)
     code = _code(x)
     batch, dim, L, stats = _norm_sizes(x, axis)
-    _check("x", x, x.shape, x.dtype, dev)
-    _check("weight", weight, (dim,), torch.float32, dev)
-    _check("mean", mean, stats, torch.float32, dev)
-    _check("rstd", rstd, stats, torch.float32, dev)
-    _check("dy", dy, x.shape, x.dtype, dev)
-    _check("dsum", dsum, x.shape, x.dtype, dev, required=False)
-    f32 = dict(dtype=torch.float32, device=dev)
-    g = dict(dx=torch.empty_like(x), dweight=torch.empty(dim, **f32), dbias=torch.empty(dim, **f32))
-    workspace, ws_bytes = _workspace(workspace, int(lib.ssm_layer_norm_bwd_workspace_bytes(batch, dim, L, code)), dev)
-    with here:
-        rc = lib.ssm_layer_norm_bwd(_ptr(x), _ptr(weight), _ptr(mean), _ptr(rstd), _ptr(dy), _ptr(dsum),
-                                    _ptr(g["dx"]), _ptr(g["dweight"]), _ptr(g["dbias"]), batch, dim, L, code,
-                                    _ptr(workspace), ws_bytes, torch.cuda.current_stream(dev).cuda_stream)
-    if rc != 0:
-        raise SsmError(rc, "ssm_layer_norm_bwd")
+    shape, dt = x.shape, x.dtype
+    px = _in("x", x, shape, dt, dev)
+    pw = _in("weight", weight, (dim,), _F32, dev)
+    pm = _in("mean", mean, stats, _F32, dev)
+    prs = _in("rstd", rstd, stats, _F32, dev)
+    pdy = _in("dy", dy, shape, dt, dev)
+    pds = _in("dsum", dsum, shape, dt, dev, required=False)
+    g = dict(dx=torch.empty_like(x), dweight=torch.empty(dim, dtype=_F32, device=dev),
+             dbias=torch.empty(dim, dtype=_F32, device=dev))
+    workspace, ws_bytes = _workspace(workspace, lib.ssm_layer_norm_bwd_workspace_bytes(batch, dim, L, code), dev)
+    _call(lib.ssm_layer_norm_bwd, "ssm_layer_norm_bwd", dev, px, pw, pm, prs, pdy, pds, _ptr(g["dx"]),
+          _ptr(g["dweight"]), _ptr(g["dbias"]), batch, dim, L, code, _ptr(workspace), ws_bytes)
     return g
