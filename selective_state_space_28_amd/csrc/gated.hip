@@ -68,40 +68,45 @@ __device__ __forceinline__ float through_waves(RowMaps<W>& s, int turn, int w, f
 
 }  // namespace
 
+// g of a step from its raw r: nb = -r_bias log2(e).
+template <int RULE>
+__device__ __forceinline__ float gate_value(float r, float rb, float nb) {
+  if constexpr ((RULE & kGateSoftplus) != 0) return softplus_f32(r + rb);
+  else return sigmoid_f32(r, nb);
+}
+
 template <typename T, int RULE, bool IG, bool ZG, int W>
 __global__ __launch_bounds__(64 * group_waves(W)) void gated_fwd_kernel(
     const T* __restrict__ x, const T* __restrict__ r, const float* __restrict__ A,
     const float* __restrict__ r_bias, const T* __restrict__ ig, const float* __restrict__ i_bias,
     const T* __restrict__ z, const uint8_t* __restrict__ starts, const float* __restrict__ h0,
     T* __restrict__ y, float* __restrict__ last_state, float* __restrict__ ckpt, const GatedSizes p) {
-  const int lane = threadIdx.x & 63;
   [[maybe_unused]] __shared__ RowMaps<W> maps;
+  const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int row = W == 1 ? blockIdx.x * group_waves(W) + wave : blockIdx.x;
   const int w0 = W == 1 ? 0 : wave;  // this wave's place among the row's
   if (row >= p.rows) return;         // (with more waves to a row the grid is the rows)
   const int b = row / p.dim, d = row - b * p.dim;
-  const float Ad = A[d];
-  const float A2 = Ad * kLog2e;
-  const float An = (RULE & kGateUnit) != 0 ? 2.0f * Ad : Ad;
-  const float rb = r_bias != nullptr ? r_bias[d] : 0.0f;
-  const float ib = IG && i_bias != nullptr ? i_bias[d] : 0.0f;
+  const float A2 = A[d] * kLog2e;
+  const float rb = r_bias != nullptr ? r_bias[d] : 0.0f, nrb = -rb * kLog2e;
+  const float nib = IG && i_bias != nullptr ? -i_bias[d] * kLog2e : 0.0f;
   const int64_t base = (int64_t)row * p.seqlen;
   float H = h0 != nullptr ? h0[row] : 0.0f;
 
-  for (int b0 = 0, turn = 0; b0 < p.nblk; b0 += W, turn ^= 1) {
+  // one block a wave; WHOLE: every step of the W blocks is in the row
+  auto blocks = [&](int b0, int turn, auto whole) {
+    constexpr bool WHOLE = decltype(whole)::value;
     const int blk = b0 + w0;  // past the last block: no steps, the identity
     const int64_t t0 = (int64_t)blk * kGatedBlock + lane * kRun;
-    const int64_t left = p.seqlen - t0;  // steps of this lane's run inside the row (may be <= 0)
-    const int valid = left < kRun ? (int)(left < 0 ? 0 : left) : kRun;
-    const bool whole = (int64_t)(blk + 1) * kGatedBlock <= p.seqlen;
-    const int v = whole ? kRun : valid;
-    const RunWords<T> wr = load_run(r + base + t0, v), wx = load_run(x + base + t0, v);
+    const int64_t left = p.seqlen - t0;
+    const int valid = WHOLE || left > kRun ? kRun : (int)(left < 0 ? 0 : left);  // steps of this lane's run
+    const RunWords<T> wr = load_run(r + base + t0, valid), wx = load_run(x + base + t0, valid);
     RunWords<T> wi, wz;
-    if constexpr (IG) wi = load_run(ig + base + t0, v);
-    if constexpr (ZG) wz = load_run(z + base + t0, v);
+    if constexpr (IG) wi = load_run(ig + base + t0, valid);
+    if constexpr (ZG) wz = load_run(z + base + t0, valid);
     uint32_t cut = 0;
-    if (starts != nullptr) cut = load_starts(starts + (int64_t)b * p.seqlen + t0, v);
+    if (starts != nullptr) cut = load_starts(starts + (int64_t)b * p.seqlen + t0, valid);
 
     float fr[kRun], fx[kRun], fi[kRun], a[kRun], q[kRun];
     run_floats<T>(wr, fr);
@@ -110,17 +115,15 @@ __global__ __launch_bounds__(64 * group_waves(W)) void gated_fwd_kernel(
     float S = 0.0f;  // exponent of the run's decay
 #pragma unroll
     for (int k = 0; k < kRun; ++k) {
-      const float pre = fr[k] + rb;
-      const float g = (RULE & kGateSoftplus) != 0 ? softplus_f32(pre) : sigmoid_f32(pre);
-      const float e2 = A2 * g;
-      a[k] = decay_of(e2);
-      q[k] = weight_of<RULE>(a[k], An, g) * fx[k];
-      if constexpr (IG) q[k] *= sigmoid_f32(fi[k] + ib);
-      if (!whole && k >= valid) {  // past the end: the identity
+      const Gate g = gate_of<RULE>(gate_value<RULE>(fr[k], rb, nrb), A2);
+      a[k] = g.a;
+      q[k] = g.w * fx[k];
+      if constexpr (IG) q[k] *= sigmoid_f32(fi[k], nib);
+      if (!WHOLE && k >= valid) {
         a[k] = 1.0f;
         q[k] = 0.0f;
       } else {
-        S += e2;
+        S += g.e2;
       }
     }
     float P = __builtin_fmaxf(exp2_hw(S), kMinNormal), Q = 0.0f, h, h_in;
@@ -156,8 +159,11 @@ __global__ __launch_bounds__(64 * group_waves(W)) void gated_fwd_kernel(
 #pragma unroll
       for (int k = 0; k < kRun; ++k) q[k] *= silu_f32(fz[k]);
     }
-    store_run<T>(y + base + t0, v, q);
-  }
+    store_run<T>(y + base + t0, valid, q);
+  };
+  int b0 = 0, turn = 0;
+  for (; (int64_t)(b0 + W) * kGatedBlock <= p.seqlen; b0 += W, turn ^= 1) blocks(b0, turn, BoolC<true>{});
+  if (b0 < p.nblk) blocks(b0, turn, BoolC<false>{});
   if (last_state != nullptr && lane == 0 && w0 == 0) last_state[row] = H;
 }
 
@@ -169,63 +175,71 @@ __global__ __launch_bounds__(64 * group_waves(W)) void gated_bwd_kernel(
     const T* __restrict__ dy, const float* __restrict__ dlast, T* __restrict__ dx, T* __restrict__ dr,
     T* __restrict__ di, T* __restrict__ dz, float* __restrict__ row_dA, float* __restrict__ row_drb,
     float* __restrict__ row_dib, float* __restrict__ dh0, const GatedSizes p) {
-  const int lane = threadIdx.x & 63;
   [[maybe_unused]] __shared__ RowMaps<W> maps;
+  const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int row = W == 1 ? blockIdx.x * group_waves(W) + wave : blockIdx.x;
   const int w0 = W == 1 ? 0 : wave;  // this wave's place among the row's
   if (row >= p.rows) return;         // (with more waves to a row the grid is the rows)
   const int b = row / p.dim, d = row - b * p.dim;
-  const float Ad = A[d];
-  const float A2 = Ad * kLog2e;
-  const float An = (RULE & kGateUnit) != 0 ? 2.0f * Ad : Ad;
-  const float rb = r_bias != nullptr ? r_bias[d] : 0.0f;
-  const float ib = IG && i_bias != nullptr ? i_bias[d] : 0.0f;
+  const float Ad = A[d], A2 = Ad * kLog2e;
+  const float rb = r_bias != nullptr ? r_bias[d] : 0.0f, nrb = -rb * kLog2e;
+  const float nib = IG && i_bias != nullptr ? -i_bias[d] * kLog2e : 0.0f;
   const int64_t base = (int64_t)row * p.seqlen;
   float M = dlast != nullptr ? dlast[row] : 0.0f;  // a_{t+1} lambda_{t+1} entering from the right
   // the row's sums, over up to 2^31 steps: in float64 across blocks
   double sA = 0.0, srb = 0.0, sib = 0.0;
 
-  for (int b0 = (p.nblk - 1) / W * W, turn = 0; b0 >= 0; b0 -= W, turn ^= 1) {
+  auto blocks = [&](int b0, int turn, auto whole) {
+    constexpr bool WHOLE = decltype(whole)::value;
     const int blk = b0 + w0;  // past the last block: no steps, the identity
     const int64_t t0 = (int64_t)blk * kGatedBlock + lane * kRun;
     const int64_t left = p.seqlen - t0;
-    const int valid = left < kRun ? (int)(left < 0 ? 0 : left) : kRun;
-    const bool whole = (int64_t)(blk + 1) * kGatedBlock <= p.seqlen;
-    const int v = whole ? kRun : valid;
-    const RunWords<T> wr = load_run(r + base + t0, v), wx = load_run(x + base + t0, v);
-    const RunWords<T> wd = load_run(dy + base + t0, v);
+    const int valid = WHOLE || left > kRun ? kRun : (int)(left < 0 ? 0 : left);
+    const RunWords<T> wr = load_run(r + base + t0, valid), wx = load_run(x + base + t0, valid);
     RunWords<T> wi, wz;
-    if constexpr (IG) wi = load_run(ig + base + t0, v);
-    if constexpr (ZG) wz = load_run(z + base + t0, v);
+    if constexpr (IG) wi = load_run(ig + base + t0, valid);
+    if constexpr (ZG) wz = load_run(z + base + t0, valid);
+    const RunWords<T> wd = load_run(dy + base + t0, valid);
     const bool packed = starts != nullptr;
     uint32_t cut = 0;
-    if (packed) cut = load_starts(starts + (int64_t)b * p.seqlen + t0, v);
-    const float H = blk < p.nblk ? ckpt[((int64_t)b * p.nblk + blk) * p.dim + d] : 0.0f;
+    if (packed) cut = load_starts(starts + (int64_t)b * p.seqlen + t0, valid);
+    const float H = WHOLE || blk < p.nblk ? ckpt[((int64_t)b * p.nblk + blk) * p.dim + d] : 0.0f;
 
-    float fr[kRun], fx[kRun], fi[kRun], ad[kRun], w[kRun], q[kRun], gi[kRun], dh[kRun];
-    run_floats<T>(wr, fr);
+    // g of each step, A dg/dr, the input gate and its complement
+    float g[kRun], sA_[kRun], fx[kRun], gi[kRun], ci[kRun], a[kRun], w[kRun], q[kRun], dh[kRun];
+    run_floats<T>(wr, g);
     run_floats<T>(wx, fx);
     run_floats<T>(wd, dh);
-    if constexpr (IG) run_floats<T>(wi, fi);
+    if constexpr (IG) run_floats<T>(wi, gi);
     float S = 0.0f;
 #pragma unroll
     for (int k = 0; k < kRun; ++k) {
-      const float pre = fr[k] + rb;
-      const float g = (RULE & kGateSoftplus) != 0 ? softplus_f32(pre) : sigmoid_f32(pre);
-      const float e2 = A2 * g;
-      ad[k] = decay_of(e2);
-      w[k] = weight_of<RULE>(ad[k], An, g);
-      q[k] = w[k] * fx[k];
+      float v, slope;
+      if constexpr ((RULE & kGateSoftplus) != 0) {
+        softplus_pair(g[k] + rb, v, slope);
+      } else {
+        float c;
+        sigmoid_pair(g[k], nrb, v, c);
+        slope = v * c;
+      }
+      const Gate t = gate_of<RULE>(v, A2);
+      g[k] = v;
+      sA_[k] = slope * Ad;
+      a[k] = t.a;
+      w[k] = t.w;
+      q[k] = t.w * fx[k];
       if constexpr (IG) {
-        gi[k] = sigmoid_f32(fi[k] + ib);
+        sigmoid_pair(gi[k], nib, gi[k], ci[k]);
         q[k] *= gi[k];
       }
-      if (!whole && k >= valid) {
-        ad[k] = 1.0f;
+      if (!WHOLE && k >= valid) {
+        a[k] = 1.0f;
         q[k] = 0.0f;
+        g[k] = 0.0f;   // nothing is added to dA,
+        sA_[k] = 0.0f;  // nor to dr_bias (x and so di are 0 already)
       } else {
-        S += e2;
+        S += t.e2;
       }
     }
     const float P = cut != 0 ? 0.0f : __builtin_fmaxf(exp2_hw(S), kMinNormal);
@@ -236,23 +250,23 @@ __global__ __launch_bounds__(64 * group_waves(W)) void gated_bwd_kernel(
       float Pf = P, Q = 0.0f, h;
       if (packed) {
 #pragma unroll
-        for (int k = 0; k < kRun; ++k) Q = apply_map<true>((cut & (1u << k)) ? 0.0f : ad[k], q[k], Q);
+        for (int k = 0; k < kRun; ++k) Q = apply_map<true>((cut & (1u << k)) ? 0.0f : a[k], q[k], Q);
         wave_prefix<true>(Pf, Q);
         h = lane_before(apply_map<true>(Pf, Q, H), H);
 #pragma unroll
         for (int k = 0; k < kRun; ++k) {
           hb[k] = (cut & (1u << k)) ? 0.0f : h;
-          q[k] = h = __builtin_fmaf(ad[k], hb[k], q[k]);
+          q[k] = h = __builtin_fmaf(a[k], hb[k], q[k]);
         }
       } else {
 #pragma unroll
-        for (int k = 0; k < kRun; ++k) Q = __builtin_fmaf(ad[k], Q, q[k]);
+        for (int k = 0; k < kRun; ++k) Q = __builtin_fmaf(a[k], Q, q[k]);
         wave_prefix<false>(Pf, Q);
         h = lane_before(__builtin_fmaf(Pf, H, Q), H);
 #pragma unroll
         for (int k = 0; k < kRun; ++k) {
           hb[k] = h;
-          q[k] = h = __builtin_fmaf(ad[k], h, q[k]);
+          q[k] = h = __builtin_fmaf(a[k], h, q[k]);
         }
       }
     }
@@ -264,23 +278,24 @@ __global__ __launch_bounds__(64 * group_waves(W)) void gated_bwd_kernel(
 #pragma unroll
       for (int k = 0; k < kRun; ++k) {
         float s, c;
-        sigmoid_pair(fz[k], s, c);
-        o[k] = dh[k] * q[k] * (s * __builtin_fmaf(fz[k], c, 1.0f));
-        dh[k] *= fz[k] * s;
+        sigmoid_pair(fz[k], 0.0f, s, c);
+        const float ds = dh[k] * s;
+        o[k] = ds * q[k] * __builtin_fmaf(fz[k], c, 1.0f);
+        dh[k] = ds * fz[k];
       }
-      store_run<T>(dz + base + t0, v, o);
+      store_run<T>(dz + base + t0, valid, o);
     }
 
     // the adjoint entering the run from the right
-    float m = 0.0f;
+    float m;
     {
       float Q = 0.0f;
       if (packed) {
 #pragma unroll
-        for (int k = kRun - 1; k >= 0; --k) Q = (cut & (1u << k)) ? 0.0f : ad[k] * (dh[k] + Q);
+        for (int k = kRun - 1; k >= 0; --k) Q = (cut & (1u << k)) ? 0.0f : a[k] * (dh[k] + Q);
       } else {
 #pragma unroll
-        for (int k = kRun - 1; k >= 0; --k) Q = ad[k] * (dh[k] + Q);
+        for (int k = kRun - 1; k >= 0; --k) Q = a[k] * (dh[k] + Q);
       }
       float Pr = lane_mirror(P, lane), Qr = lane_mirror(Q, lane), end, m_in;
       if (packed) {
@@ -296,49 +311,44 @@ __global__ __launch_bounds__(64 * group_waves(W)) void gated_bwd_kernel(
       if constexpr (W == 1) M = lane_value(end, 63);
     }
 
-    // the gradients of each step, from the right
+    // the gradients of each step, from the right; with u = x sigmoid(i)
+    // de = lambda (a h_before - u (a or a^2/w)), the bracket's second term from
+    // dw/de = -a, or -a^2/w (0 where w is 0)
     float odx[kRun], odr[kRun], odi[kRun];
     float pA = 0.0f, prb = 0.0f, pib = 0.0f;
 #pragma unroll
     for (int k = kRun - 1; k >= 0; --k) {
       const float lam = dh[k] + m;
-      m = ad[k] * lam;
+      m = a[k] * lam;
       if (packed && (cut & (1u << k))) m = 0.0f;
-      const float pre = fr[k] + rb;
-      float g, slope, s, c;
-      sigmoid_pair(pre, s, c);
-      if constexpr ((RULE & kGateSoftplus) != 0) {
-        g = softplus_f32(pre);
-        slope = s;
-      } else {
-        g = s;
-        slope = s * c;
-      }
       const float u = IG ? fx[k] * gi[k] : fx[k];
-      const float lw = lam * w[k];
-      odx[k] = IG ? lw * gi[k] : lw;
-      // dw/de: -a, or -a^2 / w (0 where w is 0)
-      float bend = ad[k];
-      if constexpr ((RULE & kGateUnit) != 0) bend = w[k] > 0.0f ? ad[k] * ad[k] * rcp_hw(w[k]) : 0.0f;
-      float de = lam * (ad[k] * hb[k] - u * bend);
-      if (!whole && k >= valid) de = 0.0f;
-      odr[k] = de * Ad * slope;
-      pA = __builtin_fmaf(de, g, pA);
+      float bend = a[k] * u;
+      if constexpr ((RULE & kGateUnit) != 0) bend = w[k] > 0.0f ? bend * a[k] * rcp_hw(w[k]) : 0.0f;
+      const float de = lam * __builtin_fmaf(a[k], hb[k], -bend);
+      odr[k] = de * sA_[k];
+      pA = __builtin_fmaf(de, g[k], pA);
       prb += odr[k];
+      odx[k] = lam * w[k];
       if constexpr (IG) {
-        float sg, cg;
-        sigmoid_pair(fi[k] + ib, sg, cg);
-        odi[k] = lw * fx[k] * sg * cg;
+        odx[k] *= gi[k];
+        odi[k] = odx[k] * fx[k] * ci[k];
         pib += odi[k];
       }
     }
-    store_run<T>(dx + base + t0, v, odx);
-    store_run<T>(dr + base + t0, v, odr);
-    if constexpr (IG) store_run<T>(di + base + t0, v, odi);
+    store_run<T>(dx + base + t0, valid, odx);
+    store_run<T>(dr + base + t0, valid, odr);
+    if constexpr (IG) store_run<T>(di + base + t0, valid, odi);
     sA += (double)pA;
     srb += (double)prb;
     if constexpr (IG) sib += (double)pib;
+  };
+  int b0 = (p.nblk - 1) / W * W, turn = 0;
+  if ((int64_t)(b0 + W) * kGatedBlock > p.seqlen) {
+    blocks(b0, turn, BoolC<false>{});
+    b0 -= W;
+    turn ^= 1;
   }
+  for (; b0 >= 0; b0 -= W, turn ^= 1) blocks(b0, turn, BoolC<true>{});
 
 #pragma unroll
   for (int off = 1; off < 64; off <<= 1) {
@@ -395,13 +405,11 @@ __global__ __launch_bounds__(256) void gated_step_kernel(
   if (d >= dim) return;
   const int b = b0 + (int)blockIdx.y;
   const int64_t at = (int64_t)b * dim + d;
-  const float Ad = A[d];
-  const float pre = Elem<T>::load(r + at) + (r_bias != nullptr ? r_bias[d] : 0.0f);
-  const float g = (RULE & kGateSoftplus) != 0 ? softplus_f32(pre) : sigmoid_f32(pre);
-  const float a = decay_of(Ad * kLog2e * g);
-  float h = weight_of<RULE>(a, (RULE & kGateUnit) != 0 ? 2.0f * Ad : Ad, g) * Elem<T>::load(x + at);
-  if constexpr (IG) h *= sigmoid_f32(Elem<T>::load(ig + at) + (i_bias != nullptr ? i_bias[d] : 0.0f));
-  if (starts == nullptr || starts[b] == 0) h = __builtin_fmaf(a, state[at], h);
+  const float rb = r_bias != nullptr ? r_bias[d] : 0.0f;
+  const Gate g = gate_of<RULE>(gate_value<RULE>(Elem<T>::load(r + at), rb, -rb * kLog2e), A[d] * kLog2e);
+  float h = g.w * Elem<T>::load(x + at);
+  if constexpr (IG) h *= sigmoid_f32(Elem<T>::load(ig + at), i_bias != nullptr ? -i_bias[d] * kLog2e : 0.0f);
+  if (starts == nullptr || starts[b] == 0) h = __builtin_fmaf(g.a, state[at], h);
   state_out[at] = h;
   if constexpr (ZG) h *= silu_f32(Elem<T>::load(z + at));
   Elem<T>::store(y + at, h);

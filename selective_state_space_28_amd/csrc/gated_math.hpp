@@ -10,47 +10,63 @@ namespace ssm {
 constexpr int kGateSoftplus = 1;
 constexpr int kGateUnit = 2;
 
-// sigmoid(x) = 1/(1 + e^-x): 0 at -inf, where e^-x is infinite.
-__device__ __forceinline__ float sigmoid_f32(float x) { return rcp_hw(1.0f + exp2_hw(-x * kLog2e)); }
+// sigmoid(x + bias) = 1/(1 + e^-(x + bias)), with nb = -bias log2(e): 0 at -inf,
+// where the exponential is infinite.
+__device__ __forceinline__ float sigmoid_f32(float x, float nb) {
+  return rcp_hw(1.0f + exp2_hw(__builtin_fmaf(x, -kLog2e, nb)));
+}
 
-// sigmoid(x) and 1 - sigmoid(x) = e^-x sigmoid(x), the latter without
-// cancellation.  Where e^-x is infinite the product 0 * inf is NaN and the
-// minimum returns its other operand, 1.
-__device__ __forceinline__ void sigmoid_pair(float x, float& s, float& c) {
-  const float t = exp2_hw(-x * kLog2e);
+// The same and its complement e^-x sigmoid(x), the latter without cancellation.
+// Where e^-x is infinite the product 0 * inf is NaN and the minimum returns its
+// other operand, 1.
+__device__ __forceinline__ void sigmoid_pair(float x, float nb, float& s, float& c) {
+  const float t = exp2_hw(__builtin_fmaf(x, -kLog2e, nb));
   s = rcp_hw(1.0f + t);
   c = __builtin_fminf(t * s, 1.0f);
 }
 
-// 1 - e^t for t <= 0 (any t works): where |t| < 1/4 the difference would
-// magnify the rounding of e^t, so the Taylor series -t (1 + t/2 + ... +
-// t^5/720) is taken (dropped terms below t^6/5040 < 5e-8 relative), elsewhere
-// 1 - e^t with `et` = e^t.  Branch-free.  A NaN t takes the series, and stays
-// NaN whatever `et` is.
-__device__ __forceinline__ float one_minus_exp(float t, float et) {
-  float p = __builtin_fmaf(t, 1.0f / 720.0f, 1.0f / 120.0f);
-  p = __builtin_fmaf(t, p, 1.0f / 24.0f);
-  p = __builtin_fmaf(t, p, 1.0f / 6.0f);
-  p = __builtin_fmaf(t, p, 0.5f);
-  p = __builtin_fmaf(t, p, 1.0f);
-  return __builtin_fabsf(t) >= 0.25f ? 1.0f - et : -t * p;
+// softplus(x) and its slope sigmoid(x) from one exponential: with w = e^-|x| the
+// slope is 1/(1 + w) or w/(1 + w).
+__device__ __forceinline__ void softplus_pair(float x, float& sp, float& slope) {
+  const float w = exp2_hw(-__builtin_fabsf(x) * kLog2e);
+  sp = __int_as_float(max(__float_as_int(x), 0)) + log1p_unit(w);
+  slope = rcp_hw(1.0f + w) * (x < 0.0f ? w : 1.0f);
 }
 
-// The decay of one step from its base-2 exponent e2 = A log2(e) g, held at or
-// above the smallest normal float: exp is never 0, and an infinite state that
-// met a decay flushed to 0 would turn into NaN.  (A NaN exponent gives the
-// floor here; the input weight of that step is NaN and reaches the state.)
-__device__ __forceinline__ float decay_of(float e2) { return __builtin_fmaxf(exp2_hw(e2), kMinNormal); }
+// The gate of one step: its value g, the base-2 exponent e2 = A log2(e) g of the
+// decay, the decay a and the input weight w.
+//
+// The decay is held at or above the smallest normal float: exp is never 0, and an
+// infinite state that met a decay flushed to 0 would turn into NaN.  (A NaN
+// exponent gives the floor; that step's weight is NaN and reaches the state.)
+//
+// The weight is 1 - e^t, or its root, with t = A g or 2 A g.  Where |t| < 1/8 the
+// difference would magnify the rounding of e^t, so -t (e^t - 1)/t is taken, the
+// quotient as the cubic through its values at the Chebyshev nodes of [-1/8, 1/8]
+// (2.7e-7 relative at most), in powers of e2; elsewhere the difference itself,
+// whose rounding is then 2^-24 / 0.118 = 5e-7 relative at most.  Branch-free; a
+// NaN takes the cubic and stays NaN.
+struct Gate {
+  float g, e2, a, w;
+};
 
-// The input weight: 1 - a, or sqrt(1 - a^2) = sqrt(1 - e^(2 A g)); An = A or
-// 2A accordingly, so that An * g is the exponent whose complement is taken.
 template <int RULE>
-__device__ __forceinline__ float weight_of(float a, float An, float g) {
-  if constexpr ((RULE & kGateUnit) != 0) {
-    return __builtin_amdgcn_sqrtf(one_minus_exp(An * g, a * a));
-  } else {
-    return one_minus_exp(An * g, a);
-  }
+__device__ __forceinline__ Gate gate_of(float g, float A2) {
+  constexpr bool unit = (RULE & kGateUnit) != 0;
+  constexpr float s = unit ? 2.0f * kLn2 : kLn2;  // t = s e2
+  constexpr float k0 = -0.99999974559f * s, k1 = -0.49999995760f * s * s, k2 = -0.16679691739f * s * s * s,
+                  k3 = -0.04168837335f * s * s * s * s;
+  Gate r;
+  r.g = g;
+  r.e2 = A2 * g;
+  r.a = __builtin_fmaxf(exp2_hw(r.e2), kMinNormal);
+  float p = __builtin_fmaf(r.e2, k3, k2);
+  p = __builtin_fmaf(r.e2, p, k1);
+  p = __builtin_fmaf(r.e2, p, k0);
+  const float far = unit ? __builtin_fmaf(-r.a, r.a, 1.0f) : 1.0f - r.a;
+  const float m = __builtin_fabsf(r.e2) >= 0.125f / s ? far : r.e2 * p;
+  r.w = unit ? __builtin_amdgcn_sqrtf(m) : m;
+  return r;
 }
 
 // Bit k set where a sequence starts at step k of the run.
@@ -101,12 +117,36 @@ __device__ __forceinline__ void prefix_round(float& P, float& Q) {
 // Inclusive prefix of the lanes' maps, lane 0 first.
 template <bool CUT>
 __device__ __forceinline__ void wave_prefix(float& P, float& Q) {
-  prefix_round<CUT, 0x111, 0xf>(P, Q);  // row_shr:1
-  prefix_round<CUT, 0x112, 0xf>(P, Q);  // row_shr:2
-  prefix_round<CUT, 0x114, 0xf>(P, Q);  // row_shr:4
-  prefix_round<CUT, 0x118, 0xf>(P, Q);  // row_shr:8
-  prefix_round<CUT, 0x142, 0xa>(P, Q);  // row_bcast:15 into rows 1 and 3
-  prefix_round<CUT, 0x143, 0xc>(P, Q);  // row_bcast:31 into rows 2 and 3
+  if constexpr (CUT) {
+    prefix_round<CUT, 0x111, 0xf>(P, Q);  // row_shr:1
+    prefix_round<CUT, 0x112, 0xf>(P, Q);  // row_shr:2
+    prefix_round<CUT, 0x114, 0xf>(P, Q);  // row_shr:4
+    prefix_round<CUT, 0x118, 0xf>(P, Q);  // row_shr:8
+    prefix_round<CUT, 0x142, 0xa>(P, Q);  // row_bcast:15 into rows 1 and 3
+    prefix_round<CUT, 0x143, 0xc>(P, Q);  // row_bcast:31 into rows 2 and 3
+  } else {
+    // The same rounds without starts, the lane shift in the operation itself:
+    // Q += P Q_from, P = max(P P_from, the smallest normal float); a lane without
+    // a source is not written and keeps its map.  (From the compiler each shift
+    // is a move of its own: 5 instructions a round instead of 3.)  An operand
+    // that comes from another lane must have been written two instructions
+    // before: the waits stand for those that are missing.
+#define SSM_ROUND(SHIFT)                             \
+  "v_fmac_f32_dpp %1, %1, %0 " SHIFT " bank_mask:0xf\n" \
+  "s_nop 0\n"                                        \
+  "v_mul_f32_dpp %0, %0, %0 " SHIFT " bank_mask:0xf\n"  \
+  "v_max_f32_e32 %0, 0x800000, %0\n"
+    asm("s_nop 1\n"
+        SSM_ROUND("row_shr:1 row_mask:0xf")
+        SSM_ROUND("row_shr:2 row_mask:0xf")
+        SSM_ROUND("row_shr:4 row_mask:0xf")
+        SSM_ROUND("row_shr:8 row_mask:0xf")
+        SSM_ROUND("row_bcast:15 row_mask:0xa")
+        SSM_ROUND("row_bcast:31 row_mask:0xc")
+        "s_nop 1"
+        : "+v"(P), "+v"(Q));
+#undef SSM_ROUND
+  }
 }
 
 // The value of the lane before (`first` in lane 0).
