@@ -10,6 +10,10 @@
 // DPP rounds), and each lane reruns its steps from the state entering them:
 // one pass over HBM.  P = exp2 of the sum of the steps' exponents.
 //
+// Rows of at most 256 steps (W = 0) share a wave: a power of two of lanes to each,
+// whose first applies its map to the row's entering state and from then on
+// forgets what is before it, as at a start.
+//
 // Where there are too few rows to fill the chip with a wave each, W waves take a
 // row's blocks in turn, W at a time: each wave's map over its block goes to the
 // others through LDS (a barrier for every W blocks), and each applies those before
@@ -26,19 +30,58 @@ namespace ssm {
 
 namespace {
 
-// Waves of a workgroup with W waves to a row: 4 rows of one wave, else one row.
-constexpr int group_waves(int W) { return W == 1 ? 4 : W; }
+// Waves of a workgroup with W waves to a row: 4 of one row or several each, else
+// those of one row.
+constexpr int group_waves(int W) { return W <= 1 ? 4 : W; }
 
 struct GatedSizes {
   int rows, dim;
   int seqlen, nblk;
+  int lanes;  // lanes of a row (W = 0; else 64)
+  int once;   // inputs are read past the caches
 };
+
+// Where the calling lane works.  row is the wave's own but for W = 0.
+template <int W>
+struct Place {
+  int row;
+  int lane, w0;     // lane among the row's lanes; wave among the row's waves
+  bool live, last;  // a row of the call; the row's last lane
+};
+
+template <int W>
+__device__ __forceinline__ Place<W> place_of(const GatedSizes& p) {
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  Place<W> q;
+  if constexpr (W == 0) {
+    q.lane = lane & (p.lanes - 1);
+    q.row = (int)((blockIdx.x * group_waves(W) * 64 + threadIdx.x) / (unsigned)p.lanes);
+    q.live = q.row < p.rows;
+    if (!q.live) q.row = 0;
+    q.w0 = 0;
+    q.last = q.lane == p.lanes - 1;
+  } else {
+    q.lane = lane;
+    q.row = W == 1 ? blockIdx.x * group_waves(W) + wave : blockIdx.x;
+    q.live = q.row < p.rows;  // (with more waves to a row the grid is the rows)
+    q.w0 = W == 1 ? 0 : wave;
+    q.last = lane == 63;
+  }
+  return q;
+}
+
+// bf16 results are written past the caches: a wave's access is 1 KiB in one
+// piece (float32's two leave half lines between them; batch 8, dim 1536, L 2048
+// float32, backward: 198 us so against 178).
+template <typename T>
+constexpr bool kStoreOnce = sizeof(T) == 2;
 
 // A wave's total map, for the other waves of its row; two buffers, so that one
 // barrier for every W blocks is enough.
 template <int W>
 struct RowMaps {
-  float P[2][W], Q[2][W];
+  float P[2][W > 0 ? W : 1], Q[2][W > 0 ? W : 1];
 };
 
 // The value that enters wave `w` of a row's W, whose waves map it in the order
@@ -46,7 +89,7 @@ struct RowMaps {
 // before it.  `in` becomes the value after all of them.
 template <bool CUT, int W, bool REVERSE>
 __device__ __forceinline__ float through_waves(RowMaps<W>& s, int turn, int w, float P, float Q, float& in) {
-  if constexpr (W == 1) {
+  if constexpr (W <= 1) {
     return in;
   } else {
     // lane 63 of the prefix holds the wave's total
@@ -82,11 +125,9 @@ __global__ __launch_bounds__(64 * group_waves(W)) void gated_fwd_kernel(
     const T* __restrict__ z, const uint8_t* __restrict__ starts, const float* __restrict__ h0,
     T* __restrict__ y, float* __restrict__ last_state, float* __restrict__ ckpt, const GatedSizes p) {
   [[maybe_unused]] __shared__ RowMaps<W> maps;
-  const int lane = threadIdx.x & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int row = W == 1 ? blockIdx.x * group_waves(W) + wave : blockIdx.x;
-  const int w0 = W == 1 ? 0 : wave;  // this wave's place among the row's
-  if (row >= p.rows) return;         // (with more waves to a row the grid is the rows)
+  const Place<W> at = place_of<W>(p);
+  if (W > 0 && !at.live) return;
+  const int lane = at.lane, row = at.row, w0 = at.w0;
   const int b = row / p.dim, d = row - b * p.dim;
   const float A2 = A[d] * kLog2e;
   const float rb = r_bias != nullptr ? r_bias[d] : 0.0f, nrb = -rb * kLog2e;
@@ -94,17 +135,18 @@ __global__ __launch_bounds__(64 * group_waves(W)) void gated_fwd_kernel(
   const int64_t base = (int64_t)row * p.seqlen;
   float H = h0 != nullptr ? h0[row] : 0.0f;
 
-  // one block a wave; WHOLE: every step of the W blocks is in the row
-  auto blocks = [&](int b0, int turn, auto whole) {
-    constexpr bool WHOLE = decltype(whole)::value;
+  // one block a wave; WHOLE: every step of the W blocks is in the row; ONCE:
+  // inputs read past the caches
+  auto blocks = [&](int b0, int turn, auto whole, auto once) {
+    constexpr bool WHOLE = decltype(whole)::value, ONCE = decltype(once)::value;
     const int blk = b0 + w0;  // past the last block: no steps, the identity
     const int64_t t0 = (int64_t)blk * kGatedBlock + lane * kRun;
-    const int64_t left = p.seqlen - t0;
+    const int64_t left = at.live ? p.seqlen - t0 : 0;
     const int valid = WHOLE || left > kRun ? kRun : (int)(left < 0 ? 0 : left);  // steps of this lane's run
-    const RunWords<T> wr = load_run(r + base + t0, valid), wx = load_run(x + base + t0, valid);
+    const RunWords<T> wr = load_run<T, ONCE>(r + base + t0, valid), wx = load_run<T, ONCE>(x + base + t0, valid);
     RunWords<T> wi, wz;
-    if constexpr (IG) wi = load_run(ig + base + t0, valid);
-    if constexpr (ZG) wz = load_run(z + base + t0, valid);
+    if constexpr (IG) wi = load_run<T, ONCE>(ig + base + t0, valid);
+    if constexpr (ZG) wz = load_run<T, ONCE>(z + base + t0, valid);
     uint32_t cut = 0;
     if (starts != nullptr) cut = load_starts(starts + (int64_t)b * p.seqlen + t0, valid);
 
@@ -127,18 +169,26 @@ __global__ __launch_bounds__(64 * group_waves(W)) void gated_fwd_kernel(
       }
     }
     float P = __builtin_fmaxf(exp2_hw(S), kMinNormal), Q = 0.0f, h, h_in;
-    if (starts != nullptr) {
+    if (W == 0 || starts != nullptr) {
 #pragma unroll
       for (int k = 0; k < kRun; ++k) {
         if (cut & (1u << k)) a[k] = 0.0f;
         Q = apply_map<true>(a[k], q[k], Q);
       }
       if (cut != 0) P = 0.0f;
+      if (W == 0 && lane == 0) {
+        Q = apply_map<true>(P, Q, H);
+        P = 0.0f;
+      }
       wave_prefix<true>(P, Q);
       h_in = through_waves<true, W, false>(maps, turn, w0, P, Q, H);
       const float end = apply_map<true>(P, Q, h_in);
       h = lane_before(end, h_in);
       if constexpr (W == 1) H = lane_value(end, 63);
+      if constexpr (W == 0) {
+        if (lane == 0) h = H;
+        H = end;
+      }
 #pragma unroll
       for (int k = 0; k < kRun; ++k) q[k] = h = apply_map<true>(a[k], q[k], h);
     } else {
@@ -152,19 +202,30 @@ __global__ __launch_bounds__(64 * group_waves(W)) void gated_fwd_kernel(
 #pragma unroll
       for (int k = 0; k < kRun; ++k) q[k] = h = __builtin_fmaf(a[k], h, q[k]);
     }
-    if (ckpt != nullptr && lane == 0 && blk < p.nblk) ckpt[((int64_t)b * p.nblk + blk) * p.dim + d] = h_in;
+    if (ckpt != nullptr && lane == 0 && at.live && blk < p.nblk)
+      ckpt[((int64_t)b * p.nblk + blk) * p.dim + d] = h_in;
     if constexpr (ZG) {
       float fz[kRun];
       run_floats<T>(wz, fz);
 #pragma unroll
       for (int k = 0; k < kRun; ++k) q[k] *= silu_f32(fz[k]);
     }
-    store_run<T>(y + base + t0, valid, q);
+    store_run<T, kStoreOnce<T>>(y + base + t0, valid, q);
   };
-  int b0 = 0, turn = 0;
-  for (; (int64_t)(b0 + W) * kGatedBlock <= p.seqlen; b0 += W, turn ^= 1) blocks(b0, turn, BoolC<true>{});
-  if (b0 < p.nblk) blocks(b0, turn, BoolC<false>{});
-  if (last_state != nullptr && lane == 0 && w0 == 0) last_state[row] = H;
+  if constexpr (W == 0) {
+    blocks(0, 0, BoolC<false>{}, BoolC<false>{});
+  } else {
+    int b0 = 0, turn = 0;
+    auto wholes = [&](auto once) {
+      for (; (int64_t)(b0 + W) * kGatedBlock <= p.seqlen; b0 += W, turn ^= 1) blocks(b0, turn, BoolC<true>{}, once);
+    };
+    if constexpr (kStoreOnce<T>) {
+      if (p.once) wholes(BoolC<true>{});
+    }
+    wholes(BoolC<false>{});
+    if (b0 < p.nblk) blocks(b0, turn, BoolC<false>{}, BoolC<false>{});
+  }
+  if (last_state != nullptr && at.live && at.last && w0 == 0) last_state[row] = H;
 }
 
 template <typename T, int RULE, bool IG, bool ZG, int W>
@@ -176,11 +237,9 @@ __global__ __launch_bounds__(64 * group_waves(W)) void gated_bwd_kernel(
     T* __restrict__ di, T* __restrict__ dz, float* __restrict__ row_dA, float* __restrict__ row_drb,
     float* __restrict__ row_dib, float* __restrict__ dh0, const GatedSizes p) {
   [[maybe_unused]] __shared__ RowMaps<W> maps;
-  const int lane = threadIdx.x & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int row = W == 1 ? blockIdx.x * group_waves(W) + wave : blockIdx.x;
-  const int w0 = W == 1 ? 0 : wave;  // this wave's place among the row's
-  if (row >= p.rows) return;         // (with more waves to a row the grid is the rows)
+  const Place<W> at = place_of<W>(p);
+  if (W > 0 && !at.live) return;
+  const int lane = at.lane, row = at.row, w0 = at.w0;
   const int b = row / p.dim, d = row - b * p.dim;
   const float Ad = A[d], A2 = Ad * kLog2e;
   const float rb = r_bias != nullptr ? r_bias[d] : 0.0f, nrb = -rb * kLog2e;
@@ -190,20 +249,20 @@ __global__ __launch_bounds__(64 * group_waves(W)) void gated_bwd_kernel(
   // the row's sums, over up to 2^31 steps: in float64 across blocks
   double sA = 0.0, srb = 0.0, sib = 0.0;
 
-  auto blocks = [&](int b0, int turn, auto whole) {
-    constexpr bool WHOLE = decltype(whole)::value;
+  auto blocks = [&](int b0, int turn, auto whole, auto once) {
+    constexpr bool WHOLE = decltype(whole)::value, ONCE = decltype(once)::value;
     const int blk = b0 + w0;  // past the last block: no steps, the identity
     const int64_t t0 = (int64_t)blk * kGatedBlock + lane * kRun;
-    const int64_t left = p.seqlen - t0;
+    const int64_t left = at.live ? p.seqlen - t0 : 0;
     const int valid = WHOLE || left > kRun ? kRun : (int)(left < 0 ? 0 : left);
-    const RunWords<T> wr = load_run(r + base + t0, valid), wx = load_run(x + base + t0, valid);
+    const RunWords<T> wr = load_run<T, ONCE>(r + base + t0, valid), wx = load_run<T, ONCE>(x + base + t0, valid);
     RunWords<T> wi, wz;
-    if constexpr (IG) wi = load_run(ig + base + t0, valid);
-    if constexpr (ZG) wz = load_run(z + base + t0, valid);
-    const RunWords<T> wd = load_run(dy + base + t0, valid);
-    const bool packed = starts != nullptr;
+    if constexpr (IG) wi = load_run<T, ONCE>(ig + base + t0, valid);
+    if constexpr (ZG) wz = load_run<T, ONCE>(z + base + t0, valid);
+    const RunWords<T> wd = load_run<T, ONCE>(dy + base + t0, valid);
+    const bool packed = W == 0 || starts != nullptr;
     uint32_t cut = 0;
-    if (packed) cut = load_starts(starts + (int64_t)b * p.seqlen + t0, valid);
+    if (starts != nullptr) cut = load_starts(starts + (int64_t)b * p.seqlen + t0, valid);
     const float H = WHOLE || blk < p.nblk ? ckpt[((int64_t)b * p.nblk + blk) * p.dim + d] : 0.0f;
 
     // g of each step, A dg/dr, the input gate and its complement
@@ -251,8 +310,13 @@ __global__ __launch_bounds__(64 * group_waves(W)) void gated_bwd_kernel(
       if (packed) {
 #pragma unroll
         for (int k = 0; k < kRun; ++k) Q = apply_map<true>((cut & (1u << k)) ? 0.0f : a[k], q[k], Q);
+        if (W == 0 && lane == 0) {
+          Q = apply_map<true>(Pf, Q, H);
+          Pf = 0.0f;
+        }
         wave_prefix<true>(Pf, Q);
         h = lane_before(apply_map<true>(Pf, Q, H), H);
+        if (W == 0 && lane == 0) h = H;
 #pragma unroll
         for (int k = 0; k < kRun; ++k) {
           hb[k] = (cut & (1u << k)) ? 0.0f : h;
@@ -283,7 +347,7 @@ __global__ __launch_bounds__(64 * group_waves(W)) void gated_bwd_kernel(
         o[k] = ds * q[k] * __builtin_fmaf(fz[k], c, 1.0f);
         dh[k] = ds * fz[k];
       }
-      store_run<T>(dz + base + t0, valid, o);
+      store_run<T, kStoreOnce<T>>(dz + base + t0, valid, o);
     }
 
     // the adjoint entering the run from the right
@@ -297,7 +361,10 @@ __global__ __launch_bounds__(64 * group_waves(W)) void gated_bwd_kernel(
 #pragma unroll
         for (int k = kRun - 1; k >= 0; --k) Q = a[k] * (dh[k] + Q);
       }
-      float Pr = lane_mirror(P, lane), Qr = lane_mirror(Q, lane), end, m_in;
+      // in a shared wave the row's last lane applies its map to what enters
+      if (W == 0 && at.last) Q = apply_map<true>(P, Q, M);
+      const int place = threadIdx.x & 63;
+      float Pr = lane_mirror(W == 0 && at.last ? 0.0f : P, place), Qr = lane_mirror(Q, place), end, m_in;
       if (packed) {
         wave_prefix<true>(Pr, Qr);
         m_in = through_waves<true, W, true>(maps, turn, w0, Pr, Qr, M);
@@ -307,8 +374,12 @@ __global__ __launch_bounds__(64 * group_waves(W)) void gated_bwd_kernel(
         m_in = through_waves<false, W, true>(maps, turn, w0, Pr, Qr, M);
         end = __builtin_fmaf(Pr, m_in, Qr);
       }
-      m = lane_mirror(lane_before(end, m_in), lane);
+      m = lane_mirror(lane_before(end, m_in), place);
       if constexpr (W == 1) M = lane_value(end, 63);
+      if constexpr (W == 0) {
+        if (at.last) m = M;
+        M = lane_mirror(end, place);  // the first lane's goes to dh0
+      }
     }
 
     // the gradients of each step, from the right; with u = x sigmoid(i)
@@ -335,23 +406,32 @@ __global__ __launch_bounds__(64 * group_waves(W)) void gated_bwd_kernel(
         pib += odi[k];
       }
     }
-    store_run<T>(dx + base + t0, valid, odx);
-    store_run<T>(dr + base + t0, valid, odr);
-    if constexpr (IG) store_run<T>(di + base + t0, valid, odi);
+    store_run<T, kStoreOnce<T>>(dx + base + t0, valid, odx);
+    store_run<T, kStoreOnce<T>>(dr + base + t0, valid, odr);
+    if constexpr (IG) store_run<T, kStoreOnce<T>>(di + base + t0, valid, odi);
     sA += (double)pA;
     srb += (double)prb;
     if constexpr (IG) sib += (double)pib;
   };
-  int b0 = (p.nblk - 1) / W * W, turn = 0;
-  if ((int64_t)(b0 + W) * kGatedBlock > p.seqlen) {
-    blocks(b0, turn, BoolC<false>{});
-    b0 -= W;
-    turn ^= 1;
+  if constexpr (W == 0) {
+    blocks(0, 0, BoolC<false>{}, BoolC<false>{});
+  } else {
+    int b0 = (p.nblk - 1) / W * W, turn = 0;
+    if ((int64_t)(b0 + W) * kGatedBlock > p.seqlen) {
+      blocks(b0, turn, BoolC<false>{}, BoolC<false>{});
+      b0 -= W;
+      turn ^= 1;
+    }
+    auto wholes = [&](auto once) {
+      for (; b0 >= 0; b0 -= W, turn ^= 1) blocks(b0, turn, BoolC<true>{}, once);
+    };
+    if constexpr (kStoreOnce<T>) {
+      if (p.once) wholes(BoolC<true>{});
+    }
+    wholes(BoolC<false>{});
   }
-  for (; b0 >= 0; b0 -= W, turn ^= 1) blocks(b0, turn, BoolC<true>{});
 
-#pragma unroll
-  for (int off = 1; off < 64; off <<= 1) {
+  for (int off = 1; off < (W == 0 ? p.lanes : 64); off <<= 1) {
     sA += __shfl_xor(sA, off);
     srb += __shfl_xor(srb, off);
     if constexpr (IG) sib += __shfl_xor(sib, off);
@@ -372,7 +452,7 @@ __global__ __launch_bounds__(64 * group_waves(W)) void gated_bwd_kernel(
       sib += s_sum[2][j];
     }
   }
-  if (lane == 0 && w0 == 0) {
+  if (lane == 0 && w0 == 0 && at.live) {
     row_dA[row] = (float)sA;
     if (row_drb != nullptr) row_drb[row] = (float)srb;
     if (IG && row_dib != nullptr) row_dib[row] = (float)sib;
@@ -435,18 +515,45 @@ hipError_t by_rule(const GatedLaunch& a, F&& f) {
   }
 }
 
-// Waves to a row: one where the rows alone make the 8192 waves that fill the
+// Waves to a row: several rows to a wave up to half a wave's block (0); one where the rows alone make the 8192 waves that fill the
 // chip, more where they do not and the sequence has blocks for them (batch 1,
 // dim 2048, L 65536 bf16: one 266 us, four 234, sixteen 238; batch 3, dim 1000,
 // L 1777 float32: 23.4, 22.6, 68; batch 8, dim 5120, L 2048, backward: 231, 257).
 int waves_of(const GatedLaunch& a) {
   const int64_t rows = (int64_t)a.batch * a.dim, nblk = (a.seqlen + kGatedBlock - 1) / kGatedBlock;
+  if (a.seqlen <= 256) return 0;
   if (rows >= 8192 || nblk == 1) return 1;
   return rows >= 2048 || nblk <= 4 ? 4 : 16;
 }
 
+// Whether inputs are read past the caches: bf16 rows of whole lines (others
+// share lines between waves, which the caches then join) in a call whose tensors
+// are more than the 256 MiB that the last cache holds anyway.  Batch 16, dim
+// 5120, L 2048: 220 us so, 238 otherwise; batch 8, its backward: 201, 212; batch
+// 4, dim 1000, L 8000 (not whole lines, smaller): 61, 52.
+bool read_once(const GatedLaunch& a) {
+  const int64_t streams = 3 + (a.i != nullptr) + (a.z != nullptr) + (a.dy != nullptr ? 2 + (a.i != nullptr) + (a.z != nullptr) : 0);
+  const int64_t bytes = (int64_t)a.batch * a.dim * a.seqlen * 2;
+  auto lines = [](const void* p) { return reinterpret_cast<uintptr_t>(p) % 128 == 0; };
+  return a.dtype == Dtype::BF16 && a.seqlen % 64 == 0 && streams * bytes > (int64_t)256 << 20 && lines(a.x) &&
+         lines(a.r) && lines(a.i) && lines(a.z) && lines(a.dy);
+}
+
 GatedSizes sizes_of(const GatedLaunch& a) {
-  return GatedSizes{a.batch * a.dim, a.dim, (int)a.seqlen, (int)((a.seqlen + kGatedBlock - 1) / kGatedBlock)};
+  int lanes = 64;
+  if (waves_of(a) == 0) {
+    lanes = 1;
+    while (lanes * kRun < a.seqlen) lanes *= 2;
+  }
+  return GatedSizes{a.batch * a.dim, a.dim, (int)a.seqlen, (int)((a.seqlen + kGatedBlock - 1) / kGatedBlock), lanes,
+                    read_once(a)};
+}
+
+// Workgroups: of rows that share waves, of a wave to a row, or a row each.
+template <int W>
+unsigned groups_of(const GatedSizes& s) {
+  const int64_t rows = W == 0 ? (int64_t)group_waves(W) * 64 / s.lanes : W == 1 ? group_waves(W) : 1;
+  return (unsigned)((s.rows + rows - 1) / rows);
 }
 
 template <typename T>
@@ -456,6 +563,7 @@ struct FwdLaunch {
   template <int RULE, bool IG, bool ZG>
   hipError_t operator()() const {
     switch (waves_of(a)) {
+      case 0: return launch<RULE, IG, ZG, 0>();
       case 1: return launch<RULE, IG, ZG, 1>();
       case 4: return launch<RULE, IG, ZG, 4>();
       default: return launch<RULE, IG, ZG, 16>();
@@ -464,7 +572,7 @@ struct FwdLaunch {
   template <int RULE, bool IG, bool ZG, int W>
   hipError_t launch() const {
     const GatedSizes s = sizes_of(a);
-    const unsigned grid = (unsigned)(W == 1 ? (s.rows + group_waves(W) - 1) / group_waves(W) : s.rows);
+    const unsigned grid = groups_of<W>(s);
     gated_fwd_kernel<T, RULE, IG, ZG, W><<<grid, 64 * group_waves(W), 0, stream>>>(
         static_cast<const T*>(a.x), static_cast<const T*>(a.r), a.A, a.r_bias, static_cast<const T*>(a.i),
         a.i_bias, static_cast<const T*>(a.z), a.starts, a.h0, static_cast<T*>(a.y), a.last_state, a.ckpt, s);
@@ -479,6 +587,7 @@ struct BwdLaunchOf {
   template <int RULE, bool IG, bool ZG>
   hipError_t operator()() const {
     switch (waves_of(a)) {
+      case 0: return launch<RULE, IG, ZG, 0>();
       case 1: return launch<RULE, IG, ZG, 1>();
       case 4: return launch<RULE, IG, ZG, 4>();
       default: return launch<RULE, IG, ZG, 16>();
@@ -487,7 +596,7 @@ struct BwdLaunchOf {
   template <int RULE, bool IG, bool ZG, int W>
   hipError_t launch() const {
     const GatedSizes s = sizes_of(a);
-    const unsigned grid = (unsigned)(W == 1 ? (s.rows + group_waves(W) - 1) / group_waves(W) : s.rows);
+    const unsigned grid = groups_of<W>(s);
     // one row per channel: its sums are the results
     const bool direct = a.batch == 1;
     const int64_t plane = (int64_t)a.batch * a.dim;

@@ -24,15 +24,17 @@ struct RunWords {
   uint32_t w[kWords];
 };
 
-// Elements p[0 .. kRun-1]; those from `valid` on read as zero and are not touched.
-template <typename T>
+// Elements p[0 .. kRun-1]; those from `valid` on read as zero and are not
+// touched.  ONCE: read past the caches (non-temporal).
+template <typename T, bool ONCE = false>
 __device__ __forceinline__ RunWords<T> load_run(const T* p, int valid) {
   typedef typename RunWords<T>::vec4 vec4;
   RunWords<T> r;
   if (valid >= kRun) {
 #pragma unroll
     for (int q = 0; q < RunWords<T>::kWords / 4; ++q) {
-      const vec4 v = reinterpret_cast<const vec4*>(p)[q];
+      const vec4 v = ONCE ? __builtin_nontemporal_load(reinterpret_cast<const vec4*>(p) + q)
+                          : reinterpret_cast<const vec4*>(p)[q];
       r.w[4 * q] = v.x; r.w[4 * q + 1] = v.y; r.w[4 * q + 2] = v.z; r.w[4 * q + 3] = v.w;
     }
   } else if constexpr (sizeof(T) == 2) {
@@ -50,7 +52,8 @@ __device__ __forceinline__ RunWords<T> load_run(const T* p, int valid) {
 }
 
 // Store the first `valid` of kRun floats as T (bf16: round to nearest even).
-template <typename T>
+// ONCE: as above.
+template <typename T, bool ONCE = false>
 __device__ __forceinline__ void store_run(T* p, int valid, const float (&f)[kRun]) {
   typedef typename RunWords<T>::vec4 vec4;
   if (valid >= kRun) {
@@ -59,7 +62,8 @@ __device__ __forceinline__ void store_run(T* p, int valid, const float (&f)[kRun
 #pragma unroll
     for (int q = 0; q < RunWords<T>::kWords / 4; ++q) {
       const vec4 v = {w[4 * q], w[4 * q + 1], w[4 * q + 2], w[4 * q + 3]};
-      reinterpret_cast<vec4*>(p)[q] = v;
+      if constexpr (ONCE) __builtin_nontemporal_store(v, reinterpret_cast<vec4*>(p) + q);
+      else reinterpret_cast<vec4*>(p)[q] = v;
     }
   } else {
 #pragma unroll
