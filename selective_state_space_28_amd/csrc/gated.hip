@@ -528,14 +528,14 @@ int waves_of(const GatedLaunch& a) {
 
 // Whether inputs are read past the caches: bf16 rows of whole lines (others
 // share lines between waves, which the caches then join) in a call whose tensors
-// are more than the 256 MiB that the last cache holds anyway.  Batch 16, dim
-// 5120, L 2048: 220 us so, 238 otherwise; batch 8, its backward: 201, 212; batch
-// 4, dim 1000, L 8000 (not whole lines, smaller): 61, 52.
+// are twice the 256 MiB that the last cache may hold.  Batch 16, dim 5120, L 2048:
+// 220 us so, 238 otherwise; batch 8, its backward: 201, 212; batch 4, dim 1000, L
+// 8000, 320 MB of tensors again and again: 61, 52.
 bool read_once(const GatedLaunch& a) {
   const int64_t streams = 3 + (a.i != nullptr) + (a.z != nullptr) + (a.dy != nullptr ? 2 + (a.i != nullptr) + (a.z != nullptr) : 0);
   const int64_t bytes = (int64_t)a.batch * a.dim * a.seqlen * 2;
   auto lines = [](const void* p) { return reinterpret_cast<uintptr_t>(p) % 128 == 0; };
-  return a.dtype == Dtype::BF16 && a.seqlen % 64 == 0 && streams * bytes > (int64_t)256 << 20 && lines(a.x) &&
+  return a.dtype == Dtype::BF16 && a.seqlen % 64 == 0 && streams * bytes > (int64_t)512 << 20 && lines(a.x) &&
          lines(a.r) && lines(a.i) && lines(a.z) && lines(a.dy);
 }
 

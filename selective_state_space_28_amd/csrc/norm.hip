@@ -433,6 +433,22 @@ __device__ __forceinline__ void add_lanes(float (&v)[N]) {
   }
 }
 
+// A lane's piece kept in LDS, and read back.
+template <typename T>
+__device__ __forceinline__ void keep(uint4* s, const Piece<T>& v) {
+  *s = make_uint4(v.w[0], v.w[1], v.w[2], v.w[3]);
+}
+template <typename T>
+__device__ __forceinline__ Piece<T> kept_piece(const uint4* s) {
+  const uint4 v = *s;
+  Piece<T> r;
+  r.w[0] = v.x; r.w[1] = v.y; r.w[2] = v.z; r.w[3] = v.w;
+  return r;
+}
+
+// Floats of LDS that n parameters of the channels take, in whole pieces.
+__host__ __device__ constexpr int param_floats(int n, int dim) { return (n * dim + 3) / 4 * 4; }
+
 // The spread of each step of a tile over the workgroup's waves: what every lane's
 // own spread (its channels) joins to.  mean and rstd of the lane's steps come
 // back, and go to mean_out and rstd_out.  Two barriers.
@@ -498,8 +514,8 @@ __device__ __forceinline__ float param(bool lds, const float* s, const float* p,
 }
 
 // Columns, forward.  A wave takes the accesses w, w + waves, ...  The first K of
-// them stay in registers from the sums to the results; any further ones are
-// read twice.  A workgroup fills a CU's registers, so it overlaps its own loads
+// them stay in registers from the sums to the results, `kept` more in LDS (each
+// lane its own pieces); any further ones are read twice.  A workgroup fills a CU's registers, so it overlaps its own loads
 // and stores: it goes over several tiles, and as a piece's result is stored the
 // same registers take the next tile's piece.  weight and bias wait in LDS (a
 // global load would wait for every piece in flight before it).
@@ -507,15 +523,17 @@ template <typename T, int TL, int K, bool RES>
 __global__ __launch_bounds__(64 * kTileWaves, 2) void norm_cols_fwd_kernel(
     const T* __restrict__ x, const T* __restrict__ residual, const float* __restrict__ weight,
     const float* __restrict__ bias, float eps, T* __restrict__ y, T* sum_out, float* __restrict__ mean_out,
-    float* __restrict__ rstd_out, int dim, int seqlen, int tiles, int all_tiles, int lds, int once) {
+    float* __restrict__ rstd_out, int dim, int seqlen, int tiles, int all_tiles, int lds, int kept,
+    int once) {
   constexpr int E = Piece<T>::kN, R = 64 / TL, U = 4;
   __shared__ TileStats<T, TL> stats;
-  extern __shared__ float s_par[];  // weight, then bias
+  extern __shared__ float s_par[];  // weight, then bias, then the kept pieces
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), waves = blockDim.x >> 6;
   int first = wave * R;
   const int stride = waves * R;
   const int beyond = K * stride;  // channels held
+  uint4* const s_kept = reinterpret_cast<uint4*>(s_par + (lds ? param_floats(2, dim) : 0)) + threadIdx.x;
   if (lds) {
     for (int k = threadIdx.x; k < dim; k += blockDim.x) {
       s_par[k] = weight[k];
@@ -569,7 +587,7 @@ __global__ __launch_bounds__(64 * kTileWaves, 2) void norm_cols_fwd_kernel(
       }
       v[c].renew();
     }
-    for (int d4 = beyond; d4 < dim; d4 += U * stride) {  // the channels that are not held
+    for (int d4 = beyond, n = 0; d4 < dim; d4 += U * stride, n += U) {  // the channels beyond
       Piece<T> e[U];
 #pragma unroll
       for (int u = 0; u < U; ++u)
@@ -591,17 +609,21 @@ __global__ __launch_bounds__(64 * kTileWaves, 2) void norm_cols_fwd_kernel(
           }
           sp.add(f, rcp_hw(sp.n + 1.0f));
         }
+        if (n + u < kept) keep(s_kept + (n + u) * blockDim.x, e[u]);
       }
     }
     float mean[E], rstd[E];
     tile_stats<T, TL>(sp, stats, eps, tile, dim, seqlen, tiles, mean_out, rstd_out, mean, rstd);
     first = renewed(first);
     const T* const again = RES ? sum_out : x;
-    for (int d4 = beyond; d4 < dim; d4 += U * stride) {
+    for (int d4 = beyond, n = 0; d4 < dim; d4 += U * stride, n += U) {
       Piece<T> e[U];
 #pragma unroll
-      for (int u = 0; u < U; ++u)
-        e[u] = load_whole(at_bytes(again + p.row + (int64_t)inside(d4 + first + u * stride, R, dim) * seqlen, p.at));
+      for (int u = 0; u < U; ++u) {
+        const int di = inside(d4 + first + u * stride, R, dim);
+        e[u] = n + u < kept ? kept_piece<T>(s_kept + (n + u) * blockDim.x)
+                            : load_whole(at_bytes(again + p.row + (int64_t)di * seqlen, p.at));
+      }
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         const int dw = d4 + first + u * stride, di = inside(dw, R, dim), d = di + lane / TL;
@@ -644,15 +666,17 @@ template <typename T, int TL, int K>
 __global__ __launch_bounds__(64 * kTileWaves, 2) void norm_cols_bwd_kernel(
     const T* __restrict__ x, const float* __restrict__ weight, const float* __restrict__ mean_in,
     const float* __restrict__ rstd_in, const T* __restrict__ dy, const T* __restrict__ dsum,
-    T* __restrict__ dx, float* __restrict__ part, int dim, int seqlen, int tiles, int all_tiles, int lds, int once) {
+    T* __restrict__ dx, float* __restrict__ part, int dim, int seqlen, int tiles, int all_tiles, int lds, int kept,
+    int once) {
   constexpr int E = Piece<T>::kN, R = 64 / TL, U = 2;
   __shared__ float s_part[kTileWaves][2][TL * E], s_mean[2][TL * E];
-  extern __shared__ float s_par[];  // sums of dweight, of dbias, then weight
+  extern __shared__ float s_par[];  // sums of dweight, of dbias, weight, then the kept pieces
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), waves = blockDim.x >> 6;
   int first = wave * R;
   const int stride = waves * R;
   const int beyond = K * stride;  // channels held
+  uint4* const s_kept = reinterpret_cast<uint4*>(s_par + (lds ? param_floats(3, dim) : 0)) + threadIdx.x;
   float* const pw = part + (int64_t)blockIdx.x * 2 * dim;
   for (int k = threadIdx.x; k < dim; k += blockDim.x) {
     if (lds) {
@@ -748,7 +772,7 @@ __global__ __launch_bounds__(64 * kTileWaves, 2) void norm_cols_bwd_kernel(
       vd[c].renew();
       hold_back(c);
     }
-    for (int d4 = beyond; d4 < dim; d4 += U * stride) {  // the channels that are not held
+    for (int d4 = beyond, n = 0; d4 < dim; d4 += U * stride, n += U) {  // the channels beyond
       Piece<T> ex[U], ed[U];
 #pragma unroll
       for (int u = 0; u < U; ++u) {
@@ -757,7 +781,13 @@ __global__ __launch_bounds__(64 * kTileWaves, 2) void norm_cols_bwd_kernel(
         ed[u] = load_whole(at_bytes(dy + base, p.at));
       }
 #pragma unroll
-      for (int u = 0; u < U; ++u) take(ex[u], ed[u], p, d4 + first + u * stride);
+      for (int u = 0; u < U; ++u) {
+        take(ex[u], ed[u], p, d4 + first + u * stride);
+        if (n + u < kept) {
+          keep(s_kept + 2 * (n + u) * blockDim.x, ex[u]);
+          keep(s_kept + (2 * (n + u) + 1) * blockDim.x, ed[u]);
+        }
+      }
     }
     add_lanes<TL, 2 * E>(s);
     if (lane < TL) {
@@ -781,13 +811,18 @@ __global__ __launch_bounds__(64 * kTileWaves, 2) void norm_cols_bwd_kernel(
       c2[k] = s_mean[1][lane % TL * E + k];
     }
     first = renewed(first);
-    for (int d4 = beyond; d4 < dim; d4 += U * stride) {
+    for (int d4 = beyond, n = 0; d4 < dim; d4 += U * stride, n += U) {
       Piece<T> ex[U], ed[U];
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         const int64_t base = p.row + (int64_t)inside(d4 + first + u * stride, R, dim) * seqlen;
-        ex[u] = load_whole(at_bytes(x + base, p.at));
-        ed[u] = load_whole(at_bytes(dy + base, p.at));
+        if (n + u < kept) {
+          ex[u] = kept_piece<T>(s_kept + 2 * (n + u) * blockDim.x);
+          ed[u] = kept_piece<T>(s_kept + (2 * (n + u) + 1) * blockDim.x);
+        } else {
+          ex[u] = load_whole(at_bytes(x + base, p.at));
+          ed[u] = load_whole(at_bytes(dy + base, p.at));
+        }
       }
 #pragma unroll
       for (int u = 0; u < U; ++u) give(ex[u], ed[u], p, d4 + first + u * stride);
@@ -1013,6 +1048,29 @@ int whole_lines(const NormLaunch& a, const ColPlan& p, size_t es, const void* ou
 // Most channels whose parameters (and sums of their gradients) wait in LDS.
 constexpr int kLdsDimFwd = 8192, kLdsDimBwd = 5120;
 
+// Dynamic LDS of a column kernel: n parameters a channel, then accesses that the
+// registers do not hold (`arrays` pieces each), as far as a CU's 160 KiB go.
+struct LdsPlan {
+  int lds, kept;
+  size_t bytes;
+};
+
+LdsPlan lds_plan(const ColPlan& p, int dim, int most, int n, int arrays) {
+  constexpr size_t room = (size_t)160 * 1024 - 40 * 1024 / 8;  // less the sums' static arrays (with TL = 64: no accesses kept)
+  LdsPlan l{};
+  l.lds = dim <= most;
+  l.bytes = l.lds ? (size_t)param_floats(n, dim) * 4 : 0;
+  const int rows = 64 / p.TL, need = (dim + rows - 1) / rows;
+  const int each = (need + p.waves - 1) / p.waves;  // accesses of a wave
+  const size_t access = (size_t)p.waves * 64 * 16 * arrays;
+  if (each > p.K && p.TL < 64) {
+    const size_t fit = (room - l.bytes) / access;
+    l.kept = each - p.K < (int)fit ? each - p.K : (int)fit;
+    l.bytes += (size_t)l.kept * access;
+  }
+  return l;
+}
+
 template <typename T, int K, int LR>
 hipError_t rows_fwd(const NormLaunch& a, const RowPlan& pl, hipStream_t stream) {
   const int slots = pl.lanes() < 256 ? 256 / pl.lanes() : 1;
@@ -1065,10 +1123,10 @@ struct RowsBwd {
 
 template <typename T, int TL, int K, bool RES>
 hipError_t cols_fwd_launch(const NormLaunch& a, const ColPlan& p, hipStream_t stream) {
-  const int lds = a.dim <= kLdsDimFwd;
-  norm_cols_fwd_kernel<T, TL, K, RES><<<(unsigned)p.groups, 64 * p.waves, lds ? (size_t)a.dim * 8 : 0, stream>>>(
+  const LdsPlan l = lds_plan(p, a.dim, kLdsDimFwd, 2, 1);
+  norm_cols_fwd_kernel<T, TL, K, RES><<<(unsigned)p.groups, 64 * p.waves, l.bytes, stream>>>(
       static_cast<const T*>(a.x), static_cast<const T*>(a.residual), a.weight, a.bias, a.eps,
-      static_cast<T*>(a.y), static_cast<T*>(a.sum_out), a.mean, a.rstd, a.dim, (int)a.seqlen, p.tiles, p.all, lds,
+      static_cast<T*>(a.y), static_cast<T*>(a.sum_out), a.mean, a.rstd, a.dim, (int)a.seqlen, p.tiles, p.all, l.lds, l.kept,
       whole_lines(a, p, sizeof(T), a.y));
   return hipGetLastError();
 }
@@ -1084,11 +1142,11 @@ hipError_t cols_fwd(const NormLaunch& a, const ColPlan& p, hipStream_t stream) {
 
 template <typename T, int TL>
 hipError_t cols_bwd(const NormLaunch& a, const ColPlan& p, hipStream_t stream) {
-  const int lds = a.dim <= kLdsDimBwd;
+  const LdsPlan l = lds_plan(p, a.dim, kLdsDimBwd, 3, 2);
   auto kernel = p.K == kHeldBwd[0] ? norm_cols_bwd_kernel<T, TL, kHeldBwd[0]> : norm_cols_bwd_kernel<T, TL, kHeldBwd[1]>;
-  kernel<<<(unsigned)p.groups, 64 * p.waves, lds ? (size_t)a.dim * 12 : 0, stream>>>(
+  kernel<<<(unsigned)p.groups, 64 * p.waves, l.bytes, stream>>>(
       static_cast<const T*>(a.x), a.weight, a.mean, a.rstd, static_cast<const T*>(a.dy),
-      static_cast<const T*>(a.dsum), static_cast<T*>(a.dx), a.part, a.dim, (int)a.seqlen, p.tiles, p.all, lds,
+      static_cast<const T*>(a.dsum), static_cast<T*>(a.dx), a.part, a.dim, (int)a.seqlen, p.tiles, p.all, l.lds, l.kept,
       whole_lines(a, p, sizeof(T), a.dx));
   return hipGetLastError();
 }
