@@ -334,7 +334,7 @@ def test_offsets_past_32_bits(dev):
 
 @pytest.mark.parametrize("gate,weight", [("sigmoid", "unit"), ("softplus", "convex"), ("softplus", "unit")])
 @pytest.mark.parametrize("i,z", [(True, True), (False, False)])
-@pytest.mark.parametrize("b,d", [(1, 1), (3, 5), (2, 513), (7, 1031), (300, 64)])
+@pytest.mark.parametrize("b,d", [(1, 1), (3, 5), (2, 513), (7, 1031), (300, 64), (64, 4096), (50, 5243), (70000, 4)])
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 def test_step(dev, dtype, b, d, i, z, gate, weight):
     import torch
