@@ -84,21 +84,15 @@ size_t ssm_gated_scan_ckpt_bytes(int batch, int dim, int64_t seqlen);
  *   ckpt         out  ssm_gated_scan_ckpt_bytes(...)    NULL -> not written
  *                     bytes or more (SSM_ERR_WORKSPACE), 4-byte aligned: what
  *                     ssm_gated_scan_bwd starts from
- *   workspace    at least ssm_gated_scan_fwd_workspace_bytes(...) bytes,
- *                256-byte aligned, owned by the caller (NULL where the query
- *                returns 0); calls sharing one workspace must not overlap
- *   batch, dim, seqlen >= 0; seqlen at most 2^31 - 4097.  seqlen == 0 only
+ *   batch, dim, seqlen >= 0; batch * dim at most 2^31 - 513, seqlen at most
+ *   2^31 - 4097 (SSM_ERR_SHAPE); no workspace.  seqlen == 0 only
  *   writes last_state (= h0, or zeros).
  */
 int ssm_gated_scan_fwd(const void* x, const void* r, const float* A, const float* r_bias,
                        const void* i, const float* i_bias, const void* z, int flags,
                        const uint8_t* starts, const float* h0, void* y, float* last_state,
                        float* ckpt, size_t ckpt_bytes, int batch, int dim, int64_t seqlen,
-                       int dtype, void* workspace, size_t workspace_bytes, void* stream);
-
-/* Bytes of device workspace of ssm_gated_scan_fwd.  Pure host function; 0 for
- * an empty problem and for arguments that it would refuse. */
-size_t ssm_gated_scan_fwd_workspace_bytes(int batch, int dim, int64_t seqlen, int dtype);
+                       int dtype, void* stream);
 
 /*
  * ssm_gated_scan_bwd -- gradients of a loss through ssm_gated_scan_fwd, given
@@ -120,7 +114,9 @@ size_t ssm_gated_scan_fwd_workspace_bytes(int batch, int dim, int64_t seqlen, in
  *                                                              with i, and for an empty sequence
  *   dz           out  (batch, dim, seqlen), dtype              required when z is given
  *   dh0          out  (batch, dim) float32                     NULL -> not written
- *   workspace    at least ssm_gated_scan_bwd_workspace_bytes(...) bytes, as above
+ *   workspace    at least ssm_gated_scan_bwd_workspace_bytes(...) bytes,
+ *                256-byte aligned, owned by the caller (NULL where the query
+ *                returns 0); calls sharing one workspace must not overlap
  * The sums over batch and steps have a fixed order.  batch == 0 or
  * seqlen == 0 writes zeros to dA and the bias gradients, and dh0 = dlast_state
  * (or zeros).

@@ -47,7 +47,9 @@ extern "C" {
  *   sum_out      out  required with residual, refused (SSM_ERR_NULL) without; must
  *                     overlap no other buffer of the call
  *   mean, rstd   out  NULL -> not written
- *   batch, seqlen >= 0, seqlen at most 2^31 - 4097; dim >= 1 (SSM_ERR_SHAPE otherwise).
+ *   batch, seqlen >= 0, seqlen at most 2^31 - 4097; dim >= 1; batch * seqlen at
+ *   most 2^31 - 4097 where seqlen < 8 or a row has 2^31 bytes, batch * seqlen / 8
+ *   elsewhere (SSM_ERR_SHAPE otherwise).
  */
 int ssm_layer_norm_fwd(const void* x, const void* residual, const float* weight, const float* bias,
                        float eps, void* y, void* sum_out, float* mean, float* rstd, int batch,

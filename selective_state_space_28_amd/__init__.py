@@ -31,9 +31,8 @@ from __future__ import annotations
 
 from ._lib import SSM_BF16, SSM_F32, SsmError, header_functions, load, status_string  # noqa: F401
 from .layers import (ssm_gated_scan_bwd, ssm_gated_scan_bwd_workspace_bytes,  # noqa: F401
-                     ssm_gated_scan_ckpt_bytes, ssm_gated_scan_fwd, ssm_gated_scan_fwd_workspace_bytes,
-                     ssm_gated_state_update, ssm_layer_norm_bwd, ssm_layer_norm_bwd_workspace_bytes,
-                     ssm_layer_norm_fwd)
+                     ssm_gated_scan_ckpt_bytes, ssm_gated_scan_fwd, ssm_gated_state_update, ssm_layer_norm_bwd,
+                     ssm_layer_norm_bwd_workspace_bytes, ssm_layer_norm_fwd)
 from .ops import (ssm_conv_scan_fwd, ssm_conv_state_update, ssm_scan_bwd,  # noqa: F401
                   ssm_scan_bwd_ckpt, ssm_scan_bwd_ckpt_workspace_bytes, ssm_scan_bwd_workspace_bytes,
                   ssm_scan_ckpt_bytes, ssm_scan_fwd, ssm_scan_fwd_ckpt, ssm_scan_fwd_noalloc,
@@ -45,7 +44,7 @@ __all__ = ["ssm_scan_fwd", "ssm_scan_fwd_noalloc", "ssm_scan_fwd_workspace_bytes
            "ssm_conv_scan_fwd", "ssm_conv_state_update", "ssm_scan_bwd",
            "ssm_scan_bwd_workspace_bytes", "ssm_scan_ckpt_bytes", "ssm_scan_fwd_ckpt",
            "ssm_scan_bwd_ckpt", "ssm_scan_bwd_ckpt_workspace_bytes", "ssm_ssd_scan_fwd", "ssm_ssd_scan_fwd_workspace_bytes",
-           "ssm_gated_scan_fwd", "ssm_gated_scan_fwd_workspace_bytes", "ssm_gated_scan_bwd",
-           "ssm_gated_scan_bwd_workspace_bytes", "ssm_gated_scan_ckpt_bytes", "ssm_gated_state_update",
+           "ssm_gated_scan_fwd", "ssm_gated_scan_bwd", "ssm_gated_scan_bwd_workspace_bytes",
+           "ssm_gated_scan_ckpt_bytes", "ssm_gated_state_update",
            "ssm_layer_norm_fwd", "ssm_layer_norm_bwd", "ssm_layer_norm_bwd_workspace_bytes",
            "ssm_status_string", "SsmError", "load"]

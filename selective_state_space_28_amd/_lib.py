@@ -79,12 +79,10 @@ def load():
         lib.ssm_scan_fwd_noalloc.restype = i32
     lib.ssm_gated_scan_ckpt_bytes.argtypes = [i32, i32, i64]
     lib.ssm_gated_scan_ckpt_bytes.restype = sz
-    lib.ssm_gated_scan_fwd_workspace_bytes.argtypes = [i32, i32, i64, i32]
-    lib.ssm_gated_scan_fwd_workspace_bytes.restype = sz
     lib.ssm_gated_scan_bwd_workspace_bytes.argtypes = [i32, i32, i64, i32]
     lib.ssm_gated_scan_bwd_workspace_bytes.restype = sz
     lib.ssm_gated_scan_fwd.argtypes = [vp, vp, fp, fp, vp, fp, vp, i32, vp, fp, vp, fp, fp, sz,
-                                       i32, i32, i64, i32, vp, sz, vp]
+                                       i32, i32, i64, i32, vp]
     lib.ssm_gated_scan_fwd.restype = i32
     lib.ssm_gated_scan_bwd.argtypes = [vp, vp, fp, fp, vp, fp, vp, i32, vp, fp, sz, vp, fp, vp, vp, fp,
                                        fp, vp, fp, vp, fp, i32, i32, i64, i32, vp, sz, vp]

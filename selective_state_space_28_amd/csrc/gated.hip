@@ -56,7 +56,7 @@ __device__ __forceinline__ Place<W> place_of(const GatedSizes& p) {
   Place<W> q;
   if constexpr (W == 0) {
     q.lane = lane & (p.lanes - 1);
-    q.row = (int)((blockIdx.x * group_waves(W) * 64 + threadIdx.x) / (unsigned)p.lanes);
+    q.row = (int)(blockIdx.x * (group_waves(W) * 64u / p.lanes) + threadIdx.x / p.lanes);
     q.live = q.row < p.rows;
     if (!q.live) q.row = 0;
     q.w0 = 0;

@@ -26,7 +26,7 @@ bool gate_flags_ok(int flags) { return (flags & ~(SSM_GATE_SOFTPLUS | SSM_GATE_U
 
 // Rows (b, d) are numbered in 32 bits.
 bool gated_shape_ok(int batch, int dim, int64_t seqlen) {
-  return shapes_fit(batch, dim, seqlen) && (int64_t)batch * dim <= INT_MAX - 64;
+  return shapes_fit(batch, dim, seqlen) && (int64_t)batch * dim <= INT_MAX - 512;
 }
 
 size_t gated_ckpt_bytes(int batch, int dim, int64_t seqlen) {
@@ -61,9 +61,12 @@ GatedLaunch gated_launch(const void* x, const void* r, const float* A, const flo
   return a;
 }
 
-// The norm numbers its tiles in 32 bits (of 8 steps and more).
+// The norm numbers its workgroups in 32 bits: tiles of 8 steps and more, or
+// tokens where a row has fewer or is too long for 32-bit offsets.
 bool norm_shape_ok(int batch, int dim, int64_t seqlen) {
-  return dim >= 1 && dim <= INT_MAX - 65536 && shapes_fit(batch, dim, seqlen) && (int64_t)batch * ((seqlen + 7) / 8) <= INT_MAX - 4096;
+  if (dim < 1 || dim > INT_MAX - 65536 || !shapes_fit(batch, dim, seqlen)) return false;
+  const bool by_token = seqlen < 8 || seqlen >= INT_MAX / 4;
+  return (int64_t)batch * (by_token ? seqlen : (seqlen + 7) / 8) <= INT_MAX - 4096;
 }
 
 size_t norm_bwd_ws_bytes(int batch, int dim, int64_t seqlen, int dtype) {
@@ -78,18 +81,10 @@ size_t ssm_gated_scan_ckpt_bytes(int batch, int dim, int64_t seqlen) {
   return gated_shape_ok(batch, dim, seqlen) ? gated_ckpt_bytes(batch, dim, seqlen) : 0;
 }
 
-size_t ssm_gated_scan_fwd_workspace_bytes(int batch, int dim, int64_t seqlen, int dtype) {
-  (void)batch;
-  (void)dim;
-  (void)seqlen;
-  (void)dtype;
-  return 0;
-}
-
 int ssm_gated_scan_fwd(const void* x, const void* r, const float* A, const float* r_bias, const void* i,
                        const float* i_bias, const void* z, int flags, const uint8_t* starts, const float* h0,
                        void* y, float* last_state, float* ckpt, size_t ckpt_bytes, int batch, int dim,
-                       int64_t seqlen, int dtype, void* workspace, size_t workspace_bytes, void* stream) {
+                       int64_t seqlen, int dtype, void* stream) {
   if (!dtype_ok(dtype)) return SSM_ERR_DTYPE;
   if (!gate_flags_ok(flags)) return SSM_ERR_FLAGS;
   if (!gated_shape_ok(batch, dim, seqlen)) return SSM_ERR_SHAPE;
@@ -98,16 +93,14 @@ int ssm_gated_scan_fwd(const void* x, const void* r, const float* A, const float
   const size_t es = (size_t)elem_bytes(dtype);
   if (!aligned(x, es) || !aligned(r, es) || !aligned(i, es) || !aligned(z, es) || !aligned(y, es) ||
       !aligned(A, 4) || !aligned(r_bias, 4) || !aligned(i_bias, 4) || !aligned(h0, 4) ||
-      !aligned(last_state, 4) || !aligned(ckpt, 4) || !aligned(workspace, 256))
+      !aligned(last_state, 4) || !aligned(ckpt, 4))
     return SSM_ERR_ALIGN;
   if (empty) return SSM_OK;
   const size_t ckb = ckpt != nullptr ? gated_ckpt_bytes(batch, dim, seqlen) : 0;
   if (ckpt_bytes < ckb) return SSM_ERR_WORKSPACE;
-  const size_t need = ssm_gated_scan_fwd_workspace_bytes(batch, dim, seqlen, dtype);
-  if (need > 0 && (workspace == nullptr || workspace_bytes < need)) return SSM_ERR_WORKSPACE;
   const size_t plane = (size_t)batch * (size_t)dim, tok = plane * (size_t)seqlen * es, ch = (size_t)dim * 4;
   {
-    const Span outs[] = {span(y, tok), span(last_state, plane * 4), span(ckpt, ckb), span(workspace, need)};
+    const Span outs[] = {span(y, tok), span(last_state, plane * 4), span(ckpt, ckb)};
     const Span ins[] = {span(x, tok), span(r, tok), span(i, tok), span(z, tok), span(A, ch),
                         span(r_bias, ch), span(i_bias, i != nullptr ? ch : 0),
                         span(starts, (size_t)batch * (size_t)seqlen), span(h0, plane * 4)};

@@ -119,10 +119,6 @@ def _sizes3(x, name="x"):
     return shape
 
 
-def ssm_gated_scan_fwd_workspace_bytes(batch: int, dim: int, seqlen: int, dtype: torch.dtype) -> int:
-    return int(load().ssm_gated_scan_fwd_workspace_bytes(batch, dim, seqlen, _DTYPES[dtype]))
-
-
 def ssm_gated_scan_bwd_workspace_bytes(batch: int, dim: int, seqlen: int, dtype: torch.dtype) -> int:
     return int(load().ssm_gated_scan_bwd_workspace_bytes(batch, dim, seqlen, _DTYPES[dtype]))
 
@@ -133,7 +129,7 @@ def ssm_gated_scan_ckpt_bytes(batch: int, dim: int, seqlen: int) -> int:
 
 def ssm_gated_scan_fwd(x, r, A, r_bias=None, i=None, i_bias=None, z=None, *, gate="sigmoid",
                        weight="unit", starts=None, h0=None, return_last_state=False,
-                       return_ckpt=False, out=None, workspace=None):
+                       return_ckpt=False, out=None):
     """The gated recurrence h = a h + w sigmoid(i) x, a = exp(A g(r)), over
     (batch, dim, L) inputs; see include/ssm_gated.h.
 
@@ -155,9 +151,8 @@ def ssm_gated_scan_fwd(x, r, A, r_bias=None, i=None, i_bias=None, z=None, *, gat
     py = _in("out", y, shape, x.dtype, dev)
     last = torch.empty((batch, dim), dtype=_F32, device=dev) if return_last_state else None
     ckpt = torch.empty((batch, -(-L // CKPT_STEPS), dim), dtype=_F32, device=dev) if return_ckpt else None
-    workspace, ws_bytes = _workspace(workspace, lib.ssm_gated_scan_fwd_workspace_bytes(batch, dim, L, code), dev)
     _call(lib.ssm_gated_scan_fwd, "ssm_gated_scan_fwd", dev, *ins, flags, ps, p0, py, _ptr(last), _ptr(ckpt),
-          ckpt.numel() * 4 if return_ckpt else 0, batch, dim, L, code, _ptr(workspace), ws_bytes)
+          ckpt.numel() * 4 if return_ckpt else 0, batch, dim, L, code)
     res = (y,)
     if return_last_state:
         res += (last,)

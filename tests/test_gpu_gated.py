@@ -179,26 +179,37 @@ def test_packed_rows_are_their_sequences(dev):
 
 
 @pytest.mark.parametrize("bad", [np.inf, -np.inf, np.nan])
-@pytest.mark.parametrize("at", [3, 700])
-def test_nothing_crosses_a_start(dev, bad, at):
-    """A non-finite input stays in its channel and its sequence, forward and backward."""
-    p = case("f32", 2, 5, 1300, 9, h0=False)
-    p["starts"] = np.zeros((2, 1300), np.uint8)
-    p["starts"][:, [0, 600, 640, 1100]] = 1
+@pytest.mark.parametrize("b,d,L,cuts,at", [(2, 5, 1300, (0, 600, 640, 1100), 3), (2, 5, 1300, (0, 600, 640, 1100), 700),
+                                           (2, 5, 17000, (0, 8000, 16999), 7000), (2, 4200, 600, (0, 100, 520), 130),
+                                           (2, 5, 100, (0, 50, 64, 90), 70), (3, 7, 33, (0,), 20), (2, 9, 6, (), 2)])
+def test_nothing_crosses_a_start(dev, bad, b, d, L, cuts, at):
+    """A non-finite input stays in its channel and its sequence, forward and backward: with a row to 16 waves, 4 and
+    one, and rows that share a wave."""
+    p = case("f32", b, d, L, 9, h0=False)
+    p["starts"] = np.zeros((b, L), np.uint8)
+    p["starts"][:, list(cuts)] = 1
     clean = check(p, dev)
     p["x"][1, 2, at] = bad
     t = put(p, dev)
     y, last, ckpt = run_fwd(t, "sigmoid", "unit")
-    end = 600 if at < 600 else 1100
-    first = 0 if at < 600 else 640
+    end = min([c for c in cuts if c > at] + [L])
+    first = max([c for c in cuts if c <= at] + [0])
     got = np64(y)
     assert not np.isfinite(got[1, 2, at:end]).any()
     got[1, 2, at:end] = np64(clean[0])[1, 2, at:end]
-    assert np.array_equal(got, np64(clean[0])) and np.array_equal(np64(last), np64(clean[1]))
+    assert np.array_equal(got, np64(clean[0]))
+    got, want = np64(last), np64(clean[1])
+    if end == L:
+        got[1, 2] = want[1, 2]
+    assert np.array_equal(got, want)
     g = run_bwd(t, ckpt, "sigmoid", "unit")
     for k in ("dx", "dr", "di", "dz"):
         v, c = np64(g[k]), np64(clean[3][k])
         v[1, 2, first:end], c[1, 2, first:end] = 0, 0
+        assert np.array_equal(v, c), k
+    for k in ("dA", "dr_bias", "di_bias"):
+        v, c = np64(g[k]), np64(clean[3][k])
+        v[2], c[2] = 0, 0
         assert np.array_equal(v, c), k
 
 

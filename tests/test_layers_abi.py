@@ -23,8 +23,8 @@ def at(k):
 
 def test_exports_every_declared_symbol():
     gated, norm = header_functions("ssm_gated.h"), header_functions("ssm_norm.h")
-    assert set(gated) == {"ssm_gated_scan_ckpt_bytes", "ssm_gated_scan_fwd", "ssm_gated_scan_fwd_workspace_bytes",
-                          "ssm_gated_scan_bwd", "ssm_gated_scan_bwd_workspace_bytes", "ssm_gated_state_update"}
+    assert set(gated) == {"ssm_gated_scan_ckpt_bytes", "ssm_gated_scan_fwd", "ssm_gated_scan_bwd",
+                          "ssm_gated_scan_bwd_workspace_bytes", "ssm_gated_state_update"}
     assert set(norm) == {"ssm_layer_norm_fwd", "ssm_layer_norm_bwd", "ssm_layer_norm_bwd_workspace_bytes"}
     lib = ctypes.CDLL(load()._name)
     for n in gated + norm:
@@ -37,11 +37,11 @@ N = 2 * 64 * 2048 * 2  # bytes of x
 
 def _fwd(**kw):
     a = dict(x=at(0), r=at(1), A=at(2), rb=None, i=None, ib=None, z=None, fl=0, st=None, h0=None, y=at(3),
-             last=None, ck=None, ckb=0, batch=2, dim=64, L=2048, dtype=1, ws=None, wsb=0)
+             last=None, ck=None, ckb=0, batch=2, dim=64, L=2048, dtype=1)
     a.update(kw)
     return load().ssm_gated_scan_fwd(a["x"], a["r"], a["A"], a["rb"], a["i"], a["ib"], a["z"], a["fl"], a["st"],
                                      a["h0"], a["y"], a["last"], a["ck"], a["ckb"], a["batch"], a["dim"],
-                                     a["L"], a["dtype"], a["ws"], a["wsb"], None)
+                                     a["L"], a["dtype"], None)
 
 
 @pytest.mark.parametrize("kw,code", [
@@ -51,7 +51,7 @@ def _fwd(**kw):
     (dict(x=None), NULL), (dict(r=None), NULL), (dict(A=None), NULL), (dict(y=None), NULL),
     (dict(x=at(0) + 1), ALIGN), (dict(dtype=0, r=at(1) + 2), ALIGN), (dict(A=at(2) + 2), ALIGN),
     (dict(rb=at(4) + 1), ALIGN), (dict(h0=at(4) + 2), ALIGN), (dict(last=at(4) + 1), ALIGN),
-    (dict(ck=at(4) + 1, ckb=CK), ALIGN), (dict(ws=at(4) + 16), ALIGN), (dict(ck=at(4), ckb=CK - 1), WS),
+    (dict(ck=at(4) + 1, ckb=CK), ALIGN), (dict(ck=at(4), ckb=CK - 1), WS),
     (dict(y=at(0)), ALIAS), (dict(y=at(1) + N - 2), ALIAS), (dict(i=at(3) + 64), ALIAS), (dict(z=at(3)), ALIAS),
     (dict(last=at(3) + 4), ALIAS), (dict(last=at(2)), ALIAS), (dict(h0=at(4), last=at(4) + 8), ALIAS),
     (dict(ck=at(4), ckb=CK, last=at(4) + CK - 4), ALIAS), (dict(st=at(3) + 128), ALIAS),
@@ -118,7 +118,7 @@ def _nf(**kw):
 @pytest.mark.parametrize("kw,code", [
     (dict(dtype=2), DTYPE), (dict(dim=0), SHAPE), (dict(dim=-1), SHAPE), (dict(batch=-1), SHAPE), (dict(L=-1), SHAPE),
     (dict(eps=-1e-6), SHAPE), (dict(eps=float("nan")), SHAPE), (dict(eps=float("inf")), SHAPE),
-    (dict(batch=(1 << 31) - 1), SHAPE),
+    (dict(batch=(1 << 31) - 1), SHAPE), (dict(batch=1 << 29, L=7, dim=1), SHAPE), (dict(batch=4, L=1 << 30), SHAPE),
     (dict(x=None), NULL), (dict(w=None), NULL), (dict(y=None), NULL), (dict(res=at(3)), NULL), (dict(so=at(3)), NULL),
     (dict(x=at(0) + 1), ALIGN), (dict(w=at(1) + 2), ALIGN), (dict(m=at(4) + 2), ALIGN),
     (dict(y=at(0)), ALIAS), (dict(y=at(1)), ALIAS), (dict(res=at(3), so=at(3)), ALIAS), (dict(res=at(3), so=at(0)), ALIAS),
