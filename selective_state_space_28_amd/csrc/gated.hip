@@ -71,11 +71,78 @@ __device__ __forceinline__ Place<W> place_of(const GatedSizes& p) {
   return q;
 }
 
-// bf16 results are written past the caches: a wave's access is 1 KiB in one
-// piece (float32's two leave half lines between them; batch 8, dim 1536, L 2048
-// float32, backward: 198 us so against 178).
-template <typename T>
-constexpr bool kStoreOnce = sizeof(T) == 2;
+// The steps that a lane holds of its wave's block: kRun in a row for bf16, one
+// access of 16 bytes.  For float32 that would be two accesses with gaps of 16
+// bytes between the lanes; the block is taken as two halves instead, 4 steps of
+// each to a lane, so that every access of a wave is 1 KiB in one piece, and the
+// prefix runs once for each half.  (Rows that share a wave keep kRun in a row.)
+template <typename T, int W>
+struct Steps {
+  static constexpr int NH = sizeof(T) == 4 && W > 0 ? 2 : 1;
+  static constexpr int RN = kRun / NH;          // steps of a run
+  static constexpr int kGap = kGatedBlock / NH;  // from a lane's run to its next
+
+  // steps 0 .. RN-1 at p and (halves) at p + kGap, `left` steps from p to the row's end
+  template <bool ONCE>
+  __device__ __forceinline__ static RunWords<T> load(const T* p, int64_t left) {
+    if constexpr (NH == 1) {
+      return load_run<T, ONCE>(p, clamped(left));
+    } else {
+      RunWords<T> r;
+#pragma unroll
+      for (int h = 0; h < NH; ++h) {
+        const T* q = p + h * kGap;
+        const int valid = clamped(left - h * kGap);
+        if (valid >= RN) {
+          const auto* at = reinterpret_cast<const typename RunWords<T>::vec4*>(q);
+          const auto v = ONCE ? __builtin_nontemporal_load(at) : *at;
+          r.w[4 * h] = v.x; r.w[4 * h + 1] = v.y; r.w[4 * h + 2] = v.z; r.w[4 * h + 3] = v.w;
+        } else {
+#pragma unroll
+          for (int k = 0; k < RN; ++k) r.w[4 * h + k] = k < valid ? __float_as_uint(q[k]) : 0u;
+        }
+      }
+      return r;
+    }
+  }
+  __device__ __forceinline__ static void store(T* p, int64_t left, const float (&f)[kRun]) {
+    if constexpr (NH == 1) {
+      store_run<T, sizeof(T) == 2>(p, clamped(left), f);
+    } else {
+#pragma unroll
+      for (int h = 0; h < NH; ++h) {
+        T* q = p + h * kGap;
+        const int valid = clamped(left - h * kGap);
+        if (valid >= RN) {
+          typename RunWords<T>::vec4 v;
+          v.x = __float_as_uint(f[4 * h]); v.y = __float_as_uint(f[4 * h + 1]);
+          v.z = __float_as_uint(f[4 * h + 2]); v.w = __float_as_uint(f[4 * h + 3]);
+          __builtin_nontemporal_store(v, reinterpret_cast<typename RunWords<T>::vec4*>(q));
+        } else {
+#pragma unroll
+          for (int k = 0; k < RN; ++k)
+            if (k < valid) q[k] = f[4 * h + k];
+        }
+      }
+    }
+  }
+  // bit k: a sequence starts at the lane's step k
+  __device__ __forceinline__ static uint32_t starts(const uint8_t* p, int64_t left) {
+    if constexpr (NH == 1) {
+      return load_starts<kRun>(p, clamped(left));
+    } else {
+      return load_starts<RN>(p, clamped(left)) | load_starts<RN>(p + kGap, clamped(left - kGap)) << RN;
+    }
+  }
+  // bit k: the lane's step k is in the row
+  __device__ __forceinline__ static uint32_t inside(int64_t left) {
+    uint32_t m = 0;
+#pragma unroll
+    for (int h = 0; h < NH; ++h) m |= ((1u << clamped(left - h * kGap)) - 1u) << (h * RN);
+    return m;
+  }
+  __device__ __forceinline__ static int clamped(int64_t left) { return left >= RN ? RN : left < 0 ? 0 : (int)left; }
+};
 
 // A wave's total map, for the other waves of its row; two buffers, so that one
 // barrier for every W blocks is enough.
@@ -124,6 +191,8 @@ __global__ __launch_bounds__(64 * group_waves(W)) void gated_fwd_kernel(
     const float* __restrict__ r_bias, const T* __restrict__ ig, const float* __restrict__ i_bias,
     const T* __restrict__ z, const uint8_t* __restrict__ starts, const float* __restrict__ h0,
     T* __restrict__ y, float* __restrict__ last_state, float* __restrict__ ckpt, const GatedSizes p) {
+  using ST = Steps<T, W>;
+  constexpr int NH = ST::NH, RN = ST::RN;
   [[maybe_unused]] __shared__ RowMaps<W> maps;
   const Place<W> at = place_of<W>(p);
   if (W > 0 && !at.live) return;
@@ -140,68 +209,77 @@ __global__ __launch_bounds__(64 * group_waves(W)) void gated_fwd_kernel(
   auto blocks = [&](int b0, int turn, auto whole, auto once) {
     constexpr bool WHOLE = decltype(whole)::value, ONCE = decltype(once)::value;
     const int blk = b0 + w0;  // past the last block: no steps, the identity
-    const int64_t t0 = (int64_t)blk * kGatedBlock + lane * kRun;
-    const int64_t left = at.live ? p.seqlen - t0 : 0;
-    const int valid = WHOLE || left > kRun ? kRun : (int)(left < 0 ? 0 : left);  // steps of this lane's run
-    const RunWords<T> wr = load_run<T, ONCE>(r + base + t0, valid), wx = load_run<T, ONCE>(x + base + t0, valid);
+    const int64_t t0 = (int64_t)blk * kGatedBlock + lane * RN;
+    const int64_t left = WHOLE ? kGatedBlock : at.live ? p.seqlen - t0 : 0;
+    const RunWords<T> wr = ST::template load<ONCE>(r + base + t0, left), wx = ST::template load<ONCE>(x + base + t0, left);
     RunWords<T> wi, wz;
-    if constexpr (IG) wi = load_run<T, ONCE>(ig + base + t0, valid);
-    if constexpr (ZG) wz = load_run<T, ONCE>(z + base + t0, valid);
+    if constexpr (IG) wi = ST::template load<ONCE>(ig + base + t0, left);
+    if constexpr (ZG) wz = ST::template load<ONCE>(z + base + t0, left);
     uint32_t cut = 0;
-    if (starts != nullptr) cut = load_starts(starts + (int64_t)b * p.seqlen + t0, valid);
+    if (starts != nullptr) cut = ST::starts(starts + (int64_t)b * p.seqlen + t0, left);
+    const uint32_t in = WHOLE ? ~0u : ST::inside(left);
 
     float fr[kRun], fx[kRun], fi[kRun], a[kRun], q[kRun];
     run_floats<T>(wr, fr);
     run_floats<T>(wx, fx);
     if constexpr (IG) run_floats<T>(wi, fi);
-    float S = 0.0f;  // exponent of the run's decay
+    float S[NH];  // exponent of a run's decay
+#pragma unroll
+    for (int h = 0; h < NH; ++h) S[h] = 0.0f;
 #pragma unroll
     for (int k = 0; k < kRun; ++k) {
       const Gate g = gate_of<RULE>(gate_value<RULE>(fr[k], rb, nrb), A2);
       a[k] = g.a;
       q[k] = g.w * fx[k];
       if constexpr (IG) q[k] *= sigmoid_f32(fi[k], nib);
-      if (!WHOLE && k >= valid) {
+      if (!WHOLE && !(in & (1u << k))) {
         a[k] = 1.0f;
         q[k] = 0.0f;
       } else {
-        S += g.e2;
+        S[k / RN] += g.e2;
       }
     }
-    float P = __builtin_fmaxf(exp2_hw(S), kMinNormal), Q = 0.0f, h, h_in;
-    if (W == 0 || starts != nullptr) {
+    float h_in;
+    auto rerun = [&](auto cuts) {
+      constexpr bool CUT = decltype(cuts)::value;
+      float P[NH], Q[NH];
 #pragma unroll
-      for (int k = 0; k < kRun; ++k) {
-        if (cut & (1u << k)) a[k] = 0.0f;
-        Q = apply_map<true>(a[k], q[k], Q);
+      for (int h = 0; h < NH; ++h) {
+        P[h] = __builtin_fmaxf(exp2_hw(S[h]), kMinNormal);
+        Q[h] = 0.0f;
+#pragma unroll
+        for (int k = h * RN; k < (h + 1) * RN; ++k) {
+          if (CUT && (cut & (1u << k))) a[k] = 0.0f;
+          Q[h] = apply_map<CUT>(a[k], q[k], Q[h]);
+        }
+        if (CUT && (cut >> (h * RN) & ((1u << RN) - 1u)) != 0) P[h] = 0.0f;
+        if (W == 0 && lane == 0) {
+          Q[h] = apply_map<true>(P[h], Q[h], H);
+          P[h] = 0.0f;
+        }
+        wave_prefix<CUT>(P[h], Q[h]);
       }
-      if (cut != 0) P = 0.0f;
-      if (W == 0 && lane == 0) {
-        Q = apply_map<true>(P, Q, H);
-        P = 0.0f;
+      float Pt = P[0], Qt = Q[0];
+      if constexpr (NH == 2) {
+        Pt = P[1], Qt = Q[1];
+        compose_map<CUT>(Pt, Qt, P[0], Q[0]);
       }
-      wave_prefix<true>(P, Q);
-      h_in = through_waves<true, W, false>(maps, turn, w0, P, Q, H);
-      const float end = apply_map<true>(P, Q, h_in);
-      h = lane_before(end, h_in);
-      if constexpr (W == 1) H = lane_value(end, 63);
-      if constexpr (W == 0) {
-        if (lane == 0) h = H;
-        H = end;
+      h_in = through_waves<CUT, W, false>(maps, turn, w0, Pt, Qt, H);
+      float from = h_in;
+#pragma unroll
+      for (int h = 0; h < NH; ++h) {
+        const float end = apply_map<CUT>(P[h], Q[h], from);
+        float v = lane_before(end, from);
+        if (W == 0 && lane == 0) v = H;
+        if constexpr (W == 0) H = end;
+        else from = lane_value(end, 63);
+#pragma unroll
+        for (int k = h * RN; k < (h + 1) * RN; ++k) q[k] = v = apply_map<CUT>(a[k], q[k], v);
       }
-#pragma unroll
-      for (int k = 0; k < kRun; ++k) q[k] = h = apply_map<true>(a[k], q[k], h);
-    } else {
-#pragma unroll
-      for (int k = 0; k < kRun; ++k) Q = __builtin_fmaf(a[k], Q, q[k]);
-      wave_prefix<false>(P, Q);
-      h_in = through_waves<false, W, false>(maps, turn, w0, P, Q, H);
-      const float end = __builtin_fmaf(P, h_in, Q);
-      h = lane_before(end, h_in);
-      if constexpr (W == 1) H = lane_value(end, 63);
-#pragma unroll
-      for (int k = 0; k < kRun; ++k) q[k] = h = __builtin_fmaf(a[k], h, q[k]);
-    }
+      if constexpr (W == 1) H = from;
+    };
+    if (W == 0 || starts != nullptr) rerun(BoolC<true>{});
+    else rerun(BoolC<false>{});
     if (ckpt != nullptr && lane == 0 && at.live && blk < p.nblk)
       ckpt[((int64_t)b * p.nblk + blk) * p.dim + d] = h_in;
     if constexpr (ZG) {
@@ -210,7 +288,7 @@ __global__ __launch_bounds__(64 * group_waves(W)) void gated_fwd_kernel(
 #pragma unroll
       for (int k = 0; k < kRun; ++k) q[k] *= silu_f32(fz[k]);
     }
-    store_run<T, kStoreOnce<T>>(y + base + t0, valid, q);
+    ST::store(y + base + t0, left, q);
   };
   if constexpr (W == 0) {
     blocks(0, 0, BoolC<false>{}, BoolC<false>{});
@@ -219,9 +297,7 @@ __global__ __launch_bounds__(64 * group_waves(W)) void gated_fwd_kernel(
     auto wholes = [&](auto once) {
       for (; (int64_t)(b0 + W) * kGatedBlock <= p.seqlen; b0 += W, turn ^= 1) blocks(b0, turn, BoolC<true>{}, once);
     };
-    if constexpr (kStoreOnce<T>) {
-      if (p.once) wholes(BoolC<true>{});
-    }
+    if (p.once) wholes(BoolC<true>{});
     wholes(BoolC<false>{});
     if (b0 < p.nblk) blocks(b0, turn, BoolC<false>{}, BoolC<false>{});
   }
@@ -236,6 +312,8 @@ __global__ __launch_bounds__(64 * group_waves(W)) void gated_bwd_kernel(
     const T* __restrict__ dy, const float* __restrict__ dlast, T* __restrict__ dx, T* __restrict__ dr,
     T* __restrict__ di, T* __restrict__ dz, float* __restrict__ row_dA, float* __restrict__ row_drb,
     float* __restrict__ row_dib, float* __restrict__ dh0, const GatedSizes p) {
+  using ST = Steps<T, W>;
+  constexpr int NH = ST::NH, RN = ST::RN;
   [[maybe_unused]] __shared__ RowMaps<W> maps;
   const Place<W> at = place_of<W>(p);
   if (W > 0 && !at.live) return;
@@ -252,17 +330,17 @@ __global__ __launch_bounds__(64 * group_waves(W)) void gated_bwd_kernel(
   auto blocks = [&](int b0, int turn, auto whole, auto once) {
     constexpr bool WHOLE = decltype(whole)::value, ONCE = decltype(once)::value;
     const int blk = b0 + w0;  // past the last block: no steps, the identity
-    const int64_t t0 = (int64_t)blk * kGatedBlock + lane * kRun;
-    const int64_t left = at.live ? p.seqlen - t0 : 0;
-    const int valid = WHOLE || left > kRun ? kRun : (int)(left < 0 ? 0 : left);
-    const RunWords<T> wr = load_run<T, ONCE>(r + base + t0, valid), wx = load_run<T, ONCE>(x + base + t0, valid);
+    const int64_t t0 = (int64_t)blk * kGatedBlock + lane * RN;
+    const int64_t left = WHOLE ? kGatedBlock : at.live ? p.seqlen - t0 : 0;
+    const RunWords<T> wr = ST::template load<ONCE>(r + base + t0, left), wx = ST::template load<ONCE>(x + base + t0, left);
     RunWords<T> wi, wz;
-    if constexpr (IG) wi = load_run<T, ONCE>(ig + base + t0, valid);
-    if constexpr (ZG) wz = load_run<T, ONCE>(z + base + t0, valid);
-    const RunWords<T> wd = load_run<T, ONCE>(dy + base + t0, valid);
+    if constexpr (IG) wi = ST::template load<ONCE>(ig + base + t0, left);
+    if constexpr (ZG) wz = ST::template load<ONCE>(z + base + t0, left);
+    const RunWords<T> wd = ST::template load<ONCE>(dy + base + t0, left);
     const bool packed = W == 0 || starts != nullptr;
     uint32_t cut = 0;
-    if (starts != nullptr) cut = load_starts(starts + (int64_t)b * p.seqlen + t0, valid);
+    if (starts != nullptr) cut = ST::starts(starts + (int64_t)b * p.seqlen + t0, left);
+    const uint32_t in = WHOLE ? ~0u : ST::inside(left);
     const float H = WHOLE || blk < p.nblk ? ckpt[((int64_t)b * p.nblk + blk) * p.dim + d] : 0.0f;
 
     // g of each step, A dg/dr, the input gate and its complement
@@ -271,7 +349,9 @@ __global__ __launch_bounds__(64 * group_waves(W)) void gated_bwd_kernel(
     run_floats<T>(wx, fx);
     run_floats<T>(wd, dh);
     if constexpr (IG) run_floats<T>(wi, gi);
-    float S = 0.0f;
+    float S[NH];
+#pragma unroll
+    for (int h = 0; h < NH; ++h) S[h] = 0.0f;
 #pragma unroll
     for (int k = 0; k < kRun; ++k) {
       float v, slope;
@@ -292,48 +372,49 @@ __global__ __launch_bounds__(64 * group_waves(W)) void gated_bwd_kernel(
         sigmoid_pair(gi[k], nib, gi[k], ci[k]);
         q[k] *= gi[k];
       }
-      if (!WHOLE && k >= valid) {
+      if (!WHOLE && !(in & (1u << k))) {
         a[k] = 1.0f;
         q[k] = 0.0f;
         g[k] = 0.0f;   // nothing is added to dA,
         sA_[k] = 0.0f;  // nor to dr_bias (x and so di are 0 already)
       } else {
-        S += t.e2;
+        S[k / RN] += t.e2;
       }
     }
-    const float P = cut != 0 ? 0.0f : __builtin_fmaxf(exp2_hw(S), kMinNormal);
+    float P[NH];
+#pragma unroll
+    for (int h = 0; h < NH; ++h)
+      P[h] = (cut >> (h * RN) & ((1u << RN) - 1u)) != 0 ? 0.0f : __builtin_fmaxf(exp2_hw(S[h]), kMinNormal);
 
     // the states: hb[k] before step k (0 at a start), q[k] after it
     float hb[kRun];
-    {
-      float Pf = P, Q = 0.0f, h;
-      if (packed) {
+    auto rerun = [&](auto cuts) {
+      constexpr bool CUT = decltype(cuts)::value;
+      float from = H;
 #pragma unroll
-        for (int k = 0; k < kRun; ++k) Q = apply_map<true>((cut & (1u << k)) ? 0.0f : a[k], q[k], Q);
+      for (int h = 0; h < NH; ++h) {
+        float Pf = P[h], Q = 0.0f;
+#pragma unroll
+        for (int k = h * RN; k < (h + 1) * RN; ++k)
+          Q = apply_map<CUT>(CUT && (cut & (1u << k)) ? 0.0f : a[k], q[k], Q);
         if (W == 0 && lane == 0) {
-          Q = apply_map<true>(Pf, Q, H);
+          Q = apply_map<true>(Pf, Q, from);
           Pf = 0.0f;
         }
-        wave_prefix<true>(Pf, Q);
-        h = lane_before(apply_map<true>(Pf, Q, H), H);
-        if (W == 0 && lane == 0) h = H;
+        wave_prefix<CUT>(Pf, Q);
+        const float end = apply_map<CUT>(Pf, Q, from);
+        float v = lane_before(end, from);
+        if (W == 0 && lane == 0) v = from;
+        if constexpr (NH > 1) from = lane_value(end, 63);
 #pragma unroll
-        for (int k = 0; k < kRun; ++k) {
-          hb[k] = (cut & (1u << k)) ? 0.0f : h;
-          q[k] = h = __builtin_fmaf(a[k], hb[k], q[k]);
-        }
-      } else {
-#pragma unroll
-        for (int k = 0; k < kRun; ++k) Q = __builtin_fmaf(a[k], Q, q[k]);
-        wave_prefix<false>(Pf, Q);
-        h = lane_before(__builtin_fmaf(Pf, H, Q), H);
-#pragma unroll
-        for (int k = 0; k < kRun; ++k) {
-          hb[k] = h;
-          q[k] = h = __builtin_fmaf(a[k], h, q[k]);
+        for (int k = h * RN; k < (h + 1) * RN; ++k) {
+          hb[k] = CUT && (cut & (1u << k)) ? 0.0f : v;
+          q[k] = v = __builtin_fmaf(a[k], hb[k], q[k]);
         }
       }
-    }
+    };
+    if (packed) rerun(BoolC<true>{});
+    else rerun(BoolC<false>{});
 
     // the output gate: dz, and dh = dy silu(z)
     if constexpr (ZG) {
@@ -347,40 +428,42 @@ __global__ __launch_bounds__(64 * group_waves(W)) void gated_bwd_kernel(
         o[k] = ds * q[k] * __builtin_fmaf(fz[k], c, 1.0f);
         dh[k] = ds * fz[k];
       }
-      store_run<T, kStoreOnce<T>>(dz + base + t0, valid, o);
+      ST::store(dz + base + t0, left, o);
     }
 
-    // the adjoint entering the run from the right
-    float m;
-    {
-      float Q = 0.0f;
-      if (packed) {
-#pragma unroll
-        for (int k = kRun - 1; k >= 0; --k) Q = (cut & (1u << k)) ? 0.0f : a[k] * (dh[k] + Q);
-      } else {
-#pragma unroll
-        for (int k = kRun - 1; k >= 0; --k) Q = a[k] * (dh[k] + Q);
-      }
-      // in a shared wave the row's last lane applies its map to what enters
-      if (W == 0 && at.last) Q = apply_map<true>(P, Q, M);
+    // the adjoint entering each run from the right: the runs of the last half
+    // first, lanes mirrored
+    float m_run[NH];
+    auto back = [&](auto cuts) {
+      constexpr bool CUT = decltype(cuts)::value;
       const int place = threadIdx.x & 63;
-      float Pr = lane_mirror(W == 0 && at.last ? 0.0f : P, place), Qr = lane_mirror(Q, place), end, m_in;
-      if (packed) {
-        wave_prefix<true>(Pr, Qr);
-        m_in = through_waves<true, W, true>(maps, turn, w0, Pr, Qr, M);
-        end = apply_map<true>(Pr, Qr, m_in);
-      } else {
-        wave_prefix<false>(Pr, Qr);
-        m_in = through_waves<false, W, true>(maps, turn, w0, Pr, Qr, M);
-        end = __builtin_fmaf(Pr, m_in, Qr);
+      float Pr[NH], Qr[NH];
+#pragma unroll
+      for (int h = 0; h < NH; ++h) {
+        float Q = 0.0f;
+#pragma unroll
+        for (int k = (h + 1) * RN - 1; k >= h * RN; --k) Q = CUT && (cut & (1u << k)) ? 0.0f : a[k] * (dh[k] + Q);
+        // in a shared wave the row's last lane applies its map to what enters
+        if (W == 0 && at.last) Q = apply_map<true>(P[h], Q, M);
+        Pr[h] = lane_mirror(W == 0 && at.last ? 0.0f : P[h], place);
+        Qr[h] = lane_mirror(Q, place);
+        wave_prefix<CUT>(Pr[h], Qr[h]);
       }
-      m = lane_mirror(lane_before(end, m_in), place);
-      if constexpr (W == 1) M = lane_value(end, 63);
-      if constexpr (W == 0) {
-        if (at.last) m = M;
-        M = lane_mirror(end, place);  // the first lane's goes to dh0
+      float Pt = Pr[0], Qt = Qr[0];
+      if constexpr (NH == 2) compose_map<CUT>(Pt, Qt, Pr[1], Qr[1]);
+      float from = through_waves<CUT, W, true>(maps, turn, w0, Pt, Qt, M);
+#pragma unroll
+      for (int h = NH - 1; h >= 0; --h) {
+        const float end = apply_map<CUT>(Pr[h], Qr[h], from);
+        m_run[h] = lane_mirror(lane_before(end, from), place);
+        if (W == 0 && at.last) m_run[h] = M;
+        if constexpr (W == 0) M = lane_mirror(end, place);  // the first lane's goes to dh0
+        else from = lane_value(end, 63);
       }
-    }
+      if constexpr (W == 1) M = from;
+    };
+    if (packed) back(BoolC<true>{});
+    else back(BoolC<false>{});
 
     // the gradients of each step, from the right; with u = x sigmoid(i)
     // de = lambda (a h_before - u (a or a^2/w)), the bracket's second term from
@@ -389,6 +472,7 @@ __global__ __launch_bounds__(64 * group_waves(W)) void gated_bwd_kernel(
     float pA = 0.0f, prb = 0.0f, pib = 0.0f;
 #pragma unroll
     for (int k = kRun - 1; k >= 0; --k) {
+      float& m = m_run[k / RN];
       const float lam = dh[k] + m;
       m = a[k] * lam;
       if (packed && (cut & (1u << k))) m = 0.0f;
@@ -406,9 +490,9 @@ __global__ __launch_bounds__(64 * group_waves(W)) void gated_bwd_kernel(
         pib += odi[k];
       }
     }
-    store_run<T, kStoreOnce<T>>(dx + base + t0, valid, odx);
-    store_run<T, kStoreOnce<T>>(dr + base + t0, valid, odr);
-    if constexpr (IG) store_run<T, kStoreOnce<T>>(di + base + t0, valid, odi);
+    ST::store(dx + base + t0, left, odx);
+    ST::store(dr + base + t0, left, odr);
+    if constexpr (IG) ST::store(di + base + t0, left, odi);
     sA += (double)pA;
     srb += (double)prb;
     if constexpr (IG) sib += (double)pib;
@@ -425,9 +509,7 @@ __global__ __launch_bounds__(64 * group_waves(W)) void gated_bwd_kernel(
     auto wholes = [&](auto once) {
       for (; b0 >= 0; b0 -= W, turn ^= 1) blocks(b0, turn, BoolC<true>{}, once);
     };
-    if constexpr (kStoreOnce<T>) {
-      if (p.once) wholes(BoolC<true>{});
-    }
+    if (p.once) wholes(BoolC<true>{});
     wholes(BoolC<false>{});
   }
 
@@ -526,17 +608,17 @@ int waves_of(const GatedLaunch& a) {
   return rows >= 2048 || nblk <= 4 ? 4 : 16;
 }
 
-// Whether inputs are read past the caches: bf16 rows of whole lines (others
+// Whether inputs are read past the caches: rows of whole lines (others
 // share lines between waves, which the caches then join) in a call whose tensors
 // are twice the 256 MiB that the last cache may hold.  Batch 16, dim 5120, L 2048:
 // 220 us so, 238 otherwise; batch 8, its backward: 201, 212; batch 4, dim 1000, L
 // 8000, 320 MB of tensors again and again: 61, 52.
 bool read_once(const GatedLaunch& a) {
   const int64_t streams = 3 + (a.i != nullptr) + (a.z != nullptr) + (a.dy != nullptr ? 2 + (a.i != nullptr) + (a.z != nullptr) : 0);
-  const int64_t bytes = (int64_t)a.batch * a.dim * a.seqlen * 2;
+  const int64_t row = a.seqlen * (a.dtype == Dtype::BF16 ? 2 : 4), bytes = (int64_t)a.batch * a.dim * row;
   auto lines = [](const void* p) { return reinterpret_cast<uintptr_t>(p) % 128 == 0; };
-  return a.dtype == Dtype::BF16 && a.seqlen % 64 == 0 && streams * bytes > (int64_t)512 << 20 && lines(a.x) &&
-         lines(a.r) && lines(a.i) && lines(a.z) && lines(a.dy);
+  return row % 128 == 0 && streams * bytes > (int64_t)512 << 20 && lines(a.x) && lines(a.r) && lines(a.i) &&
+         lines(a.z) && lines(a.dy);
 }
 
 GatedSizes sizes_of(const GatedLaunch& a) {

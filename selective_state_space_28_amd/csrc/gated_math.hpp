@@ -69,17 +69,28 @@ __device__ __forceinline__ Gate gate_of(float g, float A2) {
   return r;
 }
 
-// Bit k set where a sequence starts at step k of the run.
+// Bit k set where a sequence starts at step k of a run of N (8 or 4).
+template <int N>
 __device__ __forceinline__ uint32_t load_starts(const uint8_t* p, int valid) {
   typedef uint32_t vec2 __attribute__((ext_vector_type(2), aligned(1)));
+  typedef uint32_t word __attribute__((aligned(1)));
   uint32_t m = 0;
-  if (valid >= kRun) {
-    const vec2 v = *reinterpret_cast<const vec2*>(p);
+  if (valid >= N) {
+    uint32_t w[2] = {0u, 0u};
+    if constexpr (N == 8) {
+      const vec2 v = *reinterpret_cast<const vec2*>(p);
+      w[0] = v.x; w[1] = v.y;
+    } else {
+      w[0] = *reinterpret_cast<const word*>(p);
+    }
+    // (a bare "no start in the run" is the common answer)
+    if ((w[0] | w[1]) != 0) {
 #pragma unroll
-    for (int k = 0; k < kRun; ++k) m |= (((k < 4 ? v.x : v.y) >> (8 * (k & 3))) & 0xffu) != 0 ? 1u << k : 0u;
+      for (int k = 0; k < N; ++k) m |= ((w[k / 4] >> (8 * (k & 3))) & 0xffu) != 0 ? 1u << k : 0u;
+    }
   } else {
 #pragma unroll
-    for (int k = 0; k < kRun; ++k)
+    for (int k = 0; k < N; ++k)
       if (k < valid && p[k] != 0) m |= 1u << k;
   }
   return m;
