@@ -78,7 +78,10 @@ __device__ __forceinline__ RowPlace<LR> row_place(int W) {
 }
 
 // Rows, forward.  A row takes LR lanes (up to 8 LR channels) or 64 W, each lane
-// kRun channels K times; the workgroup's other threads other rows.
+// kRun channels K times; the workgroup's other threads other rows.  16-bit results
+// go past the caches (32768 rows of 2560 bf16: 88 us, through them 107; float32's
+// two stores of a run fill a line only together: 16384 rows of 1000 48 us, through
+// the caches 43).
 template <typename T, int K, int LR>
 __global__ __launch_bounds__(1024) void norm_rows_fwd_kernel(
     const T* __restrict__ x, const T* __restrict__ residual, const float* __restrict__ weight,
@@ -102,7 +105,7 @@ __global__ __launch_bounds__(1024) void norm_rows_fwd_kernel(
       run_floats<T>(load_run(residual + base + at, valid), f);
 #pragma unroll
       for (int k = 0; k < kRun; ++k) v[c][k] += f[k];
-      store_run<T>(sum_out + base + at, valid, v[c]);
+      store_run<T, sizeof(T) == 2>(sum_out + base + at, valid, v[c]);
       // the norm is of the stream as stored
       if constexpr (sizeof(T) == 2) {
         RunWords<T> w;
@@ -140,7 +143,7 @@ __global__ __launch_bounds__(1024) void norm_rows_fwd_kernel(
 #pragma unroll
     for (int k = 0; k < kRun; ++k)
       v[c][k] = __builtin_fmaf(v[c][k] * rstd, fw[k], bias != nullptr ? fb[k] : 0.0f);
-    store_run<T>(y + base + at, valid, v[c]);
+    store_run<T, sizeof(T) == 2>(y + base + at, valid, v[c]);
   }
 }
 
@@ -977,15 +980,27 @@ struct RowPlan {
   int lanes() const { return LR < 64 ? LR : 64 * W; }
 };
 
-RowPlan row_plan(int dim) {
+// `least`: accesses of a lane where a row has that many (the 16-bit forward's, see
+// rows_fwd_plan).
+RowPlan row_plan(int dim, int least = 1) {
   for (int LR = 8; LR < 64; LR *= 2)
     if (dim <= LR * kRun) return RowPlan{LR, 1, 1};
   const int spans = (dim + kRowSpan - 1) / kRowSpan;
-  int K = 1;
+  int K = spans < least ? 1 : least;
   while (K < 4 && spans > kMaxRowWaves * K) K *= 2;
   if (spans > kMaxRowWaves * K) return RowPlan{64, 0, 0};
   return RowPlan{64, (spans + K - 1) / K, K};
 }
+
+// The forward holds nothing over its rows, and a wave waits on its own few loads:
+// of 16-bit types two accesses a lane (32768 rows of 2560 bf16: 72 us, with one 88,
+// with four 74; with a residual 119, 140, 134; 16384 rows of 1000: 13, 15, 19),
+// of float32, whose access is twice as long, one (128, 126 and 129; with a
+// residual 258, 242, 256).  Fewer, longer-lived workgroups that read their next
+// row ahead were no faster (88 us and more).  The backward's sums of dweight and
+// dbias want the registers (16384 rows of 2560: one access 74 us, two 88).
+template <typename T>
+RowPlan rows_fwd_plan(int dim) { return row_plan(dim, sizeof(T) == 2 ? 2 : 1); }
 
 // The backward's workgroups: several short rows (their sums of dweight and dbias
 // then make one part) or a long one, and 4 rows and more to a slot, so that the
@@ -1153,7 +1168,7 @@ hipError_t cols_bwd(const NormLaunch& a, const ColPlan& p, hipStream_t stream) {
 
 template <typename T>
 hipError_t fwd_typed(const NormLaunch& a, hipStream_t stream) {
-  const RowPlan pl = row_plan(a.dim);
+  const RowPlan pl = rows_fwd_plan<T>(a.dim);
   if (a.seqlen == 1 && pl.K > 0) return by_row_plan(pl, RowsFwd<T>{a, pl, stream});
   const ColPlan cp = a.residual != nullptr ? col_plan(kHeldSum, kFwdGroups, a.batch, a.dim, a.seqlen, sizeof(T))
                                            : col_plan(kHeldFwd, kFwdGroups, a.batch, a.dim, a.seqlen, sizeof(T));
