@@ -56,15 +56,16 @@ __device__ __forceinline__ Place<W> place_of(const GatedSizes& p) {
   Place<W> q;
   if constexpr (W == 0) {
     q.lane = lane & (p.lanes - 1);
-    q.row = (int)(blockIdx.x * (group_waves(W) * 64u / p.lanes) + threadIdx.x / p.lanes);
-    q.live = q.row < p.rows;
-    if (!q.live) q.row = 0;
+    const int64_t row = group_index() * (group_waves(W) * 64 / p.lanes) + threadIdx.x / p.lanes;
+    q.live = row < p.rows;
+    q.row = q.live ? (int)row : 0;
     q.w0 = 0;
     q.last = q.lane == p.lanes - 1;
   } else {
     q.lane = lane;
-    q.row = W == 1 ? blockIdx.x * group_waves(W) + wave : blockIdx.x;
-    q.live = q.row < p.rows;  // (with more waves to a row the grid is the rows)
+    const int64_t row = W == 1 ? group_index() * group_waves(W) + wave : blockIdx.x;
+    q.live = row < p.rows;  // (with more waves to a row the grid is the rows)
+    q.row = (int)row;
     q.w0 = W == 1 ? 0 : wave;
     q.last = lane == 63;
   }
@@ -633,9 +634,9 @@ GatedSizes sizes_of(const GatedLaunch& a) {
 
 // Workgroups: of rows that share waves, of a wave to a row, or a row each.
 template <int W>
-unsigned groups_of(const GatedSizes& s) {
+dim3 groups_of(const GatedSizes& s) {
   const int64_t rows = W == 0 ? (int64_t)group_waves(W) * 64 / s.lanes : W == 1 ? group_waves(W) : 1;
-  return (unsigned)((s.rows + rows - 1) / rows);
+  return grid_of((s.rows + rows - 1) / rows, 64 * group_waves(W));
 }
 
 template <typename T>
@@ -654,7 +655,7 @@ struct FwdLaunch {
   template <int RULE, bool IG, bool ZG, int W>
   hipError_t launch() const {
     const GatedSizes s = sizes_of(a);
-    const unsigned grid = groups_of<W>(s);
+    const dim3 grid = groups_of<W>(s);
     gated_fwd_kernel<T, RULE, IG, ZG, W><<<grid, 64 * group_waves(W), 0, stream>>>(
         static_cast<const T*>(a.x), static_cast<const T*>(a.r), a.A, a.r_bias, static_cast<const T*>(a.i),
         a.i_bias, static_cast<const T*>(a.z), a.starts, a.h0, static_cast<T*>(a.y), a.last_state, a.ckpt, s);
@@ -678,7 +679,7 @@ struct BwdLaunchOf {
   template <int RULE, bool IG, bool ZG, int W>
   hipError_t launch() const {
     const GatedSizes s = sizes_of(a);
-    const unsigned grid = groups_of<W>(s);
+    const dim3 grid = groups_of<W>(s);
     // one row per channel: its sums are the results
     const bool direct = a.batch == 1;
     const int64_t plane = (int64_t)a.batch * a.dim;

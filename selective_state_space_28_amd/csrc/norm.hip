@@ -89,9 +89,9 @@ __global__ __launch_bounds__(1024) void norm_rows_fwd_kernel(
     float* __restrict__ mean_out, float* __restrict__ rstd_out, int rows, int dim, int W) {
   __shared__ float s_mean[4][kMaxRowWaves], s_var[4][kMaxRowWaves];
   const RowPlace<LR> p = row_place<LR>(W);
-  const int row = blockIdx.x * p.slots + p.slot;
+  const int64_t row = group_index() * p.slots + p.slot;
   const bool live = row < rows;  // idle rows run along to the barriers
-  const int64_t base = (int64_t)(live ? row : 0) * dim;
+  const int64_t base = (live ? row : 0) * dim;
 
   float v[K][kRun];
   float sum = 0.0f;
@@ -870,9 +870,10 @@ template <typename T>
 __global__ __launch_bounds__(256) void norm_few_fwd_kernel(
     const T* __restrict__ x, const T* __restrict__ residual, const float* __restrict__ weight,
     const float* __restrict__ bias, float eps, T* __restrict__ y, T* sum_out, float* __restrict__ mean_out,
-    float* __restrict__ rstd_out, int dim, int seqlen) {
+    float* __restrict__ rstd_out, int64_t tokens, int dim, int seqlen) {
   __shared__ float s_mean[4][kMaxRowWaves], s_var[4][kMaxRowWaves];
-  const int64_t token = blockIdx.x;
+  const int64_t token = group_index();
+  if (token >= tokens) return;
   const int wave = threadIdx.x >> 6;
   const int64_t base = token / seqlen * dim * seqlen + token % seqlen;
   const T* const again = residual != nullptr ? sum_out : x;
@@ -946,7 +947,7 @@ __global__ __launch_bounds__(256) void norm_few_bwd_kernel(
 __global__ __launch_bounds__(1024) void norm_sum_kernel(const float* __restrict__ part, float* __restrict__ dweight,
                                                         float* __restrict__ dbias, int parts, int dim) {
   __shared__ float s[32][33];
-  const int64_t at = (int64_t)blockIdx.x * 32 + (threadIdx.x & 31);
+  const int64_t at = group_index() * 32 + (threadIdx.x & 31);
   const int j = threadIdx.x >> 5;
   float v = 0.0f;
   if (at < 2 * (int64_t)dim) {
@@ -1071,7 +1072,7 @@ struct LdsPlan {
 };
 
 LdsPlan lds_plan(const ColPlan& p, int dim, int most, int n, int arrays) {
-  constexpr size_t room = (size_t)160 * 1024 - 40 * 1024 / 8;  // less the sums' static arrays (with TL = 64: no accesses kept)
+  constexpr size_t room = (size_t)155 * 1024;  // the sums' static arrays have the rest (with TL = 64: no accesses kept)
   LdsPlan l{};
   l.lds = dim <= most;
   l.bytes = l.lds ? (size_t)param_floats(n, dim) * 4 : 0;
@@ -1089,7 +1090,7 @@ LdsPlan lds_plan(const ColPlan& p, int dim, int most, int n, int arrays) {
 template <typename T, int K, int LR>
 hipError_t rows_fwd(const NormLaunch& a, const RowPlan& pl, hipStream_t stream) {
   const int slots = pl.lanes() < 256 ? 256 / pl.lanes() : 1;
-  const unsigned grid = (unsigned)(((int64_t)a.batch + slots - 1) / slots);
+  const dim3 grid = grid_of(((int64_t)a.batch + slots - 1) / slots, pl.lanes() * slots);
   norm_rows_fwd_kernel<T, K, LR><<<grid, pl.lanes() * slots, 0, stream>>>(
       static_cast<const T*>(a.x), static_cast<const T*>(a.residual), a.weight, a.bias, a.eps,
       static_cast<T*>(a.y), static_cast<T*>(a.sum_out), a.mean, a.rstd, a.batch, a.dim, pl.W);
@@ -1180,9 +1181,9 @@ hipError_t fwd_typed(const NormLaunch& a, hipStream_t stream) {
     case 64: return cols_fwd<T, 64>(a, cp, stream);
   }
   const int64_t tokens = (int64_t)a.batch * a.seqlen;
-  norm_few_fwd_kernel<T><<<(unsigned)tokens, 256, 0, stream>>>(
+  norm_few_fwd_kernel<T><<<grid_of(tokens, 256), 256, 0, stream>>>(
       static_cast<const T*>(a.x), static_cast<const T*>(a.residual), a.weight, a.bias, a.eps,
-      static_cast<T*>(a.y), static_cast<T*>(a.sum_out), a.mean, a.rstd, a.dim, (int)a.seqlen);
+      static_cast<T*>(a.y), static_cast<T*>(a.sum_out), a.mean, a.rstd, tokens, a.dim, (int)a.seqlen);
   return hipGetLastError();
 }
 
@@ -1210,7 +1211,7 @@ hipError_t bwd_typed(const NormLaunch& a, hipStream_t stream) {
   }
   if (e != hipSuccess) return e;
   const int parts = norm_bwd_parts(a.batch, a.dim, a.seqlen, sizeof(T));
-  norm_sum_kernel<<<(unsigned)((2 * (int64_t)a.dim + 31) / 32), 1024, 0, stream>>>(a.part, a.dweight, a.dbias,
+  norm_sum_kernel<<<grid_of((2 * (int64_t)a.dim + 31) / 32, 1024), 1024, 0, stream>>>(a.part, a.dweight, a.dbias,
                                                                                    parts, a.dim);
   return hipGetLastError();
 }

@@ -10,6 +10,16 @@ namespace ssm {
 
 constexpr int kRun = 8;  // consecutive elements that a lane holds
 
+// A grid of `groups` workgroups or a few more.  A dimension of a grid has fewer
+// than 2^32 threads: past 2^31 the workgroups go to a second one.
+inline dim3 grid_of(int64_t groups, int threads) {
+  const int64_t most = (INT64_C(1) << 31) / threads, y = (groups + most - 1) / most;
+  return dim3((unsigned)((groups + y - 1) / y), (unsigned)y);
+}
+
+// The workgroup's number in such a grid.
+__device__ __forceinline__ int64_t group_index() { return (int64_t)blockIdx.y * gridDim.x + blockIdx.x; }
+
 // ---- runs of kRun consecutive elements of a row --------------------------------
 // Rows start at any element (their length need not be a multiple of the run), so the
 // vector accesses are declared with the element's alignment; global memory

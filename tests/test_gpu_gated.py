@@ -341,6 +341,39 @@ def test_offsets_past_32_bits(dev):
     assert torch.allclose(last[:, -3:], lasts, rtol=1e-4, atol=1e-4)
 
 
+@pytest.mark.parametrize("d,L", [(2**27 + 5, 129), (2**26 + 5, 257)])
+def test_more_threads_than_a_grid_dimension_has(dev, d, L):
+    """2^32 threads and more, of rows that share a wave and of a wave each: rows in the middle and at the end are those
+    of a call on them alone, forward and backward."""
+    import torch
+    import selective_state_space_28_amd as ssm
+    if torch.cuda.mem_get_info()[0] < 130 * 2**30:
+        pytest.skip("needs 130 GiB of GPU memory")
+    gen = torch.Generator(device=dev)
+    gen.manual_seed(6)
+    x = torch.empty((1, d, L), dtype=torch.bfloat16, device=dev)
+    for k in range(0, d, 2**24):
+        x[:, k:k + 2**24].normal_(generator=gen)
+    A = -torch.rand(d, generator=gen, device=dev) - 0.2
+    windows = [slice(at, at + 9) for at in (0, d // 2, d - 9)]
+    alone = [(x[:, s].contiguous(), A[s].contiguous()) for s in windows]
+    y, last, ckpt = ssm.ssm_gated_scan_fwd(x, x, A, return_last_state=True, return_ckpt=True,
+                                           out=torch.full_like(x, float("nan")))
+    assert not bool(y[0, :, -1].isnan().any()) and not bool(last.isnan().any())
+    small = [ssm.ssm_gated_scan_fwd(xs, xs, As, return_last_state=True, return_ckpt=True) for xs, As in alone]
+    for s, (ys, lasts, _) in zip(windows, small):
+        assert torch.equal(y[:, s], ys) and torch.equal(last[:, s], lasts)
+    del y, last
+    g = ssm.ssm_gated_scan_bwd(x, x, A, ckpt=ckpt, dy=x)
+    for s, (xs, As), (_, _, cks) in zip(windows, alone, small):
+        gs = ssm.ssm_gated_scan_bwd(xs, xs, As, ckpt=cks, dy=xs)
+        for name in ("dx", "dr"):
+            assert torch.equal(g[name][:, s], gs[name]), name
+        for name in ("dA", "dr_bias"):
+            assert torch.equal(g[name][s], gs[name]), name
+        assert torch.equal(g["dh0"][:, s], gs["dh0"])
+
+
 # ---- one token ----------------------------------------------------------------------
 
 @pytest.mark.parametrize("gate,weight", [("sigmoid", "unit"), ("softplus", "convex"), ("softplus", "unit")])

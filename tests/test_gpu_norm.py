@@ -243,6 +243,35 @@ def test_offsets_past_32_bits(dev):
     assert near(g["dx"][:, :, -64:], one["dx"])
 
 
+def test_more_threads_than_a_grid_dimension_has(dev):
+    """2^32 threads and more: tokens in the middle and at the end are those of a call on them alone, and none is left out."""
+    import torch
+    import selective_state_space_28_amd as ssm
+    gen = torch.Generator(device=dev)
+    gen.manual_seed(8)
+    w = torch.tensor([0.5, 1.25, -2.0], device=dev)
+    # a workgroup a token
+    x = torch.empty((2**23 + 5, 3, 2), dtype=torch.bfloat16, device=dev).normal_(generator=gen)
+    y = ssm.ssm_layer_norm_fwd(x, w, axis=1, out=torch.full_like(x, float("nan")))
+    assert not bool(y.isnan().any())
+    for at in (0, 2**22, 2**23 - 9):
+        assert torch.equal(y[at:at + 14], ssm.ssm_layer_norm_fwd(x[at:at + 14], w, axis=1))
+    # eight lanes a row
+    x = torch.empty((2**29 + 7, 2), dtype=torch.bfloat16, device=dev).normal_(generator=gen)
+    y = ssm.ssm_layer_norm_fwd(x, w[:2], out=torch.full_like(x, float("nan")))
+    assert not bool(y.isnan().any())
+    for at in (0, 2**28, 2**29 - 9):
+        assert torch.equal(y[at:at + 16], ssm.ssm_layer_norm_fwd(x[at:at + 16], w[:2]))
+    del x, y
+    # as many sums as channels: one token's are its dy, and dy xhat rounded once
+    d = 2**26 + 3
+    x = torch.empty((1, d), dtype=torch.bfloat16, device=dev).normal_(generator=gen)
+    one = torch.ones(d, device=dev)
+    m, r = torch.zeros(1, device=dev), torch.ones(1, device=dev)
+    g = ssm.ssm_layer_norm_bwd(x, one, m, r, x)
+    assert torch.equal(g["dbias"], x[0].float()) and torch.equal(g["dweight"], x[0].float() ** 2)
+
+
 def test_refusals(dev):
     import torch
     import selective_state_space_28_amd as ssm
