@@ -1018,20 +1018,50 @@ int row_bwd_groups(const RowPlan& pl, int rows) {
 
 // Columns: lanes of a channel's piece (0: fewer steps than a piece), accesses a
 // wave holds in registers, waves of a workgroup, tiles of a batch row and of the
-// call, workgroups.
+// call, workgroups, LDS for parameters and kept accesses.
 struct ColPlan {
   int TL, K, waves, tiles, all, groups;
+  size_t room;
 };
 
-constexpr int kHeldFwd[] = {10, 40};
-constexpr int kHeldSum[] = {10, 20};  // forward with a residual
-constexpr int kHeldBwd[] = {5, 16};
+// What a column kernel holds: accesses in registers (the first two where two
+// workgroups of a CU can run, the last with the registers of a CU to one), most
+// workgroups, parameters (and sums of their gradients) a channel and the most
+// channels for which they wait in LDS, arrays that it holds pieces of.
 // Workgroups: the backward's each leave a part of dweight and dbias, so one for
 // each CU (batch 8, dim 1536, L 2047 float32: 88 us, with two 97); the
 // forward's two (batch 16, dim 5120, L 2048 bf16: 164 us, with one 170).
-constexpr int kFwdGroups = 512, kBwdGroups = 256;
+struct ColKind {
+  int held[3], groups, params, lds_dim, arrays;
+};
 
-ColPlan col_plan(const int (&held)[2], int most, int batch, int dim, int64_t seqlen, int elem_bytes) {
+constexpr ColKind kColFwd = {{10, 16, 40}, 512, 2, 8192, 1};
+constexpr ColKind kColSum = {{10, 10, 20}, 512, 2, 8192, 1};  // forward with a residual
+constexpr ColKind kColBwd = {{5, 5, 16}, 256, 3, 5120, 2};
+
+// Dynamic LDS of a column kernel: the parameters, then accesses that the registers
+// do not hold, as far as the plan's room goes.
+struct LdsPlan {
+  int lds, kept;
+  size_t bytes;
+};
+
+LdsPlan lds_plan(const ColKind& kind, const ColPlan& p, int dim) {
+  LdsPlan l{};
+  l.lds = dim <= kind.lds_dim;
+  l.bytes = l.lds ? (size_t)param_floats(kind.params, dim) * 4 : 0;
+  const int rows = 64 / p.TL, need = (dim + rows - 1) / rows;
+  const int each = (need + p.waves - 1) / p.waves;  // accesses of a wave
+  const size_t access = (size_t)p.waves * 64 * 16 * kind.arrays;
+  if (each > p.K && p.TL < 64 && p.room > l.bytes) {  // (of TL = 64 the sums' arrays are too long)
+    const size_t fit = (p.room - l.bytes) / access;
+    l.kept = each - p.K < (int)fit ? each - p.K : (int)fit;
+    l.bytes += (size_t)l.kept * access;
+  }
+  return l;
+}
+
+ColPlan col_plan(const ColKind& kind, int batch, int dim, int64_t seqlen, int elem_bytes) {
   ColPlan p{};
   const int64_t row = seqlen * elem_bytes;
   if (row < 16 || row >= INT32_MAX) {
@@ -1048,43 +1078,28 @@ ColPlan col_plan(const int (&held)[2], int most, int batch, int dim, int64_t seq
   while (dim < 64 / p.TL) p.TL = p.TL < 8 ? 2 * p.TL : 64;
   if (row * (64 / p.TL) >= INT32_MAX) p.TL = 64;  // byte offsets within an access in 32 bits
   const int need = (dim + 64 / p.TL - 1) / (64 / p.TL);
-  p.K = need <= kTileWaves * held[0] ? held[0] : held[1];
   p.waves = need < kTileWaves ? need : kTileWaves;
   p.tiles = (int)((row + 16 * p.TL - 1) / (16 * p.TL));
   p.all = batch * p.tiles;
-  p.groups = p.all < most ? p.all : most;
+  p.groups = p.all < kind.groups ? p.all : kind.groups;
+  // A CU's 160 KiB of LDS, or half of them, less the sums' static arrays.  Two
+  // workgroups of a CU overlap one's loads with the other's stores, so they are
+  // taken as long as they hold all but an access of a wave (batch 16, L 2048
+  // bf16, dim 768: 20 us, one workgroup with 40 accesses held 35).
+  const int each = (need + p.waves - 1) / p.waves;
+  p.room = (size_t)75 * 1024;
+  for (int k = 0; k < 2; ++k) {
+    p.K = kind.held[k];
+    if (each <= p.K + lds_plan(kind, p, dim).kept + (k == 1 ? 1 : 0)) return p;
+  }
+  p.K = kind.held[2];
+  p.room = (size_t)155 * 1024;
   return p;
 }
 
 // Whether every access writes whole lines of `out`.
 int whole_lines(const NormLaunch& a, const ColPlan& p, size_t es, const void* out) {
   return p.TL >= 8 && (size_t)a.seqlen * es % 128 == 0 && reinterpret_cast<uintptr_t>(out) % 128 == 0;
-}
-
-// Most channels whose parameters (and sums of their gradients) wait in LDS.
-constexpr int kLdsDimFwd = 8192, kLdsDimBwd = 5120;
-
-// Dynamic LDS of a column kernel: n parameters a channel, then accesses that the
-// registers do not hold (`arrays` pieces each), as far as a CU's 160 KiB go.
-struct LdsPlan {
-  int lds, kept;
-  size_t bytes;
-};
-
-LdsPlan lds_plan(const ColPlan& p, int dim, int most, int n, int arrays) {
-  constexpr size_t room = (size_t)155 * 1024;  // the sums' static arrays have the rest (with TL = 64: no accesses kept)
-  LdsPlan l{};
-  l.lds = dim <= most;
-  l.bytes = l.lds ? (size_t)param_floats(n, dim) * 4 : 0;
-  const int rows = 64 / p.TL, need = (dim + rows - 1) / rows;
-  const int each = (need + p.waves - 1) / p.waves;  // accesses of a wave
-  const size_t access = (size_t)p.waves * 64 * 16 * arrays;
-  if (each > p.K && p.TL < 64) {
-    const size_t fit = (room - l.bytes) / access;
-    l.kept = each - p.K < (int)fit ? each - p.K : (int)fit;
-    l.bytes += (size_t)l.kept * access;
-  }
-  return l;
 }
 
 template <typename T, int K, int LR>
@@ -1139,7 +1154,7 @@ struct RowsBwd {
 
 template <typename T, int TL, int K, bool RES>
 hipError_t cols_fwd_launch(const NormLaunch& a, const ColPlan& p, hipStream_t stream) {
-  const LdsPlan l = lds_plan(p, a.dim, kLdsDimFwd, 2, 1);
+  const LdsPlan l = lds_plan(RES ? kColSum : kColFwd, p, a.dim);
   norm_cols_fwd_kernel<T, TL, K, RES><<<(unsigned)p.groups, 64 * p.waves, l.bytes, stream>>>(
       static_cast<const T*>(a.x), static_cast<const T*>(a.residual), a.weight, a.bias, a.eps,
       static_cast<T*>(a.y), static_cast<T*>(a.sum_out), a.mean, a.rstd, a.dim, (int)a.seqlen, p.tiles, p.all, l.lds, l.kept,
@@ -1149,17 +1164,20 @@ hipError_t cols_fwd_launch(const NormLaunch& a, const ColPlan& p, hipStream_t st
 
 template <typename T, int TL>
 hipError_t cols_fwd(const NormLaunch& a, const ColPlan& p, hipStream_t stream) {
+  constexpr const int (&fwd)[3] = kColFwd.held, (&sum)[3] = kColSum.held;
   if (a.residual != nullptr)
-    return p.K == kHeldSum[0] ? cols_fwd_launch<T, TL, kHeldSum[0], true>(a, p, stream)
-                              : cols_fwd_launch<T, TL, kHeldSum[1], true>(a, p, stream);
-  return p.K == kHeldFwd[0] ? cols_fwd_launch<T, TL, kHeldFwd[0], false>(a, p, stream)
-                            : cols_fwd_launch<T, TL, kHeldFwd[1], false>(a, p, stream);
+    return p.K == sum[2] ? cols_fwd_launch<T, TL, sum[2], true>(a, p, stream)
+                         : cols_fwd_launch<T, TL, sum[0], true>(a, p, stream);
+  return p.K == fwd[2]   ? cols_fwd_launch<T, TL, fwd[2], false>(a, p, stream)
+         : p.K == fwd[1] ? cols_fwd_launch<T, TL, fwd[1], false>(a, p, stream)
+                         : cols_fwd_launch<T, TL, fwd[0], false>(a, p, stream);
 }
 
 template <typename T, int TL>
 hipError_t cols_bwd(const NormLaunch& a, const ColPlan& p, hipStream_t stream) {
-  const LdsPlan l = lds_plan(p, a.dim, kLdsDimBwd, 3, 2);
-  auto kernel = p.K == kHeldBwd[0] ? norm_cols_bwd_kernel<T, TL, kHeldBwd[0]> : norm_cols_bwd_kernel<T, TL, kHeldBwd[1]>;
+  const LdsPlan l = lds_plan(kColBwd, p, a.dim);
+  constexpr const int (&held)[3] = kColBwd.held;
+  auto kernel = p.K == held[2] ? norm_cols_bwd_kernel<T, TL, held[2]> : norm_cols_bwd_kernel<T, TL, held[0]>;
   kernel<<<(unsigned)p.groups, 64 * p.waves, l.bytes, stream>>>(
       static_cast<const T*>(a.x), a.weight, a.mean, a.rstd, static_cast<const T*>(a.dy),
       static_cast<const T*>(a.dsum), static_cast<T*>(a.dx), a.part, a.dim, (int)a.seqlen, p.tiles, p.all, l.lds, l.kept,
@@ -1171,8 +1189,7 @@ template <typename T>
 hipError_t fwd_typed(const NormLaunch& a, hipStream_t stream) {
   const RowPlan pl = rows_fwd_plan<T>(a.dim);
   if (a.seqlen == 1 && pl.K > 0) return by_row_plan(pl, RowsFwd<T>{a, pl, stream});
-  const ColPlan cp = a.residual != nullptr ? col_plan(kHeldSum, kFwdGroups, a.batch, a.dim, a.seqlen, sizeof(T))
-                                           : col_plan(kHeldFwd, kFwdGroups, a.batch, a.dim, a.seqlen, sizeof(T));
+  const ColPlan cp = col_plan(a.residual != nullptr ? kColSum : kColFwd, a.batch, a.dim, a.seqlen, sizeof(T));
   switch (cp.TL) {
     case 1: return cols_fwd<T, 1>(a, cp, stream);
     case 2: return cols_fwd<T, 2>(a, cp, stream);
@@ -1194,7 +1211,7 @@ hipError_t bwd_typed(const NormLaunch& a, hipStream_t stream) {
   if (a.seqlen == 1 && pl.K > 0) {
     e = by_row_plan(pl, RowsBwd<T>{a, pl, stream});
   } else {
-    const ColPlan cp = col_plan(kHeldBwd, kBwdGroups, a.batch, a.dim, a.seqlen, sizeof(T));
+    const ColPlan cp = col_plan(kColBwd, a.batch, a.dim, a.seqlen, sizeof(T));
     switch (cp.TL) {
       case 1: e = cols_bwd<T, 1>(a, cp, stream); break;
       case 2: e = cols_bwd<T, 2>(a, cp, stream); break;
@@ -1221,7 +1238,7 @@ hipError_t bwd_typed(const NormLaunch& a, hipStream_t stream) {
 int norm_bwd_parts(int batch, int dim, int64_t seqlen, int elem_bytes) {
   const RowPlan pl = row_plan(dim);
   if (seqlen == 1 && pl.K > 0) return row_bwd_groups(pl, batch);
-  return col_plan(kHeldBwd, kBwdGroups, batch, dim, seqlen, elem_bytes).groups;
+  return col_plan(kColBwd, batch, dim, seqlen, elem_bytes).groups;
 }
 
 hipError_t launch_norm_fwd(const NormLaunch& a, hipStream_t stream) {
