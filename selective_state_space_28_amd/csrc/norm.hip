@@ -998,8 +998,11 @@ RowPlan row_plan(int dim, int least = 1) {
 // with four 74; with a residual 119, 140, 134; 16384 rows of 1000: 13, 15, 19),
 // of float32, whose access is twice as long, one (128, 126 and 129; with a
 // residual 258, 242, 256).  Fewer, longer-lived workgroups that read their next
-// row ahead were no faster (88 us and more).  The backward's sums of dweight and
-// dbias want the registers (16384 rows of 2560: one access 74 us, two 88).
+// row ahead were no faster (88 us and more).  Also for few rows, where one is
+// quicker (256 rows of 2560 with a residual: 3.8 us, two 4.6): a token's sums are
+// then in one order, and its result the same bits, in a batch of any size.  The
+// backward's sums of dweight and dbias want the registers (16384 rows of 2560: one
+// access 74 us, two 88).
 template <typename T>
 RowPlan rows_fwd_plan(int dim) { return row_plan(dim, sizeof(T) == 2 ? 2 : 1); }
 

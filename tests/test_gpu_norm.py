@@ -117,6 +117,15 @@ def test_columns(dev, dtype, b, dim, L):
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("b,dim,L,residual", [(256, 500, 64, False), (260, 500, 20, True), (130, 700, 70, False),
+                                              (260, 1100, 20, False), (260, 1100, 20, True), (130, 1300, 66, True),
+                                              (260, 1500, 20, False), (260, 1600, 20, False)])
+def test_columns_of_many_tiles(dev, dtype, b, dim, L, residual):
+    """A line of 128 bytes to a channel's piece, held in registers, in LDS, and what neither holds."""
+    check(dev, dtype, (b, dim, L), 1, 21, residual=residual)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
 def test_layouts_agree(dev, dtype):
     """The same tokens with their channels together and in the scans' layout."""
     import selective_state_space_28_amd as ssm
