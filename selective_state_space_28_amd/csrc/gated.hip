@@ -24,6 +24,7 @@
 // lambda_t = dh_t + a_{t+1} lambda_{t+1} by the same prefix over the mirrored
 // lanes (its map m -> P m + Q carries m_t = a_t lambda_t to the left).
 #include "gated_math.hpp"
+#include "row_slices.hpp"
 #include "ssm_kernels.hpp"
 
 namespace ssm {
@@ -706,17 +707,13 @@ struct StepLaunch {
   hipStream_t stream;
   template <int RULE, bool IG, bool ZG>
   hipError_t operator()() const {
-    constexpr int kMaxRows = 65535;  // grid y per launch
-    for (int b0 = 0; b0 < a.batch; b0 += kMaxRows) {
-      const int nb = a.batch - b0 < kMaxRows ? a.batch - b0 : kMaxRows;
+    return by_row_slices(a.batch, hipSuccess, [&](int b0, int nb) {
       gated_step_kernel<T, RULE, IG, ZG><<<dim3((unsigned)((a.dim + 255) / 256), (unsigned)nb), 256, 0, stream>>>(
           a.h0, static_cast<const T*>(a.x), static_cast<const T*>(a.r), a.A, a.r_bias,
           static_cast<const T*>(a.i), a.i_bias, static_cast<const T*>(a.z), a.starts, static_cast<T*>(a.y),
           a.last_state, b0, a.dim);
-      const hipError_t e = hipGetLastError();
-      if (e != hipSuccess) return e;
-    }
-    return hipSuccess;
+      return hipGetLastError();
+    });
   }
 };
 

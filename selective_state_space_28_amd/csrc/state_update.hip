@@ -21,6 +21,7 @@
 // conv1d + silu in front of the SSM): u = silu(cb + sum_k w[k] x[t-K+1+k])
 // from the carried K-1 previous inputs and this token's x; the carried
 // inputs are shifted in place to end with x.
+#include "row_slices.hpp"
 #include "ssm_kernels.hpp"
 #include "ssm_math.hpp"
 
@@ -173,18 +174,14 @@ static hipError_t launch_n(const DecodeLaunch& a, hipStream_t stream) {
                                         : state_update_kernel<T, N, MODE, true, false>)
                       : (a.z != nullptr ? state_update_kernel<T, N, MODE, false, true>
                                         : state_update_kernel<T, N, MODE, false, false>);
-  constexpr int kMaxRows = 65535;  // grid y per launch
-  for (int b0 = 0; b0 < a.batch; b0 += kMaxRows) {
-    const int nb = a.batch - b0 < kMaxRows ? a.batch - b0 : kMaxRows;
+  return by_row_slices(a.batch, hipSuccess, [&](int b0, int nb) {
     kernel<<<dim3(gx, (unsigned)nb), 256, 0, stream>>>(
         a.state, static_cast<const T*>(a.u), static_cast<const T*>(a.delta), a.A,
         static_cast<const T*>(a.B), static_cast<const T*>(a.C), a.Dskip,
         static_cast<const T*>(a.z), a.bias, static_cast<T*>(a.y), b0, a.dim, a.softplus,
         a.conv_state, a.conv_w, a.conv_b, a.conv_k);
-    const hipError_t e = hipGetLastError();
-    if (e != hipSuccess) return e;
-  }
-  return hipSuccess;
+    return hipGetLastError();
+  });
 }
 
 template <typename T, int MODE>
