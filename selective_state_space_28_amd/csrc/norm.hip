@@ -388,12 +388,15 @@ struct Spread {
   }
   __device__ __forceinline__ void join(float nb, const float (&mb)[E], const float (&sb)[E]) {
     const float all = n + nb;
-    const float share = all > 0.0f ? nb / all : 0.0f;
+    const float share = all > 0.0f ? nb / all : 0.0f, both = n * share;
 #pragma unroll
     for (int k = 0; k < E; ++k) {
       const float d = mb[k] - mean[k];
       mean[k] = __builtin_fmaf(d, share, mean[k]);
-      sq[k] += __builtin_fmaf(d * d, n * share, sb[k]);
+      // Where a side has no values d is the other's mean, whose square may be
+      // infinite: it has no part.
+      const float apart = both > 0.0f ? d : 0.0f;
+      sq[k] += __builtin_fmaf(apart * apart, both, sb[k]);
     }
     n = all;
   }

@@ -2,6 +2,9 @@
 steps, at the ends of their sizes and of float32's range."""
 import pytest
 
+from tests import layers_ref as ref
+from tests import layers_torch_ref as tref
+
 pytestmark = pytest.mark.gpu
 
 
@@ -43,3 +46,38 @@ def test_steps_of_the_largest_batch(dev):
     check(lambda st, u, out: ssm.ssm_gated_state_update(st, u, u, A, out=out), x)
     A = A.view(1, 1)
     check(lambda st, u, out: ssm.ssm_state_update(st, u, u, A, u, u, out=out), x)
+
+
+@pytest.mark.parametrize("residual", [False, True])
+@pytest.mark.parametrize("shape,axis", [((4, 500), -1), ((2, 1537, 3), 1), ((2, 10, 40), 1), ((2, 300, 40), 1),
+                                        ((130, 1300, 32), 1), ((130, 5121, 41), 1)])
+def test_means_whose_square_passes_float32(dev, shape, axis, residual):
+    """Values near 3e19, their spread 1e17: the square of the mean is outside float32, every deviation's inside."""
+    import torch
+    import selective_state_space_28_amd as ssm
+    gen = torch.Generator(device=dev)
+    gen.manual_seed(6)
+    rnd = lambda *s: torch.randn(s, generator=gen, device=dev)  # noqa: E731
+    n = shape[axis]
+    x, w, b, dy = 3e19 + 1e17 * rnd(*shape), 1 + 0.3 * rnd(n), 0.3 * rnd(n), rnd(*shape)
+    res = 1e17 * rnd(*shape) if residual else None
+    out = ssm.ssm_layer_norm_fwd(x, w, b, res, axis=axis, return_stats=True)
+    s = x if res is None else x + res
+    wide = [1] * len(shape)
+    wide[axis] = -1
+    s64, w64, d64 = s.double(), w.double().view(wide), dy.double()
+    mean, var = s64.mean(axis, keepdim=True), s64.var(axis, unbiased=False, keepdim=True)
+    xh = (s64 - mean) / var.sqrt()
+    # 128 half steps, and those of a mean of 300 spreads
+    slack = 128 * ref.EPS32 + 300 * ref.EPS32
+    tref.close(out[0], xh * w64 + b.double().view(wide), ref.EPS32, slack, "y")
+    tref.close(out[-2], mean.squeeze(axis), ref.EPS32, slack, "mean")
+    tref.close(out[-1], 1 / var.sqrt().squeeze(axis), ref.EPS32, slack, "rstd")
+    g = ssm.ssm_layer_norm_bwd(s, w, out[-2], out[-1], dy, axis=axis)
+    m, rs = (v.double().unsqueeze(axis) for v in out[-2:])
+    xh, dn = (s64 - m) * rs, d64 * w64
+    over = [k for k in range(len(shape)) if k != axis % len(shape)]
+    tref.close(g["dweight"], (d64 * xh).sum(over), ref.EPS32, slack, "dweight", (d64 * xh).abs().sum(over))
+    # dx is near 1e-17, far above what close() adds for zero
+    dx = (dn - dn.mean(axis, keepdim=True) - xh * (dn * xh).mean(axis, keepdim=True)) * rs
+    tref.close(g["dx"], dx, ref.EPS32, slack, "dx", dn.abs() * rs)
