@@ -23,7 +23,8 @@
  *    (batch, seqlen) float32; weight, bias, dweight, dbias: (dim) float32.
  *    Contiguous; pointers need their element's alignment only.
  *  - Every sum is held in float32 or wider, the variance taken about the mean;
- *    y and dx are rounded once.
+ *    y and dx are rounded once.  A token of equal values has exactly that mean
+ *    and variance 0: y is the bias (NaN where eps is 0 too).
  *  - A NaN or Inf in one token makes that token's y (and dx) NaN where the
  *    formula does and leaves the other tokens alone.
  */

@@ -14,8 +14,10 @@
 //    pieces of 16 TL bytes.  It goes over the tile twice, once for the sums over
 //    the channels and once for the results.
 //
-// The mean is taken first and the variance about it, both in float32, as
-// quotients by dim (a token of equal values has exactly that mean).
+// The mean is taken first and the variance about it.  A token of equal values has
+// exactly that mean: a column's is a running one, and where values are summed and
+// divided by dim their sum is exact, in float32 of up to 2^16 values of bf16 (8
+// bits), in float64 otherwise (rows of float32, columns of a few steps).
 //
 // dweight and dbias are sums over the tokens: each workgroup leaves its part
 // (part[p][0] of dweight, part[p][1] of dbias) and norm_sum_kernel adds the
@@ -33,9 +35,9 @@ constexpr int kRowSpan = 64 * kRun;  // elements of one access of a wave
 
 // Sum over a row, in every lane of it: over its LR lanes, and over the W waves
 // of a row longer than a wave (LR = 64), the `slot`-th of its workgroup.  `s` is
-// this sum's own LDS.  The order is fixed.
-template <int LR = 64>
-__device__ __forceinline__ float row_sum(float v, float (*s)[kMaxRowWaves], int slot, int wave, int W) {
+// this sum's own LDS.  The order is fixed.  V: float or double.
+template <int LR = 64, typename V>
+__device__ __forceinline__ V row_sum(V v, V (*s)[kMaxRowWaves], int slot, int wave, int W) {
   if constexpr (LR < 64) {
     v += dpp_moved<0xb1, 0xf>(v);   // quad_perm: the pair's other
     v += dpp_moved<0x4e, 0xf>(v);   // quad_perm: the other pair
@@ -48,10 +50,14 @@ __device__ __forceinline__ float row_sum(float v, float (*s)[kMaxRowWaves], int 
   if (W == 1) return v;
   if ((threadIdx.x & 63) == 0) s[slot][wave] = v;
   __syncthreads();
-  float t = 0.0f;
+  V t = 0;
   for (int k = 0; k < W; ++k) t += s[slot][k];
   return t;
 }
+
+// What a row's values of T are summed in: exact for equal values.
+template <typename T>
+using RowSum = typename std::conditional<sizeof(T) == 4, double, float>::type;
 
 __device__ __forceinline__ void load_f32_run(const float* p, int valid, float (&f)[kRun]) {
   run_floats<float>(load_run<float>(p, valid), f);
@@ -78,23 +84,24 @@ __device__ __forceinline__ RowPlace<LR> row_place(int W) {
 }
 
 // Rows, forward.  A row takes LR lanes (up to 8 LR channels) or 64 W, each lane
-// kRun channels K times; the workgroup's other threads other rows.  16-bit results
-// go past the caches (32768 rows of 2560 bf16: 88 us, through them 107; float32's
-// two stores of a run fill a line only together: 16384 rows of 1000 48 us, through
-// the caches 43).
+// kRun channels K times; the workgroup's other threads other rows; rn = 1 / dim.
+// 16-bit results go past the caches (32768 rows of 2560 bf16: 88 us, through them
+// 107; float32's two stores of a run fill a line only together: 16384 rows of 1000
+// 48 us, through the caches 43).
 template <typename T, int K, int LR>
 __global__ __launch_bounds__(1024) void norm_rows_fwd_kernel(
     const T* __restrict__ x, const T* __restrict__ residual, const float* __restrict__ weight,
     const float* __restrict__ bias, float eps, T* __restrict__ y, T* __restrict__ sum_out,
-    float* __restrict__ mean_out, float* __restrict__ rstd_out, int rows, int dim, int W) {
-  __shared__ float s_mean[4][kMaxRowWaves], s_var[4][kMaxRowWaves];
+    float* __restrict__ mean_out, float* __restrict__ rstd_out, int rows, int dim, double rn, int W) {
+  __shared__ RowSum<T> s_mean[4][kMaxRowWaves];
+  __shared__ float s_var[4][kMaxRowWaves];
   const RowPlace<LR> p = row_place<LR>(W);
   const int64_t row = group_index() * p.slots + p.slot;
   const bool live = row < rows;  // idle rows run along to the barriers
   const int64_t base = (live ? row : 0) * dim;
 
   float v[K][kRun];
-  float sum = 0.0f;
+  RowSum<T> sum = 0;
 #pragma unroll
   for (int c = 0; c < K; ++c) {
     const int at = (c * p.span + p.lane) * kRun;
@@ -117,7 +124,10 @@ __global__ __launch_bounds__(1024) void norm_rows_fwd_kernel(
     for (int k = 0; k < kRun; ++k) sum += v[c][k];  // past the end: zeros
   }
   const float n = (float)dim;
-  const float mean = row_sum<LR>(sum, s_mean, p.slot, p.wave, W) / n;
+  sum = row_sum<LR>(sum, s_mean, p.slot, p.wave, W);
+  // (a division in float64 is some 15 instructions; the product's two roundings
+  // to 53 bits do not reach the 24 of equal values' mean)
+  const float mean = sizeof(T) == 4 ? (float)(sum * rn) : (float)sum / n;
   float sq = 0.0f;
 #pragma unroll
   for (int c = 0; c < K; ++c) {
@@ -874,13 +884,14 @@ __global__ __launch_bounds__(256) void norm_few_fwd_kernel(
     const T* __restrict__ x, const T* __restrict__ residual, const float* __restrict__ weight,
     const float* __restrict__ bias, float eps, T* __restrict__ y, T* sum_out, float* __restrict__ mean_out,
     float* __restrict__ rstd_out, int64_t tokens, int dim, int seqlen) {
-  __shared__ float s_mean[4][kMaxRowWaves], s_var[4][kMaxRowWaves];
+  __shared__ double s_mean[4][kMaxRowWaves];
+  __shared__ float s_var[4][kMaxRowWaves];
   const int64_t token = group_index();
   if (token >= tokens) return;
   const int wave = threadIdx.x >> 6;
   const int64_t base = token / seqlen * dim * seqlen + token % seqlen;
   const T* const again = residual != nullptr ? sum_out : x;
-  float sum = 0.0f;
+  double sum = 0.0;
   for (int d = threadIdx.x; d < dim; d += 256) {
     const int64_t at = base + (int64_t)d * seqlen;
     float f = Elem<T>::load(x + at);
@@ -891,7 +902,7 @@ __global__ __launch_bounds__(256) void norm_few_fwd_kernel(
     }
     sum += f;
   }
-  const float mean = row_sum(sum, s_mean, 0, wave, 4) / (float)dim;
+  const float mean = (float)(row_sum(sum, s_mean, 0, wave, 4) / (double)dim);
   float sq = 0.0f;
   for (int d = threadIdx.x; d < dim; d += 256) {
     const float f = Elem<T>::load(again + base + (int64_t)d * seqlen) - mean;
@@ -1114,7 +1125,7 @@ hipError_t rows_fwd(const NormLaunch& a, const RowPlan& pl, hipStream_t stream) 
   const dim3 grid = grid_of(((int64_t)a.batch + slots - 1) / slots, pl.lanes() * slots);
   norm_rows_fwd_kernel<T, K, LR><<<grid, pl.lanes() * slots, 0, stream>>>(
       static_cast<const T*>(a.x), static_cast<const T*>(a.residual), a.weight, a.bias, a.eps,
-      static_cast<T*>(a.y), static_cast<T*>(a.sum_out), a.mean, a.rstd, a.batch, a.dim, pl.W);
+      static_cast<T*>(a.y), static_cast<T*>(a.sum_out), a.mean, a.rstd, a.batch, a.dim, 1.0 / a.dim, pl.W);
   return hipGetLastError();
 }
 

@@ -87,15 +87,31 @@ __device__ __forceinline__ void run_floats(const RunWords<T>& r, float (&f)[kRun
   words_to_floats<T, kRun>(r.w, f);
 }
 
+// A float64 by two moves of its halves.
+template <int CTRL, int ROW_MASK>
+__device__ __forceinline__ double dpp_moved(double v) {
+  return __hiloint2double(__builtin_amdgcn_update_dpp(0, __double2hiint(v), CTRL, ROW_MASK, 0xf, false),
+                          __builtin_amdgcn_update_dpp(0, __double2loint(v), CTRL, ROW_MASK, 0xf, false));
+}
+
+__device__ __forceinline__ float last_lane(float v) {
+  return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), 63));
+}
+__device__ __forceinline__ double last_lane(double v) {
+  return __hiloint2double(__builtin_amdgcn_readlane(__double2hiint(v), 63),
+                          __builtin_amdgcn_readlane(__double2loint(v), 63));
+}
+
 // The sum of v over the wave, in every lane; the order is fixed.
-__device__ __forceinline__ float wave_sum(float v) {
+template <typename V>
+__device__ __forceinline__ V wave_sum(V v) {
   v += dpp_moved<0x111, 0xf>(v);  // row_shr:1
   v += dpp_moved<0x112, 0xf>(v);  // row_shr:2
   v += dpp_moved<0x114, 0xf>(v);  // row_shr:4
   v += dpp_moved<0x118, 0xf>(v);  // row_shr:8
   v += dpp_moved<0x142, 0xa>(v);  // row_bcast:15 into rows 1 and 3
   v += dpp_moved<0x143, 0xc>(v);  // row_bcast:31 into rows 2 and 3
-  return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), 63));
+  return last_lane(v);
 }
 
 }  // namespace ssm

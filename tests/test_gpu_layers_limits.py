@@ -81,3 +81,26 @@ def test_means_whose_square_passes_float32(dev, shape, axis, residual):
     # dx is near 1e-17, far above what close() adds for zero
     dx = (dn - dn.mean(axis, keepdim=True) - xh * (dn * xh).mean(axis, keepdim=True)) * rs
     tref.close(g["dx"], dx, ref.EPS32, slack, "dx", dn.abs() * rs)
+
+
+@pytest.mark.parametrize("value", [777.7001, 0.1, -1e8 / 3, 1e30])
+@pytest.mark.parametrize("shape,axis", [((5, 200), -1), ((3, 1000), -1), ((2, 2560), -1), ((2, 5000), -1),
+                                        ((2, 9000), -1), ((2, 33000), -1), ((3, 1537, 3), 1), ((2, 200, 9), 1),
+                                        ((1, 2560, 64), 1), ((130, 5121, 32), 1)])
+def test_tokens_of_one_value(dev, shape, axis, value):
+    """A token whose channels are all the same number: its mean is that number, so y is the bias, whatever the layout;
+    the number's sums are not exact."""
+    import torch
+    import selective_state_space_28_amd as ssm
+    n = shape[axis]
+    for dt in (torch.float32, torch.bfloat16):
+        x = torch.full(shape, value, device=dev, dtype=dt)
+        w, b = torch.full((n,), 1.5, device=dev), torch.linspace(-1, 1, n, device=dev)
+        y, mean, rstd = ssm.ssm_layer_norm_fwd(x, w, b, eps=1e-5, axis=axis, return_stats=True)
+        assert bool((mean == x.flatten()[0].float()).all())
+        assert torch.allclose(rstd, torch.full_like(rstd, 1e-5 ** -0.5), rtol=1e-6)
+        assert bool((y == (b if axis == -1 else b[:, None]).to(dt)).all())
+        half = torch.full(shape, value / 2, device=dev, dtype=dt)
+        if bool((half + half == x).all()):
+            z, s = ssm.ssm_layer_norm_fwd(half, w, b, half, axis=axis)
+            assert torch.equal(s, x) and torch.equal(z, y)
