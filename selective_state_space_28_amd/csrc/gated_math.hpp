@@ -37,8 +37,10 @@ __device__ __forceinline__ void softplus_pair(float x, float& sp, float& slope) 
 // decay, the decay a and the input weight w.
 //
 // The decay is held at or above the smallest normal float: exp is never 0, and an
-// infinite state that met a decay flushed to 0 would turn into NaN.  (A NaN
-// exponent gives the floor; that step's weight is NaN and reaches the state.)
+// infinite state that met a decay flushed to 0 would turn into NaN.  A NaN
+// exponent gives a NaN decay (the maximum that keeps it; a run's is floored
+// all the same, and the run's Q carries the NaN): the backward pass' adjoint
+// has it to itself, where the state has the step's weight too.
 //
 // The weight is 1 - e^t, or its root, with t = A g or 2 A g.  Where |t| < 1/8 the
 // difference would magnify the rounding of e^t, so -t (e^t - 1)/t is taken, the
@@ -59,7 +61,7 @@ __device__ __forceinline__ Gate gate_of(float g, float A2) {
   Gate r;
   r.g = g;
   r.e2 = A2 * g;
-  r.a = __builtin_fmaxf(exp2_hw(r.e2), kMinNormal);
+  r.a = __builtin_elementwise_maximum(exp2_hw(r.e2), kMinNormal);
   float p = __builtin_fmaf(r.e2, k3, k2);
   p = __builtin_fmaf(r.e2, p, k1);
   p = __builtin_fmaf(r.e2, p, k0);

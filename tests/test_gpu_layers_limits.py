@@ -104,3 +104,40 @@ def test_tokens_of_one_value(dev, shape, axis, value):
         if bool((half + half == x).all()):
             z, s = ssm.ssm_layer_norm_fwd(half, w, b, half, axis=axis)
             assert torch.equal(s, x) and torch.equal(z, y)
+
+
+@pytest.mark.parametrize("gate,weight", [("sigmoid", "unit"), ("softplus", "convex")])
+@pytest.mark.parametrize("b,d,L,at", [(2, 5, 100, 70), (1, 4, 500, 30), (2, 5, 1300, 700), (2, 5, 17000, 7000),
+                                      (2, 4200, 600, 530)])
+def test_a_nan_decay_reaches_the_gradients_before_it(dev, gate, weight, b, d, L, at):
+    """lambda_t = dy_t + a_{t+1} lambda_{t+1}: a NaN in r makes every gradient of its channel's earlier steps NaN, back
+    to the start of its sequence, and leaves the other rows alone."""
+    import torch
+    import selective_state_space_28_amd as ssm
+    gen = torch.Generator(device=dev)
+    gen.manual_seed(3)
+    x, r, dy = (torch.randn((b, d, L), generator=gen, device=dev) for _ in range(3))
+    A = -torch.rand(d, generator=gen, device=dev) - 0.2
+    kw = dict(gate=gate, weight=weight)
+
+    def grads(r, starts=None):
+        ckpt = ssm.ssm_gated_scan_fwd(x, r, A, starts=starts, return_ckpt=True, **kw)[1]
+        return ssm.ssm_gated_scan_bwd(x, r, A, starts=starts, ckpt=ckpt, dy=dy, **kw)
+
+    clean = grads(r)
+    bad = r.clone()
+    bad[-1, 2, at] = float("nan")
+    g = grads(bad)
+    assert bool(g["dx"][-1, 2, :at + 1].isnan().all()) and torch.equal(g["dx"][-1, 2, at + 1:], clean["dx"][-1, 2, at + 1:])
+    assert bool(g["dr"][-1, 2].isnan().all())  # after it by the states
+    assert bool(g["dh0"][-1, 2].isnan()) and bool(g["dA"][2].isnan())
+    for k in ("dx", "dr", "dh0"):
+        u, v = g[k].clone(), clean[k]
+        u[-1, 2] = v[-1, 2]
+        assert torch.equal(u, v), k
+    starts = torch.zeros((b, L), dtype=torch.bool, device=dev)
+    starts[:, at - 9] = True
+    g, clean = grads(bad, starts), grads(r, starts)
+    assert bool(g["dx"][-1, 2, at - 9:at + 1].isnan().all())
+    assert torch.equal(g["dx"][-1, 2, :at - 9], clean["dx"][-1, 2, :at - 9])
+    assert torch.equal(g["dh0"], clean["dh0"])
