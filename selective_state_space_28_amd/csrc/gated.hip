@@ -367,7 +367,10 @@ __global__ __launch_bounds__(64 * group_waves(W)) void gated_bwd_kernel(
         slope = v * c;
       }
       const Gate t = gate_of<RULE>(v, A2);
-      g[k] = v;
+      // A softplus has no bound: where the decay is at its floor, g may be as far
+      // above 1 as the floor is below it, and its product with the decay's gradient
+      // (for dA) not the 0 that it is for a = 0.
+      g[k] = (RULE & kGateSoftplus) == 0 || t.a > kMinNormal ? v : 0.0f;
       sA_[k] = slope * Ad;
       a[k] = t.a;
       w[k] = t.w;

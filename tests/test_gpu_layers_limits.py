@@ -141,3 +141,29 @@ def test_a_nan_decay_reaches_the_gradients_before_it(dev, gate, weight, b, d, L,
     assert bool(g["dx"][-1, 2, at - 9:at + 1].isnan().all())
     assert torch.equal(g["dx"][-1, 2, :at - 9], clean["dx"][-1, 2, :at - 9])
     assert torch.equal(g["dh0"], clean["dh0"])
+
+
+@pytest.mark.parametrize("weight", ["unit", "convex"])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("b,d,L", [(2, 5, 100), (2, 5, 1300)])
+def test_a_gate_of_the_types_largest_value(dev, dtype, b, d, L, weight):
+    """softplus of the largest finite r: the decay is 0, so nothing of that step reaches dA, though g is 1e38."""
+    import torch
+    import selective_state_space_28_amd as ssm
+    gen = torch.Generator(device=dev)
+    gen.manual_seed(4)
+    dt = torch.bfloat16 if dtype == "bf16" else torch.float32
+    x, r, dy = (torch.randn((b, d, L), generator=gen, device=dev).to(dt) for _ in range(3))
+    r[:, :, 20::30] = torch.finfo(dt).max
+    A = -torch.rand(d, generator=gen, device=dev) - 0.2
+    kw = dict(gate="softplus", weight=weight)
+    y, ckpt = ssm.ssm_gated_scan_fwd(x, r, A, return_ckpt=True, **kw)
+    g = ssm.ssm_gated_scan_bwd(x, r, A, ckpt=ckpt, dy=dy, **kw)
+    yr, _, _, want = tref.gated(x, r, A, dy=dy, **kw)
+    # the gates are reset every 30 steps, which is all the memory there is
+    slack, half = 32 * ref.EPS32 * 31, ref.HALF[dtype]
+    tref.close(y, yr, half, slack, "y")
+    for k in ("dx", "dr"):
+        tref.close(g[k], want[k], half, 3 * slack, k)
+    for k in ("dA", "dr_bias"):
+        tref.close(g[k], want[k], ref.EPS32, 3 * slack, k, want["size"][k])
