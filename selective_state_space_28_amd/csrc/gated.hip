@@ -180,6 +180,62 @@ __device__ __forceinline__ float through_waves(RowMaps<W>& s, int turn, int w, f
   }
 }
 
+// Where A > 0 the decays grow: over several runs they may multiply past float32
+// while every state is inside it (0 until late, or small), and a composed map would
+// form inf * 0.  A wave with a channel whose decays might pass 2^100 over a block
+// (what is left of the exponents is for the inputs) composes nothing: it takes a step
+// a lane and goes from lane to lane, and the row's other waves have nothing to do
+// (batch 8, dim 5120, L 2048 bf16 without gates, no channel so, one in 100, all:
+// forward 91, 168, 890 us, backward 180, 320, 1950).
+//
+// The largest A log2(e) g of a step that is safe, over a block:
+constexpr float kSafeGrowth = 100.0f / kGatedBlock;
+
+// Whether a channel of the wave may pass it (A2 = A log2 e), as far as A says.
+template <int RULE>
+__device__ __forceinline__ bool grows_fast(float A2) {
+  return __any(A2 > ((RULE & kGateSoftplus) != 0 ? 0.0f : kSafeGrowth));
+}
+
+// Whether one does, anywhere in its row: a sigmoid is at most 1, for a softplus the
+// row's waves look for the largest r.
+template <typename T, int RULE, int W>
+__device__ __forceinline__ bool may_overflow(const T* r, float A2, float rb, const Place<W>& at, const GatedSizes& p,
+                                             float (&s_most)[W > 1 ? W : 1]) {
+  float g = 1.0f;
+  if constexpr ((RULE & kGateSoftplus) != 0) {
+    float most = -__builtin_inff();
+    const int lanes = W == 0 ? p.lanes : 64;
+#pragma unroll 1
+    for (int64_t t = ((int64_t)at.w0 * lanes + at.lane) * kRun; t < p.seqlen; t += (W > 1 ? W : 1) * lanes * kRun) {
+      const int64_t left = p.seqlen - t;
+      float f[kRun];
+      run_floats<T>(load_run(r + t, left < kRun ? (int)left : kRun), f);
+#pragma unroll
+      for (int k = 0; k < kRun; ++k) most = k < left ? __builtin_fmaxf(most, f[k]) : most;
+    }
+    for (int off = 1; off < lanes; off <<= 1) most = __builtin_fmaxf(most, __shfl_xor(most, off));
+    if constexpr (W > 1) {
+      if (at.lane == 0) s_most[at.w0] = most;
+      __syncthreads();
+      for (int w = 0; w < W; ++w) most = __builtin_fmaxf(most, s_most[w]);
+    }
+    g = softplus_f32(most + rb);
+  }
+  return __any(A2 * g > kSafeGrowth);
+}
+
+// What enters each lane's step: `first` for the row's first lane (as `next` hands
+// it), for the others what `step` makes of the lane before's, known after as many
+// turns as there are lanes before.
+template <typename S, typename N>
+__device__ __forceinline__ float lanes_in_turn(int lanes, float first, S&& step, N&& next) {
+  float in = first;
+#pragma unroll 1
+  for (int n = 1; n < lanes; ++n) in = next(step(in));
+  return in;
+}
+
 }  // namespace
 
 // g of a step from its raw r: nb = -r_bias log2(e).
@@ -198,6 +254,7 @@ __global__ __launch_bounds__(64 * group_waves(W)) void gated_fwd_kernel(
   using ST = Steps<T, W>;
   constexpr int NH = ST::NH, RN = ST::RN;
   [[maybe_unused]] __shared__ RowMaps<W> maps;
+  [[maybe_unused]] __shared__ float s_most[W > 1 ? W : 1];
   const Place<W> at = place_of<W>(p);
   if (W > 0 && !at.live) return;
   const int lane = at.lane, row = at.row, w0 = at.w0;
@@ -208,6 +265,41 @@ __global__ __launch_bounds__(64 * group_waves(W)) void gated_fwd_kernel(
   const int64_t base = (int64_t)row * p.seqlen;
   float H = h0 != nullptr ? h0[row] : 0.0f;
 
+  // the row's steps in turn
+  auto in_turn = [&] {
+    const int lanes = W == 0 ? p.lanes : 64, place = threadIdx.x & 63;
+#pragma unroll 1
+    for (int c = 0; c < p.seqlen; c += lanes) {
+      const int t = c + lane;
+      const bool in = at.live && t < p.seqlen;
+      float a = 1.0f, q = 0.0f;
+      if (in) {
+        const Gate g = gate_of<RULE>(gate_value<RULE>(Elem<T>::load(r + base + t), rb, nrb), A2);
+        a = starts != nullptr && starts[(int64_t)b * p.seqlen + t] != 0 ? 0.0f : g.a;
+        q = g.w * Elem<T>::load(x + base + t);
+        if constexpr (IG) q *= sigmoid_f32(Elem<T>::load(ig + base + t), nib);
+      }
+      auto step = [&](float v) { return apply_map<true>(a, q, v); };
+      const float from = lanes_in_turn(lanes, H, step, [&](float v) {
+        const float before = lane_before(v, H);
+        return lane == 0 ? H : before;
+      });
+      const float h = step(from);
+      if (in) {
+        if (ckpt != nullptr && t % kGatedBlock == 0) ckpt[((int64_t)b * p.nblk + t / kGatedBlock) * p.dim + d] = from;
+        float o = h;
+        if constexpr (ZG) o *= silu_f32(Elem<T>::load(z + base + t));
+        Elem<T>::store(y + base + t, o);
+      }
+      H = __shfl(h, place | (lanes - 1));
+    }
+  };
+
+  // whether the row cannot be composed
+  auto must_turn = [&] {
+    return grows_fast<RULE>(A2) && may_overflow<T, RULE, W>(r + base, A2, rb, at, p, s_most);
+  };
+
   // one block a wave; WHOLE: every step of the W blocks is in the row; ONCE:
   // inputs read past the caches
   auto blocks = [&](int b0, int turn, auto whole, auto once) {
@@ -215,10 +307,23 @@ __global__ __launch_bounds__(64 * group_waves(W)) void gated_fwd_kernel(
     const int blk = b0 + w0;  // past the last block: no steps, the identity
     const int64_t t0 = (int64_t)blk * kGatedBlock + lane * RN;
     const int64_t left = WHOLE ? kGatedBlock : at.live ? p.seqlen - t0 : 0;
-    const RunWords<T> wr = ST::template load<ONCE>(r + base + t0, left), wx = ST::template load<ONCE>(x + base + t0, left);
-    RunWords<T> wi, wz;
-    if constexpr (IG) wi = ST::template load<ONCE>(ig + base + t0, left);
-    if constexpr (ZG) wz = ST::template load<ONCE>(z + base + t0, left);
+    RunWords<T> wr, wx, wi, wz;
+    auto load = [&] {
+      wr = ST::template load<ONCE>(r + base + t0, left);
+      wx = ST::template load<ONCE>(x + base + t0, left);
+      if constexpr (IG) wi = ST::template load<ONCE>(ig + base + t0, left);
+      if constexpr (ZG) wz = ST::template load<ONCE>(z + base + t0, left);
+    };
+    load();
+    if constexpr (W == 0) {
+      // Asked with the rows' only loads on their way, which would else wait for A (batch
+      // 64, dim 1536, L 200 float32: 72 us, 80); they are not held meanwhile.
+      if (grows_fast<RULE>(A2)) {
+        if (must_turn()) return in_turn();
+        asm volatile("" ::: "memory");
+        load();
+      }
+    }
     uint32_t cut = 0;
     if (starts != nullptr) cut = ST::starts(starts + (int64_t)b * p.seqlen + t0, left);
     const uint32_t in = WHOLE ? ~0u : ST::inside(left);
@@ -296,6 +401,8 @@ __global__ __launch_bounds__(64 * group_waves(W)) void gated_fwd_kernel(
   };
   if constexpr (W == 0) {
     blocks(0, 0, BoolC<false>{}, BoolC<false>{});
+  } else if (must_turn()) {
+    if (w0 == 0) in_turn();
   } else {
     int b0 = 0, turn = 0;
     auto wholes = [&](auto once) {
@@ -319,6 +426,7 @@ __global__ __launch_bounds__(64 * group_waves(W)) void gated_bwd_kernel(
   using ST = Steps<T, W>;
   constexpr int NH = ST::NH, RN = ST::RN;
   [[maybe_unused]] __shared__ RowMaps<W> maps;
+  [[maybe_unused]] __shared__ float s_most[W > 1 ? W : 1];
   const Place<W> at = place_of<W>(p);
   if (W > 0 && !at.live) return;
   const int lane = at.lane, row = at.row, w0 = at.w0;
@@ -331,6 +439,101 @@ __global__ __launch_bounds__(64 * group_waves(W)) void gated_bwd_kernel(
   // the row's sums, over up to 2^31 steps: in float64 across blocks
   double sA = 0.0, srb = 0.0, sib = 0.0;
 
+  // the row's steps in turn, a block's states first (those that enter its 8 pieces
+  // and less are kept, each lane its own copy)
+  __shared__ float s_enter[W == 1 || W == 0 ? group_waves(W) : 1][8][64];
+  auto in_turn = [&] {
+    const int lanes = W == 0 ? p.lanes : 64, place = threadIdx.x & 63;
+    float(*const enter)[64] = s_enter[W <= 1 ? threadIdx.x >> 6 : 0];
+#pragma unroll 1
+    for (int blk = p.nblk - 1; blk >= 0; --blk) {
+      const int t0 = blk * kGatedBlock;
+      const int steps = p.seqlen - t0 < kGatedBlock ? p.seqlen - t0 : kGatedBlock;
+      const int pieces = (steps + lanes - 1) / lanes;
+      float from = ckpt[((int64_t)b * p.nblk + blk) * p.dim + d];
+#pragma unroll 1
+      for (int n = 0; n < 2 * pieces - 1; ++n) {
+        const bool ahead = n < pieces - 1;  // only the states
+        const int c = ahead ? n : 2 * pieces - 2 - n;
+        const int t = t0 + c * lanes + lane;
+        const bool in = at.live && t < p.seqlen;
+        const bool cut = in && starts != nullptr && starts[(int64_t)b * p.seqlen + t] != 0;
+        float v = 0.0f, slope = 0.0f, u = 0.0f, xv = 0.0f, s_i = 1.0f, c_i = 0.0f;
+        Gate g{0.0f, 0.0f, 1.0f, 0.0f};
+        if (in) {
+          const float rv = Elem<T>::load(r + base + t);
+          if constexpr ((RULE & kGateSoftplus) != 0) {
+            softplus_pair(rv + rb, v, slope);
+          } else {
+            float comp;
+            sigmoid_pair(rv, nrb, v, comp);
+            slope = v * comp;
+          }
+          g = gate_of<RULE>(v, A2);
+          if ((RULE & kGateSoftplus) != 0 && !(g.a > kMinNormal)) v = 0.0f;  // (as below)
+          u = xv = Elem<T>::load(x + base + t);
+          if constexpr (IG) {
+            sigmoid_pair(Elem<T>::load(ig + base + t), nib, s_i, c_i);
+            u *= s_i;
+          }
+        }
+        const float q = g.w * u;
+        if (!ahead && c < pieces - 1) from = enter[c][place];
+        else enter[c][place] = from;
+        auto step = [&](float h) { return apply_map<true>(cut ? 0.0f : g.a, q, h); };
+        float hb = lanes_in_turn(lanes, from, step, [&](float h) {
+          const float before = lane_before(h, from);
+          return lane == 0 ? from : before;
+        });
+        const float h = step(hb);
+        if (ahead) {
+          from = __shfl(h, place | (lanes - 1));
+          continue;
+        }
+        if (cut) hb = 0.0f;
+        float dh = in ? Elem<T>::load(dy + base + t) : 0.0f;
+        if constexpr (ZG) {
+          if (in) {
+            const float zv = Elem<T>::load(z + base + t);
+            float s, c_z;
+            sigmoid_pair(zv, 0.0f, s, c_z);
+            const float ds = dh * s;
+            Elem<T>::store(dz + base + t, ds * h * __builtin_fmaf(zv, c_z, 1.0f));
+            dh = ds * zv;
+          }
+        }
+        auto back = [&](float m) { return cut ? 0.0f : g.a * (dh + m); };
+        const float m = lanes_in_turn(lanes, M, back, [&](float w) {
+          const float after = lane_after(w, M);
+          return at.last ? M : after;
+        });
+        M = __shfl(back(m), place & ~(lanes - 1));
+        if (in) {  // the gradients of the step, as below
+          const float lam = dh + m;
+          float bend = g.a * u;
+          if constexpr ((RULE & kGateUnit) != 0) bend = g.w > 0.0f ? bend * g.a * rcp_hw(g.w) : 0.0f;
+          const float de = lam * __builtin_fmaf(g.a, hb, -bend);
+          const float o = de * (slope * Ad);
+          Elem<T>::store(dr + base + t, o);
+          sA += (double)(de * v);
+          srb += (double)o;
+          float ox = lam * g.w;
+          if constexpr (IG) {
+            ox *= s_i;
+            const float oi = ox * xv * c_i;
+            Elem<T>::store(di + base + t, oi);
+            sib += (double)oi;
+          }
+          Elem<T>::store(dx + base + t, ox);
+        }
+      }
+    }
+  };
+
+  // whether the row cannot be composed
+  auto must_turn = [&] {
+    return grows_fast<RULE>(A2) && may_overflow<T, RULE, W>(r + base, A2, rb, at, p, s_most);
+  };
   auto blocks = [&](int b0, int turn, auto whole, auto once) {
     constexpr bool WHOLE = decltype(whole)::value, ONCE = decltype(once)::value;
     const int blk = b0 + w0;  // past the last block: no steps, the identity
@@ -504,7 +707,9 @@ __global__ __launch_bounds__(64 * group_waves(W)) void gated_bwd_kernel(
     srb += (double)prb;
     if constexpr (IG) sib += (double)pib;
   };
-  if constexpr (W == 0) {
+  if (must_turn()) {
+    if (w0 == 0) in_turn();
+  } else if constexpr (W == 0) {
     blocks(0, 0, BoolC<false>{}, BoolC<false>{});
   } else {
     int b0 = (p.nblk - 1) / W * W, turn = 0;

@@ -1,5 +1,6 @@
 """GPU tests of the gated recurrence and the layer norm, and of the one-token
 steps, at the ends of their sizes and of float32's range."""
+import numpy as np
 import pytest
 
 from tests import layers_ref as ref
@@ -167,3 +168,163 @@ def test_a_gate_of_the_types_largest_value(dev, dtype, b, d, L, weight):
         tref.close(g[k], want[k], half, 3 * slack, k)
     for k in ("dA", "dr_bias"):
         tref.close(g[k], want[k], ref.EPS32, 3 * slack, k, want["size"][k])
+
+
+# Rows that share a wave, a wave to a row of one block and of several, four and sixteen waves to a row.
+GROWING = [(2, 9, 200), (1, 5, 512), (2, 4100, 1300), (2, 3, 1300), (2, 3, 5000)]
+
+
+# A sigmoid and a softplus near r = 0, and a softplus whose size is its own.
+GATES = [("sigmoid", 0.0), ("softplus", 0.0), ("softplus", 500.0)]
+
+
+def growing(dev, dtype, b, d, L, total, seed, gate="sigmoid", r0=0.0):
+    """Channels with A > 0 whose state grows by e^total or a little more in one block of 512 steps (all of a shorter
+    row), where r is about r0, and is kept outside it, between channels that decay.  Returns x, r, A and the block's
+    first and end step."""
+    import torch
+    gen = torch.Generator(device=dev)
+    gen.manual_seed(seed)
+    s, e = (0, L) if L <= 512 else (512, 1024)
+    dt = torch.bfloat16 if dtype == "bf16" else torch.float32
+    r = torch.full((b, d, L), -60.0, device=dev, dtype=dt)
+    r[:, :, s:e] = (r0 + 0.1 * torch.randn((b, d, e - s), generator=gen, device=dev)).to(dt)
+    size = 0.5 if gate == "sigmoid" else float(np.logaddexp(0, r0))
+    A = torch.full((d,), total / size / (e - s), device=dev) * (1 + 0.1 * torch.rand(d, generator=gen, device=dev))
+    A[1::3] *= -1
+    return torch.randn((b, d, L), generator=gen, device=dev).to(dt), r, A, s, e
+
+
+def grown_close(got, want, size, half, L, what):
+    """|got - want| <= half |want| + 32 2^-24 L times the sum of the terms' sizes: a state of step t is a sum of
+    products of up to t decays, each off by at most 32 half steps of float32 (the decays' own tolerance)."""
+    import torch
+    assert bool(torch.isfinite(got).all()), f"{what}: non-finite values"
+    bound = half * want.abs() + 32 * ref.EPS32 * L * size.abs() + 1e-37
+    worst = ((got.double() - want).abs() / bound).max().item()
+    assert worst <= 1.0, f"{what}: error {worst:.2f} times the bound"
+
+
+@pytest.mark.parametrize("packed", [False, True])
+@pytest.mark.parametrize("gate,r0", GATES)
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("b,d,L", GROWING)
+def test_growth_past_float32_from_a_zero_state(dev, dtype, b, d, L, gate, r0, packed):
+    """A > 0: the decays of a block multiply to e^400, but nothing enters the state before the last eighth of it."""
+    import torch
+    import selective_state_space_28_amd as ssm
+    x, r, A, s, e = growing(dev, dtype, b, d, L, 400.0, 1, gate, r0)
+    x[:, :, :e - (e - s) // 8] = 0
+    x[:, :, e:] = 0
+    starts = None
+    if packed:
+        starts = torch.zeros((b, L), dtype=torch.uint8, device=dev)
+        starts[:, [0, s + 9]] = 1
+    kw = dict(gate=gate, weight="convex", starts=starts)
+    y, last, ckpt = ssm.ssm_gated_scan_fwd(x, r, A, return_last_state=True, return_ckpt=True, **kw)
+    yr, lr, before = tref.gated(x, r, A, **kw)
+    size = tref.gated(x.abs(), r, A, **kw)  # (the weights of a growing channel are all of one sign)
+    half = ref.HALF[dtype]
+    grown_close(y, yr, size[0], half, L, "y")
+    grown_close(last, lr, size[1], ref.EPS32, L, "last_state")
+    grown_close(ckpt.transpose(1, 2), before[:, :, ::512], size[2][:, :, ::512], ref.EPS32, L, "ckpt")
+
+
+@pytest.mark.parametrize("b,d,L", GROWING)
+def test_growth_of_a_small_state(dev, b, d, L):
+    """A > 0: the decays of a block multiply past float32, the state that they grow was 1e-30 and stays inside it."""
+    import torch
+    import selective_state_space_28_amd as ssm
+    x, r, A, s, e = growing(dev, "f32", b, d, L, 95.0, 2)
+    x.zero_()
+    h0 = torch.full((b, d), 1e-30, device=dev)
+    h0[:, ::2] *= -1
+    y, last = ssm.ssm_gated_scan_fwd(x, r, A, weight="convex", h0=h0, return_last_state=True)
+    yr, lr, _ = tref.gated(x, r, A, weight="convex", h0=h0)
+    # (from 1e-30 on the decaying channels fall below the smallest normal float, where only its size is left)
+    grown_close(y, yr, yr, ref.EPS32, L, "y")
+    grown_close(last, lr, lr, ref.EPS32, L, "last_state")
+
+
+def test_growth_past_float32(dev):
+    """A state that leaves float32's range is infinite from there on, of its sign, and finite before."""
+    import selective_state_space_28_amd as ssm
+    for b, d, L in GROWING:
+        x, r, A, s, e = growing(dev, "f32", b, d, L, 300.0, 3)
+        y = ssm.ssm_gated_scan_fwd(x, r, A, weight="convex").double()
+        yr = tref.gated(x, r, A, weight="convex")[0]
+        size = tref.gated(x.abs(), r, A, weight="convex")[0].abs()
+        inside, outside = size < 1e38, yr.abs() > 1e39
+        assert bool(outside.any()) and bool((outside | inside)[:, 1::3].all())
+        grown_close(y[inside], yr[inside], size[inside], ref.EPS32, L, "y")
+        assert bool((y[outside] == yr[outside].sign() * float("inf")).all())
+
+
+@pytest.mark.parametrize("packed", [False, True])
+@pytest.mark.parametrize("gate,r0", GATES)
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("b,d,L", GROWING)
+def test_gradients_of_growth_past_float32(dev, dtype, b, d, L, gate, r0, packed):
+    """A > 0: the decays of a block multiply past float32, while every state (of inputs to the block's last 0.6 alone)
+    and adjoint (of gradients from its first 0.6 alone) stays inside it."""
+    import torch
+    import selective_state_space_28_amd as ssm
+    x, r, A, s, e = growing(dev, dtype, b, d, L, 105.0, 4, gate, r0)
+    dy = torch.randn(x.shape, generator=torch.Generator(device=dev).manual_seed(5), device=dev).to(x.dtype)
+    n = e - s
+    x[:, :, :s + int(0.4 * n)] = 0
+    dy[:, :, s + int(0.6 * n):] = 0
+    starts = None
+    if packed:
+        starts = torch.zeros((b, L), dtype=torch.uint8, device=dev)
+        starts[:, 0] = 1
+    kw = dict(gate=gate, weight="convex", starts=starts)
+    _, ckpt = ssm.ssm_gated_scan_fwd(x, r, A, return_ckpt=True, **kw)
+    g = ssm.ssm_gated_scan_bwd(x, r, A, ckpt=ckpt, dy=dy, **kw)
+    want = tref.gated(x, r, A, dy=dy, **kw)[3]
+    size = tref.gated(x.abs(), r, A, dy=dy.abs(), **kw)[3]
+    half = ref.HALF[dtype]
+    grown_close(g["dx"], want["dx"], size["dx"], half, L, "dx")
+    # (a state and an adjoint: twice the error, and a gate's slope)
+    grown_close(g["dr"], want["dr"], size["size"]["dr_terms"], half, 3 * L, "dr")
+    grown_close(g["dA"], want["dA"], size["size"]["dA_terms"], ref.EPS32, 3 * L, "dA")
+    grown_close(g["dh0"], want["dh0"], size["dh0"], ref.EPS32, L, "dh0")
+
+
+@pytest.mark.parametrize("i,z", [(True, True), (False, False)])
+@pytest.mark.parametrize("gate", ["sigmoid", "softplus"])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("rate,b,d,L", [(2e-3, *c) for c in GROWING] + [(0.2, 2, 9, 200), (0.15, 3, 40, 400)])
+def test_some_channels_grow(dev, rate, b, d, L, dtype, gate, i, z):
+    """Every second channel with A up to `rate`: slow growth, where maps are composed, and growth on both sides of the
+    border past which they are not."""
+    import torch
+    import selective_state_space_28_amd as ssm
+    gen = torch.Generator(device=dev)
+    gen.manual_seed(11)
+    dt = torch.bfloat16 if dtype == "bf16" else torch.float32
+    x, r, dy, gi, gz = (torch.randn((b, d, L), generator=gen, device=dev).to(dt) for _ in range(5))
+    A = rate * torch.rand(d, generator=gen, device=dev)
+    A[1::2] = -torch.rand(A[1::2].shape, generator=gen, device=dev) - 0.1
+    h0, dl = (torch.randn((b, d), generator=gen, device=dev) for _ in range(2))
+    gi, gz = gi if i else None, gz if z else None
+    kw = dict(gate=gate, weight="convex")
+    y, last, ckpt = ssm.ssm_gated_scan_fwd(x, r, A, None, gi, None, gz, h0=h0, return_last_state=True, return_ckpt=True, **kw)
+    g = ssm.ssm_gated_scan_bwd(x, r, A, None, gi, None, gz, ckpt=ckpt, dy=dy, dlast_state=dl, **kw)
+    yr, lr, before, want = tref.gated(x, r, A, None, gi, None, gz, h0=h0, dy=dy, dlast=dl, **kw)
+    # sizes of the terms: with every input positive (negative where the weight is)
+    sign = torch.where(A > 0, -1.0, 1.0)[:, None]
+    size = tref.gated((x.abs() * sign).to(dt), r, A, None, gi, None, None if gz is None else gz.abs(), h0=h0.abs(),
+                      dy=dy.abs(), dlast=dl.abs(), **kw)
+    half = ref.HALF[dtype]
+    grown_close(y, yr, size[0], half, L, "y")
+    grown_close(last, lr, size[1], ref.EPS32, L, "last_state")
+    grown_close(ckpt.transpose(1, 2), before[:, :, ::512], size[2][:, :, ::512], ref.EPS32, L, "ckpt")
+    # (silu of |z| bounds that of z, and so do its slopes' sizes up to 1.1; a gradient has three such factors)
+    for k in ("dx", "dz", "di"):
+        if want[k] is not None:
+            grown_close(g[k], want[k], 1.1 * size[3][k].abs() + want[k].abs(), half, 3 * L, k)
+    grown_close(g["dr"], want["dr"], size[3]["size"]["dr_terms"], half, 3 * L, "dr")
+    grown_close(g["dA"], want["dA"], size[3]["size"]["dA_terms"], ref.EPS32, 3 * L, "dA")
+    grown_close(g["dr_bias"], want["dr_bias"], size[3]["size"]["dr_terms"].sum((0, 2)), ref.EPS32, 3 * L, "dr_bias")
+    grown_close(g["dh0"], want["dh0"], size[3]["dh0"], ref.EPS32, 3 * L, "dh0")
