@@ -212,6 +212,13 @@ __global__ __launch_bounds__(1024) void norm_rows_bwd_kernel(
     for (int c = 0; c < K; ++c) {
       run_floats<T>(wx[c], xh[c]);
       run_floats<T>(wd[c], g[c]);
+      // Past the end dy is 0, but a zero less a far mean, times rstd, may be infinite:
+      // x is the mean there.
+      const int at = (c * p.span + p.lane) * kRun;
+      if (dim - at < kRun) {
+#pragma unroll
+        for (int k = 0; k < kRun; ++k) xh[c][k] = at + k < dim ? xh[c][k] : mu;
+      }
 #pragma unroll
       for (int k = 0; k < kRun; ++k) {
         xh[c][k] = (xh[c][k] - mu) * rs;

@@ -365,3 +365,28 @@ def test_tokens_of_the_types_lowest_value(dev, dtype, shape, axis):
     assert bool((y == b.view(wide).to(x.dtype))[at].all())
     free = torch.where(at, torch.zeros_like(x), x)
     assert torch.equal(y[~at], ssm.ssm_layer_norm_fwd(free, w, b, axis=axis)[~at])
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("shape,axis", LOWEST)
+def test_gradients_of_tokens_of_the_types_lowest_value(dev, dtype, shape, axis):
+    """xhat is 0 in all their channels: dx = rstd (dn - mean(dn)), and nothing of them in dweight.  The tolerances are
+    those of the norm's other tests: 128 half steps of float32 of the largest value, for each addition of a sum one
+    more of its terms, and the rounding of bf16."""
+    import torch
+    import selective_state_space_28_amd as ssm
+    x, dy, w, _, masked = masked_tokens(dev, dtype, shape, axis)
+    mean, rstd = x.double().mean(axis), (x.double().var(axis, unbiased=False) + 1e-5).rsqrt()
+    mean[masked], rstd[masked] = torch.finfo(x.dtype).min, 1e-5 ** -0.5
+    mean, rstd = mean.float(), rstd.float()
+    g = ssm.ssm_layer_norm_bwd(x, w, mean, rstd, dy, axis=axis)
+    wide = [1] * len(shape)
+    wide[axis] = -1
+    rs, d64 = rstd.double().unsqueeze(axis), dy.double()
+    xh, dn = (x.double() - mean.double().unsqueeze(axis)) * rs, dy.double() * w.double().view(wide)
+    over = [k for k in range(len(shape)) if k != axis % len(shape)]
+    slack, half = 128 * ref.EPS32, ref.HALF[dtype]
+    dx = rs * (dn - dn.mean(axis, keepdim=True) - xh * (dn * xh).mean(axis, keepdim=True))
+    tref.close(g["dx"], dx, half, slack, "dx")
+    tref.close(g["dweight"], (d64 * xh).sum(over), ref.EPS32, slack, "dweight", (d64 * xh).abs().sum(over))
+    tref.close(g["dbias"], d64.sum(over), ref.EPS32, slack, "dbias", d64.abs().sum(over))
