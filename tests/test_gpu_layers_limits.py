@@ -390,3 +390,32 @@ def test_gradients_of_tokens_of_the_types_lowest_value(dev, dtype, shape, axis):
     tref.close(g["dx"], dx, half, slack, "dx")
     tref.close(g["dweight"], (d64 * xh).sum(over), ref.EPS32, slack, "dweight", (d64 * xh).abs().sum(over))
     tref.close(g["dbias"], d64.sum(over), ref.EPS32, slack, "dbias", d64.abs().sum(over))
+
+
+@pytest.mark.parametrize("gate", ["sigmoid", "softplus"])
+@pytest.mark.parametrize("weight", ["unit", "convex"])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("L,cut", [(90, 41), (1300, 777)])
+def test_padding_with_the_types_lowest_value(dev, dtype, gate, weight, L, cut):
+    """A step whose r is finfo.min is the identity, as one with -inf: the same bits, whatever i and z hold."""
+    import torch
+    import selective_state_space_28_amd as ssm
+    gen = torch.Generator(device=dev)
+    gen.manual_seed(13)
+    dt = torch.bfloat16 if dtype == "bf16" else torch.float32
+    x, r, i, z, dy = (torch.randn((2, 5, L), generator=gen, device=dev).to(dt) for _ in range(5))
+    A = -torch.rand(5, generator=gen, device=dev) - 0.2
+    dy[1, :, cut:] = 0
+    i[1, :, cut:] = torch.finfo(dt).min
+    z[1, :, cut:] = torch.finfo(dt).max
+    kw = dict(gate=gate, weight=weight)
+    got = []
+    for pad in (-float("inf"), torch.finfo(dt).min):
+        r[1, :, cut:] = pad
+        y, last, ckpt = ssm.ssm_gated_scan_fwd(x, r, A, None, i, None, z, return_last_state=True, return_ckpt=True, **kw)
+        g = ssm.ssm_gated_scan_bwd(x, r, A, None, i, None, z, ckpt=ckpt, dy=dy, **kw)
+        got.append([y[:, :, :cut], last, ckpt] + [g[k] for k in sorted(g)])
+    assert all(torch.equal(u, v) and bool(torch.isfinite(u).all()) for u, v in zip(*got))
+    rows = [v[1:2, :, :cut].contiguous() for v in (x, r, i, z)]
+    _, one = ssm.ssm_gated_scan_fwd(rows[0], rows[1], A, None, rows[2], None, rows[3], return_last_state=True, **kw)
+    assert torch.equal(got[1][1][1], one[0])
