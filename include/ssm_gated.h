@@ -34,14 +34,15 @@
  *    gradient and no NaN or Inf crosses a start.  NULL -> none.
  *  - Pointers need their element's alignment only; rows of any length and
  *    alignment take the same vector accesses.
- *  - A padded batch: a step with r = -inf (and finite x) is the identity,
- *    a_t = 1 and w_t = 0, under either gate, so last_state and the gradients
- *    are those of the steps before it.
+ *  - A padded batch: a step with r = -inf or the type's lowest value (and
+ *    finite x and z, and no NaN in i) is the identity, a_t = 1 and w_t = 0,
+ *    under either gate, so last_state and the gradients are those of the steps
+ *    before it.
  *  - A is not checked for sign; A > 0 grows (and w_t is then negative, or NaN
  *    with SSM_GATE_UNIT), and a state that leaves float32's range is infinite
  *    from there on (a decay that does so in one step is infinite, and NaN times
  *    a state of 0).  Channels whose decays might multiply past 2^100 over 512
- *    steps (A > 0.135 with a sigmoid) are scanned a step at a time, up to 40
+ *    steps (A > 0.135 with a sigmoid) are scanned a step at a time, up to 45
  *    times slower.  A decay that underflows is held at the smallest normal
  *    float, so an infinite state stays infinite until the next start.
  *  - Where w_t = 0 under SSM_GATE_UNIT (A g = 0), the square root's infinite

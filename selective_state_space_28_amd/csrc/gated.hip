@@ -810,10 +810,14 @@ hipError_t by_rule(const GatedLaunch& a, F&& f) {
 }
 
 // Waves to a row: several rows to a wave up to half a wave's block (0); one where
-// the rows alone make the 8192 waves that fill the chip, more where they do not
-// and the sequence has blocks for them (batch 1,
-// dim 2048, L 65536 bf16: one 266 us, four 234, sixteen 238; batch 3, dim 1000,
-// L 1777 float32: 23.4, 22.6, 68; batch 8, dim 5120, L 2048, backward: 231, 257).
+// the rows alone make the 8192 waves that fill the chip (batch 8, dim 5120, L 2048,
+// backward: 231 us, with four 257), more where they do not and the sequence has
+// blocks for them (batch 3, dim 1000, L 1777 float32: one 23.4, four 22.6, sixteen 68;
+// batch 1, dim 2048, L 65536 bf16: 266, 234, 238).  Sixteen for the fewest rows, by
+// what it gives in long ones (batch 1, L 65536 bf16, both gates, forward and backward
+// with sixteen, with four: dim 64 28 and 45 us, 41 and 65; dim 512 60 and 122, 61 and
+// 121; dim 1500 179 and 345, 199 and 370); in short ones it costs (dim 1500, L 8192: 31
+// and 52, 23 and 39; L 4096: 24 and 51, 13 and 23; dim 512 the same at both).
 int waves_of(const GatedLaunch& a) {
   const int64_t rows = (int64_t)a.batch * a.dim, nblk = (a.seqlen + kGatedBlock - 1) / kGatedBlock;
   if (a.seqlen <= 256) return 0;

@@ -1052,13 +1052,16 @@ struct ColPlan {
   size_t room;
 };
 
-// What a column kernel holds: accesses in registers (the first two where two
-// workgroups of a CU can run, the last with the registers of a CU to one), most
+// What a column kernel holds: accesses in registers (the first two with half a CU's
+// LDS, the last with the registers and LDS of a CU to one workgroup), most
 // workgroups, parameters (and sums of their gradients) a channel and the most
 // channels for which they wait in LDS, arrays that it holds pieces of.
-// Workgroups: the backward's each leave a part of dweight and dbias, so one for
-// each CU (batch 8, dim 1536, L 2047 float32: 88 us, with two 97); the
-// forward's two (batch 16, dim 5120, L 2048 bf16: 164 us, with one 170).
+// Workgroups: the forward's are two for each CU (batch 16, dim 5120, L 2048 bf16:
+// 164 us, with one 170).  The backward's each leave a part of dweight and dbias, so
+// one for each CU, whatever it holds (batch 8, dim 1536, L 2047 float32: 88 us, with
+// two 97); its smaller plan, which in bf16 builds to 129 registers and could not run
+// twice on a CU, is there for what needs no more (batch 8, L 2048 bf16: dim 500 17 us,
+// 768 27, 1536 39).
 struct ColKind {
   int held[3], groups, params, lds_dim, arrays;
 };
@@ -1111,8 +1114,8 @@ ColPlan col_plan(const ColKind& kind, int batch, int dim, int64_t seqlen, int el
   p.all = batch * p.tiles;
   p.groups = p.all < kind.groups ? p.all : kind.groups;
   // A CU's 160 KiB of LDS, or half of them, less the sums' static arrays.  Two
-  // workgroups of a CU overlap one's loads with the other's stores, so they are
-  // taken as long as they hold all but an access of a wave (batch 16, L 2048
+  // workgroups of a CU overlap one's loads with the other's stores, so the forward
+  // takes them as long as they hold all but an access of a wave (batch 16, L 2048
   // bf16, dim 768: 20 us, one workgroup with 40 accesses held 35).
   const int each = (need + p.waves - 1) / p.waves;
   p.room = (size_t)75 * 1024;
