@@ -419,3 +419,46 @@ def test_padding_with_the_types_lowest_value(dev, dtype, gate, weight, L, cut):
     rows = [v[1:2, :, :cut].contiguous() for v in (x, r, i, z)]
     _, one = ssm.ssm_gated_scan_fwd(rows[0], rows[1], A, None, rows[2], None, rows[3], return_last_state=True, **kw)
     assert torch.equal(got[1][1][1], one[0])
+
+
+@pytest.mark.parametrize("i,z", [(True, True), (True, False), (False, True)])
+@pytest.mark.parametrize("gate", ["sigmoid", "softplus"])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("b,d,L", [(3, 7, 5), (2, 9, 200), (1, 5, 511), (2, 4100, 520), (2, 3, 1300), (2, 3, 5000)])
+def test_packed_channels_that_grow_fast(dev, b, d, L, dtype, gate, i, z):
+    """Growth that is gone through step by step, with every gate and sequences of some 20 steps, beside channels that
+    decay (which a wave of several rows takes along)."""
+    import torch
+    import selective_state_space_28_amd as ssm
+    gen = torch.Generator(device=dev)
+    gen.manual_seed(14)
+    dt = torch.bfloat16 if dtype == "bf16" else torch.float32
+    x, r, dy, gi, gz = (torch.randn((b, d, L), generator=gen, device=dev).to(dt) for _ in range(5))
+    A = 0.14 + 0.1 * torch.rand(d, generator=gen, device=dev)
+    A[1::2] = -torch.rand(A[1::2].shape, generator=gen, device=dev) - 0.1
+    starts = torch.rand((b, L), generator=gen, device=dev) < 0.05
+    h0, dl, rb = (torch.randn(s, generator=gen, device=dev) for s in ((b, d), (b, d), (d,)))
+    gi, gz, ib = gi if i else None, gz if z else None, rb.flip(0).contiguous() if i else None
+    kw = dict(gate=gate, weight="convex", starts=starts)
+    y, last, ckpt = ssm.ssm_gated_scan_fwd(x, r, A, rb, gi, ib, gz, h0=h0, return_last_state=True, return_ckpt=True, **kw)
+    g = ssm.ssm_gated_scan_bwd(x, r, A, rb, gi, ib, gz, ckpt=ckpt, dy=dy, dlast_state=dl, **kw)
+    yr, lr, _, want = tref.gated(x, r, A, rb, gi, ib, gz, h0=h0, dy=dy, dlast=dl, **kw)
+    # sizes of the terms, as above; an error stays in its sequence (some 200 steps at the most, 300 are counted)
+    sign = torch.where(A > 0, -1.0, 1.0)[:, None]
+    size = tref.gated((x.abs() * sign).to(dt), r, A, rb, gi, ib, None if gz is None else gz.abs(), h0=h0.abs(),
+                      dy=dy.abs(), dlast=dl.abs(), **kw)
+    half, n = ref.HALF[dtype], min(L, 300)
+    grown_close(y, yr, size[0], half, n, "y")
+    grown_close(last, lr, size[1], ref.EPS32, n, "last_state")
+    for k in ("dx", "dz", "di"):
+        if want[k] is not None:
+            grown_close(g[k], want[k], 1.1 * size[3][k].abs() + want[k].abs(), half, 3 * n, k)
+    grown_close(g["dr"], want["dr"], size[3]["size"]["dr_terms"], half, 3 * n, "dr")
+    grown_close(g["dA"], want["dA"], size[3]["size"]["dA_terms"], ref.EPS32, 3 * n, "dA")
+    grown_close(g["dr_bias"], want["dr_bias"], size[3]["size"]["dr_terms"].sum((0, 2)), ref.EPS32, 3 * n, "dr_bias")
+    if i:
+        grown_close(g["di_bias"], want["di_bias"], (1.1 * size[3]["di"].abs() + want["di"].abs()).sum((0, 2)),
+                    ref.EPS32, 3 * n, "di_bias")
+    grown_close(g["dh0"], want["dh0"], size[3]["dh0"], ref.EPS32, 3 * n, "dh0")
+    again = ssm.ssm_gated_scan_bwd(x, r, A, rb, gi, ib, gz, ckpt=ckpt, dy=dy, dlast_state=dl, **kw)
+    assert all(torch.equal(g[k], again[k]) for k in g if g[k] is not None)
