@@ -25,7 +25,8 @@
  *  - Every sum is held in float32 or wider, the variance taken about the mean;
  *    y and dx are rounded once.  A token of equal values has exactly that mean
  *    and variance 0: y is the bias (NaN where eps is 0 too).  Where the squares
- *    of a token's deviations pass float32's range, rstd is 0 and y the bias.
+ *    of a token's deviations pass float32's range, rstd is 0 and y the bias
+ *    (or NaN, where a deviation passes it itself).
  *  - A NaN or Inf in one token makes that token's y (and dx) NaN where the
  *    formula does and leaves the other tokens alone.
  */
