@@ -26,10 +26,22 @@ Beside them a gated linear recurrence with one state per channel
     y = ssm_gated_state_update(state, x, r, A, r_bias, i, i_bias, z)
     y, s, mean, rstd = ssm_layer_norm_fwd(x, weight, bias, residual, return_stats=True)
     grads = ssm_layer_norm_bwd(s, weight, mean, rstd, dy, dsum)
+
+And linear attention with a decay for each head (include/ssm_linear_attn.h) with
+the norm of its heads' outputs and their gate (include/ssm_group_norm.h):
+
+    y, last = ssm_linear_attn_fwd(q, k, v, log_decay, h0=h0, return_last_state=True)
+    grads = ssm_linear_attn_bwd(q, k, v, log_decay, h0=h0, dy=dy, dlast_state=dlast)
+    y = ssm_linear_attn_state_update(state, q, k, v, log_decay)
+    y, mean, rstd = ssm_group_norm_fwd(x, groups, weight, bias, z, act="silu", return_stats=True)
+    grads = ssm_group_norm_bwd(x, groups, weight, bias, z, act="silu", mean=mean, rstd=rstd, dy=dy)
 """
 from __future__ import annotations
 
 from ._lib import SSM_BF16, SSM_F32, SsmError, header_functions, load, status_string  # noqa: F401
+from .heads import (ssm_group_norm_bwd, ssm_group_norm_bwd_workspace_bytes, ssm_group_norm_fwd,  # noqa: F401
+                    ssm_linear_attn_bwd, ssm_linear_attn_bwd_workspace_bytes, ssm_linear_attn_fwd,
+                    ssm_linear_attn_fwd_workspace_bytes, ssm_linear_attn_state_update)
 from .layers import (ssm_gated_scan_bwd, ssm_gated_scan_bwd_workspace_bytes,  # noqa: F401
                      ssm_gated_scan_ckpt_bytes, ssm_gated_scan_fwd, ssm_gated_state_update, ssm_layer_norm_bwd,
                      ssm_layer_norm_bwd_workspace_bytes, ssm_layer_norm_fwd)
@@ -47,4 +59,7 @@ __all__ = ["ssm_scan_fwd", "ssm_scan_fwd_noalloc", "ssm_scan_fwd_workspace_bytes
            "ssm_gated_scan_fwd", "ssm_gated_scan_bwd", "ssm_gated_scan_bwd_workspace_bytes",
            "ssm_gated_scan_ckpt_bytes", "ssm_gated_state_update",
            "ssm_layer_norm_fwd", "ssm_layer_norm_bwd", "ssm_layer_norm_bwd_workspace_bytes",
+           "ssm_linear_attn_fwd", "ssm_linear_attn_fwd_workspace_bytes", "ssm_linear_attn_bwd",
+           "ssm_linear_attn_bwd_workspace_bytes", "ssm_linear_attn_state_update",
+           "ssm_group_norm_fwd", "ssm_group_norm_bwd", "ssm_group_norm_bwd_workspace_bytes",
            "ssm_status_string", "SsmError", "load"]

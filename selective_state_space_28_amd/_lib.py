@@ -1,4 +1,4 @@
-"""ctypes view of libssm.so (include/ssm.h, ssm_gated.h, ssm_norm.h).  Loading fails loudly when the
+"""ctypes view of libssm.so (the headers of include/).  Loading fails loudly when the
 library has not been built: there is no other implementation to fall back to."""
 from __future__ import annotations
 
@@ -11,6 +11,7 @@ from .build import LIB, INCLUDE
 SSM_F32, SSM_BF16 = 0, 1
 SSM_DELTA_SOFTPLUS, SSM_BBAR_ZOH = 1, 2
 SSM_GATE_SOFTPLUS, SSM_GATE_UNIT = 1, 2
+SSM_ACT_NONE, SSM_ACT_SILU, SSM_ACT_SIGMOID = 0, 1, 2
 _lib = None
 
 
@@ -96,6 +97,26 @@ def load():
     lib.ssm_layer_norm_bwd_workspace_bytes.restype = sz
     lib.ssm_layer_norm_bwd.argtypes = [vp, fp, fp, fp, vp, vp, vp, fp, fp, i32, i32, i64, i32, vp, sz, vp]
     lib.ssm_layer_norm_bwd.restype = i32
+    lib.ssm_linear_attn_fwd_workspace_bytes.argtypes = [i32, i64, i32, i32, i32, i32]
+    lib.ssm_linear_attn_fwd_workspace_bytes.restype = sz
+    lib.ssm_linear_attn_fwd.argtypes = [vp, vp, vp, vp, fp, ctypes.c_float, vp, vp, fp, vp, fp, i32, i64, i32, i32, i32, i32,
+                                        i32, i32, i32, vp, sz, vp]
+    lib.ssm_linear_attn_fwd.restype = i32
+    lib.ssm_linear_attn_bwd_workspace_bytes.argtypes = [i32, i64, i32, i32, i32, i32, i32, i32, i32]
+    lib.ssm_linear_attn_bwd_workspace_bytes.restype = sz
+    lib.ssm_linear_attn_bwd.argtypes = [vp, vp, vp, vp, fp, ctypes.c_float, vp, vp, fp, vp, fp, vp, vp, vp, fp, fp,
+                                        i32, i64, i32, i32, i32, i32, i32, i32, i32, vp, sz, vp]
+    lib.ssm_linear_attn_bwd.restype = i32
+    lib.ssm_linear_attn_state_update.argtypes = [fp, vp, vp, vp, vp, fp, ctypes.c_float, vp, vp, fp, i32, i32, i32, i32, i32,
+                                                 i32, i32, i32, vp]
+    lib.ssm_linear_attn_state_update.restype = i32
+    lib.ssm_group_norm_fwd.argtypes = [vp, i64, fp, fp, vp, i64, i32, ctypes.c_float, vp, fp, fp, i64, i32, i32, i32, vp]
+    lib.ssm_group_norm_fwd.restype = i32
+    lib.ssm_group_norm_bwd_workspace_bytes.argtypes = [i64, i32, i32, i32]
+    lib.ssm_group_norm_bwd_workspace_bytes.restype = sz
+    lib.ssm_group_norm_bwd.argtypes = [vp, i64, fp, fp, vp, i64, i32, fp, fp, vp, vp, vp, fp, fp, i64, i32, i32, i32, vp, sz,
+                                       vp]
+    lib.ssm_group_norm_bwd.restype = i32
     lib.ssm_status_string.argtypes = [i32]
     lib.ssm_status_string.restype = ctypes.c_char_p
     _lib = lib

@@ -992,9 +992,14 @@ __global__ __launch_bounds__(1024) void norm_sum_kernel(const float* __restrict_
   if (j == 0 && at < 2 * (int64_t)dim) {
     float t = 0.0f;
     for (int k = 0; k < 32; ++k) t += s[k][threadIdx.x];
-    if (at < dim) dweight[at] = t;
-    else if (dbias != nullptr) dbias[at - dim] = t;
+    float* to = at < dim ? dweight : dbias;
+    if (to != nullptr) to[at < dim ? at : at - dim] = t;
   }
+}
+
+hipError_t launch_norm_sum(const float* part, float* dweight, float* dbias, int parts, int dim, hipStream_t stream) {
+  norm_sum_kernel<<<grid_of((2 * (int64_t)dim + 31) / 32, 1024), 1024, 0, stream>>>(part, dweight, dbias, parts, dim);
+  return hipGetLastError();
 }
 
 namespace {
@@ -1259,9 +1264,7 @@ hipError_t bwd_typed(const NormLaunch& a, hipStream_t stream) {
   }
   if (e != hipSuccess) return e;
   const int parts = norm_bwd_parts(a.batch, a.dim, a.seqlen, sizeof(T));
-  norm_sum_kernel<<<grid_of((2 * (int64_t)a.dim + 31) / 32, 1024), 1024, 0, stream>>>(a.part, a.dweight, a.dbias,
-                                                                                   parts, a.dim);
-  return hipGetLastError();
+  return launch_norm_sum(a.part, a.dweight, a.dbias, parts, a.dim, stream);
 }
 
 }  // namespace

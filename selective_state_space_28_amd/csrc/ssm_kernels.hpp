@@ -234,6 +234,38 @@ struct NormLaunch {
 // Workgroups that each leave one partial sum of dweight and dbias.
 int norm_bwd_parts(int batch, int dim, int64_t seqlen, int elem_bytes);
 
+// dweight[d] = sum_p part[p][0][d], dbias[d] = sum_p part[p][1][d], each written where it is not null.
+hipError_t launch_norm_sum(const float* part, float* dweight, float* dbias, int parts, int dim, hipStream_t stream);
+
+// The norm of groups of a token's channels (include/ssm_group_norm.h).
+struct GroupNormLaunch {
+  const void* x;
+  int64_t x_stride;
+  const float* weight;    // nullable
+  const float* bias;      // nullable
+  const void* z;          // nullable
+  int64_t z_stride;
+  int act;                // ssm_act_t
+  float eps;
+  void* y;
+  float* mean;            // nullable in the forward
+  float* rstd;            // nullable in the forward
+  int64_t tokens;
+  int dim, groups, width; // width = dim / groups
+  Dtype dtype;
+  // backward only
+  const void* dy;
+  void* dx;
+  void* dz;               // with z
+  float* dweight;         // nullable
+  float* dbias;           // nullable
+  float* part;            // (group_norm_bwd_parts, 2, dim) partial sums; null where neither is wanted
+};
+// Workgroups that each leave one partial sum of dweight and dbias.
+int64_t group_norm_bwd_parts(int64_t tokens, int dim, int groups);
+hipError_t launch_group_norm_fwd(const GroupNormLaunch& a, hipStream_t stream);
+hipError_t launch_group_norm_bwd(const GroupNormLaunch& a, hipStream_t stream);
+
 hipError_t launch_gated_fwd(const GatedLaunch& a, hipStream_t stream);
 hipError_t launch_gated_bwd(const GatedLaunch& a, hipStream_t stream);
 hipError_t launch_gated_step(const GatedLaunch& a, hipStream_t stream);

@@ -1,0 +1,244 @@
+"""The C ABI of the linear attention and the group norm without a GPU: every
+declared function is exported, and bad arguments are refused before any HIP call;
+the Python wrappers' own checks; and the 64-bit reference of their tests, pinned by
+the recurrence step by step, by torch's own gradients and by differences."""
+import ctypes
+
+import pytest
+import torch
+
+import selective_state_space_28_amd as ssm
+from selective_state_space_28_amd._lib import header_functions, load
+from tests import heads_ref as ref
+
+OK, NULL, SHAPE, DTYPE, ALIGN, WS, ALIAS, FLAGS = 0, -1, -2, -3, -4, -5, -7, -8
+R = 0x10000000
+
+
+def at(k):
+    """Fake device address of the k-th distinct buffer of a call, never dereferenced."""
+    return 0x4000000000 + k * R
+
+
+def test_exports_every_declared_symbol():
+    attn, group = header_functions("ssm_linear_attn.h"), header_functions("ssm_group_norm.h")
+    assert set(attn) == {"ssm_linear_attn_fwd", "ssm_linear_attn_fwd_workspace_bytes", "ssm_linear_attn_bwd",
+                         "ssm_linear_attn_bwd_workspace_bytes", "ssm_linear_attn_state_update"}
+    assert set(group) == {"ssm_group_norm_fwd", "ssm_group_norm_bwd", "ssm_group_norm_bwd_workspace_bytes"}
+    lib = ctypes.CDLL(load()._name)
+    for n in attn + group:
+        assert hasattr(lib, n), n
+        assert n in ssm.__all__, n
+
+
+B, L, H, K, V = 2, 512, 64, 32, 64
+Y = B * L * H * V * 2  # bytes of y
+S = B * H * K * V * 4
+
+
+def strides(*v):
+    return (ctypes.c_int64 * len(v))(*v)
+
+
+def _fwd(**kw):
+    a = dict(q=at(0), k=at(1), v=at(2), sd=None, g=at(3), scale=1.0, st=None, ln=None, h0=None, y=at(4), last=None,
+             batch=B, L=L, H=H, hq=H, hk=1, hv=H, kd=K, vd=V, dtype=1, ws=at(10), wsb=1 << 28)
+    a.update(kw)
+    return load().ssm_linear_attn_fwd(a["q"], a["k"], a["v"], a["sd"], a["g"], a["scale"], a["st"], a["ln"], a["h0"],
+                                      a["y"], a["last"], a["batch"], a["L"], a["H"], a["hq"], a["hk"], a["hv"], a["kd"],
+                                      a["vd"], a["dtype"], a["ws"], a["wsb"], None)
+
+
+BAD_SIZES = [
+    (dict(dtype=2), DTYPE), (dict(dtype=-1), DTYPE), (dict(batch=-1), SHAPE), (dict(L=-1), SHAPE), (dict(H=-1), SHAPE),
+    (dict(L=(1 << 31) - 4096), SHAPE), (dict(batch=1 << 20, H=1 << 12), SHAPE), (dict(kd=0), SHAPE), (dict(kd=257), SHAPE),
+    (dict(vd=0), SHAPE), (dict(vd=257), SHAPE), (dict(hq=0), SHAPE), (dict(hk=3), SHAPE), (dict(hv=-2), SHAPE),
+    (dict(hq=128), SHAPE), (dict(scale=float("nan")), SHAPE), (dict(scale=float("inf")), SHAPE),
+    (dict(sd=strides(1, 1, -1, 1, 1, 1, 1, 1, 1)), SHAPE), (dict(sd=strides(1, 1, 1, 1, 1 << 41, 1, 1, 1, 1)), SHAPE),
+    (dict(q=None), NULL), (dict(k=None), NULL), (dict(v=None), NULL), (dict(g=None), NULL),
+    (dict(q=at(0) + 1), ALIGN), (dict(dtype=0, k=at(1) + 2), ALIGN), (dict(g=at(3) + 2), ALIGN), (dict(ln=at(9) + 2), ALIGN),
+    (dict(h0=at(9) + 1), ALIGN),
+]
+
+
+@pytest.mark.parametrize("kw,code", BAD_SIZES + [
+    (dict(y=None), NULL), (dict(y=at(4) + 1), ALIGN), (dict(last=at(9) + 2), ALIGN), (dict(ws=at(10) + 64), ALIGN),
+    (dict(batch=1, H=1, hq=1, hv=1, ws=None), WS), (dict(batch=1, H=1, hq=1, hv=1, wsb=100), WS),
+    (dict(y=at(0)), ALIAS), (dict(y=at(2) + Y - 2), ALIAS), (dict(last=at(4) + 4), ALIAS), (dict(last=at(3)), ALIAS),
+    (dict(h0=at(9), last=at(9) + 8), ALIAS), (dict(st=at(4) + 128), ALIAS), (dict(ln=at(4) + 128), ALIAS),
+    (dict(sd=strides(0, 0, 0, 0, 0, 0, L * 1000, 1000, 64), y=at(2) + 2 * L * 1000), ALIAS),
+    (dict(batch=1, H=1, hq=1, hv=1, ws=at(4)), ALIAS),
+    (dict(batch=0), OK), (dict(H=0, q=None, y=None), OK), (dict(L=0, q=None, y=None), OK),
+    (dict(batch=0, kd=300), SHAPE),
+])
+def test_attn_fwd_validation(kw, code):
+    assert _fwd(**kw) == code
+
+
+def _bwd(**kw):
+    a = dict(q=at(0), k=at(1), v=at(2), sd=None, g=at(3), scale=1.0, st=None, ln=None, h0=None, dy=at(4), dl=None, dq=at(5),
+             dk=at(6), dv=at(7), dg=None, dh0=None, batch=B, L=L, H=H, hq=H, hk=1, hv=H, kd=K, vd=V, dtype=1, ws=at(10),
+             wsb=1 << 28)
+    a.update(kw)
+    return load().ssm_linear_attn_bwd(a["q"], a["k"], a["v"], a["sd"], a["g"], a["scale"], a["st"], a["ln"], a["h0"],
+                                      a["dy"], a["dl"], a["dq"], a["dk"], a["dv"], a["dg"], a["dh0"], a["batch"], a["L"],
+                                      a["H"], a["hq"], a["hk"], a["hv"], a["kd"], a["vd"], a["dtype"], a["ws"], a["wsb"],
+                                      None)
+
+
+@pytest.mark.parametrize("kw,code", BAD_SIZES + [
+    (dict(dy=None), NULL), (dict(dq=None), NULL), (dict(dk=None), NULL), (dict(dv=None), NULL),
+    (dict(dy=at(4) + 1), ALIGN), (dict(dv=at(7) + 1), ALIGN), (dict(dg=at(9) + 2), ALIGN), (dict(dl=at(9) + 2), ALIGN),
+    (dict(ws=None), WS), (dict(wsb=100), WS),
+    (dict(dq=at(0)), ALIAS), (dict(dv=at(4)), ALIAS), (dict(dk=at(5) + 4), ALIAS), (dict(dg=at(3)), ALIAS),
+    (dict(dl=at(9), dh0=at(9)), ALIAS), (dict(h0=at(9), dh0=at(9) + 4), ALIAS), (dict(ws=at(7)), ALIAS),
+    (dict(batch=0, dg=None), OK), (dict(H=0, q=None), OK), (dict(L=0, q=None, dq=None, ws=None), OK),
+])
+def test_attn_bwd_validation(kw, code):
+    assert _bwd(**kw) == code
+
+
+def _step(**kw):
+    a = dict(s=at(0), q=at(1), k=at(2), v=at(3), sd=None, g=at(4), scale=1.0, st=None, y=at(5), so=None, batch=B, H=H, hq=H,
+             hk=1, hv=H, kd=K, vd=V, dtype=1)
+    a.update(kw)
+    return load().ssm_linear_attn_state_update(a["s"], a["q"], a["k"], a["v"], a["sd"], a["g"], a["scale"], a["st"], a["y"],
+                                               a["so"], a["batch"], a["H"], a["hq"], a["hk"], a["hv"], a["kd"], a["vd"],
+                                               a["dtype"], None)
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(dtype=9), DTYPE), (dict(batch=-1), SHAPE), (dict(kd=257), SHAPE), (dict(vd=0), SHAPE), (dict(hk=5), SHAPE),
+    (dict(scale=float("nan")), SHAPE), (dict(sd=strides(1, 1, 1, -1, 1, 1)), SHAPE),
+    (dict(s=None), NULL), (dict(q=None), NULL), (dict(k=None), NULL), (dict(v=None), NULL), (dict(g=None), NULL),
+    (dict(y=None), NULL), (dict(s=at(0) + 2), ALIGN), (dict(y=at(5) + 1), ALIGN), (dict(so=at(6) + 2), ALIGN),
+    (dict(y=at(1)), ALIAS), (dict(y=at(0) + 16), ALIAS), (dict(so=at(0) + 4), ALIAS), (dict(so=at(3)), ALIAS),
+    (dict(so=at(5)), ALIAS), (dict(st=at(5)), ALIAS), (dict(batch=0), OK), (dict(H=0, s=None), OK),
+])
+def test_attn_step_validation(kw, code):
+    assert _step(**kw) == code
+
+
+def _gf(**kw):
+    a = dict(x=at(0), xs=256, w=None, b=None, z=None, zs=0, act=1, eps=1e-5, y=at(1), m=None, r=None, n=100, dim=256,
+             groups=4, dtype=1)
+    a.update(kw)
+    return load().ssm_group_norm_fwd(a["x"], a["xs"], a["w"], a["b"], a["z"], a["zs"], a["act"], a["eps"], a["y"], a["m"],
+                                     a["r"], a["n"], a["dim"], a["groups"], a["dtype"], None)
+
+
+GROUP_SIZES = [
+    (dict(dtype=2), DTYPE), (dict(act=3), FLAGS), (dict(act=-1), FLAGS), (dict(n=-1), SHAPE), (dict(dim=0), SHAPE),
+    (dict(groups=0), SHAPE), (dict(groups=3), SHAPE), (dict(dim=16384, xs=16384, groups=1), SHAPE), (dict(n=1 << 30), SHAPE),
+    (dict(xs=255), SHAPE), (dict(xs=1 << 31), SHAPE), (dict(z=at(2), zs=0, dz=at(9)), SHAPE), (dict(x=None), NULL),
+    (dict(x=at(0) + 1), ALIGN), (dict(z=at(2) + 1, zs=256, dz=at(9)), ALIGN), (dict(w=at(2) + 2), ALIGN),
+]
+
+
+@pytest.mark.parametrize("kw,code", GROUP_SIZES + [
+    (dict(eps=-1.0), SHAPE), (dict(eps=float("nan")), SHAPE), (dict(y=None), NULL), (dict(m=at(3) + 1), ALIGN),
+    (dict(y=at(0)), ALIAS), (dict(z=at(1) - 64, zs=256), ALIAS), (dict(xs=1000, y=at(0) + 99 * 2000), ALIAS),
+    (dict(m=at(3), r=at(3) + 4), ALIAS), (dict(w=at(1)), ALIAS), (dict(n=0, x=None), OK),
+])
+def test_group_fwd_validation(kw, code):
+    kw = {k: v for k, v in kw.items() if k != "dz"}
+    assert _gf(**kw) == code
+
+
+def _gb(**kw):
+    a = dict(x=at(0), xs=256, w=None, b=None, z=None, zs=0, act=1, m=at(1), r=at(2), dy=at(3), dx=at(4), dz=None, dw=at(5),
+             db=None, n=100, dim=256, groups=4, dtype=1, ws=at(6), wsb=1 << 24)
+    a.update(kw)
+    return load().ssm_group_norm_bwd(a["x"], a["xs"], a["w"], a["b"], a["z"], a["zs"], a["act"], a["m"], a["r"], a["dy"],
+                                     a["dx"], a["dz"], a["dw"], a["db"], a["n"], a["dim"], a["groups"], a["dtype"], a["ws"],
+                                     a["wsb"], None)
+
+
+@pytest.mark.parametrize("kw,code", [(kw if "z" not in kw else dict(kw, z=at(8) + kw["z"] % 2), c) for kw, c in GROUP_SIZES
+                                     if "w" not in kw] + [
+    (dict(m=None), NULL), (dict(r=None), NULL), (dict(dy=None), NULL), (dict(dx=None), NULL), (dict(z=at(8), zs=256), NULL),
+    (dict(dx=at(4) + 1), ALIGN), (dict(dw=at(5) + 2), ALIGN), (dict(ws=at(6) + 8), ALIGN), (dict(ws=None), WS),
+    (dict(wsb=16), WS), (dict(dx=at(3)), ALIAS), (dict(dx=at(0)), ALIAS), (dict(db=at(5) + 8), ALIAS), (dict(ws=at(4)), ALIAS),
+    (dict(z=at(8), zs=256, dz=at(4)), ALIAS), (dict(n=0, w=at(5)), ALIAS),
+])
+def test_group_bwd_validation(kw, code):
+    assert _gb(**kw) == code
+
+
+def test_workspace_queries():
+    f, b = ssm.ssm_linear_attn_fwd_workspace_bytes, ssm.ssm_linear_attn_bwd_workspace_bytes
+    bf = torch.bfloat16
+    assert f(1, 4096, 2, 64, 64, bf) > 0 and f(0, 4096, 2, 64, 64, bf) == 0 and f(1, 0, 2, 64, 64, bf) == 0
+    assert f(1, 4096, 2, 300, 64, bf) == 0 and f(64, 4096, 64, 64, 64, bf) == 0
+    assert b(1, 100, 4, 4, 4, 4, 64, 64, bf) > 0 and b(1, 100, 4, 3, 4, 4, 64, 64, bf) == 0
+    assert b(1, 100, 4, 1, 4, 4, 64, 64, bf) - b(1, 100, 4, 4, 4, 4, 64, 64, bf) == 100 * 4 * 64 * 4
+    n = ssm.ssm_group_norm_bwd_workspace_bytes
+    assert n(100, 256, 4, bf) > 0 and n(0, 256, 4, bf) == 0 and n(100, 256, 3, bf) == 0
+
+
+def test_wrappers_refuse_cpu_tensors():
+    q = torch.zeros(1, 4, 2, 8)
+    g = torch.zeros(2)
+    for call in (lambda: ssm.ssm_linear_attn_fwd(q, q, q, g), lambda: ssm.ssm_linear_attn_bwd(q, q, q, g, dy=q),
+                 lambda: ssm.ssm_linear_attn_state_update(torch.zeros(1, 2, 8, 8), q[:, 0], q[:, 0], q[:, 0], g),
+                 lambda: ssm.ssm_group_norm_fwd(q[0, 0], 2),
+                 lambda: ssm.ssm_group_norm_bwd(q[0, 0], 2, mean=g, rstd=g, dy=q[0, 0])):
+        with pytest.raises(ValueError, match="GPU"):
+            call()
+
+
+# ---- the reference ------------------------------------------------------------------
+
+def case(packed, padded, seed=0):
+    gen = torch.Generator().manual_seed(seed)
+    b, n, heads, dk, dv = 3, 13, 4, 3, 5
+
+    def draw(*shape):
+        return torch.randn(shape, generator=gen, dtype=torch.float64)
+
+    p = dict(q=draw(b, n, 2, dk), k=draw(b, n, 1, dk), v=draw(b, n, 4, dv), g=-torch.rand(heads, generator=gen).double())
+    rows = dict(starts=(torch.rand(b, n, generator=gen) < 0.2).to(torch.uint8) if packed else None,
+                lengths=torch.tensor([13, 6, 0], dtype=torch.int32) if padded else None, h0=draw(b, heads, dk, dv))
+    return p, rows, draw(b, n, heads, dv), draw(b, heads, dk, dv)
+
+
+@pytest.mark.parametrize("packed", [False, True])
+@pytest.mark.parametrize("padded", [False, True])
+def test_attn_reference(packed, padded):
+    p, rows, dy, dl = case(packed, padded)
+    scale = 0.7
+    want = ref.attn(*p.values(), scale, **rows, dy=dy, dlast=dl)
+    y, last = ref.attn_steps(*p.values(), scale, **rows)
+    assert torch.allclose(want["y"], y, rtol=1e-12, atol=1e-12)
+    assert torch.allclose(want["last"], last, rtol=1e-12, atol=1e-12)
+
+    def loss(q, k, v, g, h0):
+        y, last = ref.attn_steps(q, k, v, g, scale, **dict(rows, h0=h0))
+        return (y * dy).sum() + (last * dl).sum()
+
+    args = [p["q"], p["k"], p["v"], p["g"], rows["h0"]]
+    gen = torch.Generator().manual_seed(5)
+    for name, i in (("dq", 0), ("dk", 1), ("dv", 2), ("dlog_decay", 3), ("dh0", 4)):
+        for _ in range(3):  # along a random direction
+            step = torch.randn(args[i].shape, generator=gen, dtype=torch.float64)
+            hi, lo = list(args), list(args)
+            hi[i], lo[i] = args[i] + 1e-6 * step, args[i] - 1e-6 * step
+            slope = (loss(*hi) - loss(*lo)) / 2e-6
+            assert abs(slope - (want[name] * step).sum()) <= 1e-7 * (1 + abs(slope)), name
+
+
+@pytest.mark.parametrize("gate", [False, True])
+@pytest.mark.parametrize("kind", ["none", "silu", "sigmoid"])
+def test_group_reference(gate, kind):
+    gen = torch.Generator().manual_seed(3)
+    x, z, dy = (torch.randn(4, 12, generator=gen, dtype=torch.float64).requires_grad_() for _ in range(3))
+    w, c = (torch.randn(12, generator=gen, dtype=torch.float64).requires_grad_() for _ in range(2))
+    n = torch.nn.functional.group_norm(x, 3, w, c, 1e-5)
+    f = {"none": lambda t: t, "silu": torch.nn.functional.silu, "sigmoid": torch.sigmoid}[kind]
+    y = n * f(z) if gate else f(n)
+    got, mean, rstd, _ = ref.group_fwd(x, 3, w, c, z if gate else None, kind, 1e-5)
+    assert torch.allclose(got, y, rtol=1e-12, atol=1e-12)
+    y.backward(dy)
+    g = ref.group_bwd(x, 3, w, c, z if gate else None, kind, mean, rstd, dy)
+    for name, t in (("dx", x), ("dweight", w), ("dbias", c)) + ((("dz", z),) if gate else ()):
+        assert torch.allclose(g[name], t.grad, rtol=1e-10, atol=1e-10), name
