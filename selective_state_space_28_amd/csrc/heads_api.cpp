@@ -101,7 +101,7 @@ BwdBytes bwd_bytes(const AttnSizes& s) {
   if (s.hq != s.heads) w.dq = round256(steps * (size_t)s.kd);
   if (s.hk != s.heads) w.dk = round256(steps * (size_t)s.kd);
   if (s.hv != s.heads) w.dv = round256(steps * (size_t)s.vd);
-  w.decay = round256((size_t)s.batch * (size_t)s.heads * (size_t)attn_column_blocks(s.vd) * 8);
+  w.decay = round256((size_t)s.batch * (size_t)s.heads * (size_t)attn_decay_blocks(s.vd) * 8);
   return w;
 }
 

@@ -17,8 +17,8 @@
 // state *before* step t's decay is what the step before receives): the entering
 // weights are e^{g i} and the leaving ones e^{g (C-j)} (`sh` below).
 //
-// A workgroup owns a (batch row, head, segment) and 16 value columns for each of
-// its waves.  S never leaves the matrix cores' accumulators.  16-bit operands use
+// A workgroup owns a (batch row, head, segment) and 16 or 32 value columns for each
+// of its waves.  S never leaves the matrix cores' accumulators.  16-bit operands use
 // v_mfma_f32_16x16x32_bf16, float32 v_mfma_f32_16x16x4_f32.
 #include "linear_attn.hpp"
 #include "runs.hpp"
@@ -32,6 +32,22 @@ typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
+typedef __attribute__((address_space(3))) char lds_char;
+
+// The compiler moves nothing over this: loads of later operands, moved up, would
+// take registers that the state needs.
+__device__ __forceinline__ void in_order() { __builtin_amdgcn_sched_barrier(0); }
+
+// A lane's number as a value of its own: LDS addresses formed from it, one
+// instruction each, are neither formed before the loop nor shared with other code,
+// and held in registers meanwhile.
+__device__ __forceinline__ int own(int lane) {
+  asm volatile("" : "+v"(lane));
+  return lane;
+}
+
+constexpr int kWaves = 4;  // of a sweep's workgroup
+constexpr int kThreads = 64 * kWaves;
 
 __device__ __forceinline__ bool finite_f32(float v) { return __builtin_fabsf(v) <= 3.4028234664e38f; }
 
@@ -55,10 +71,34 @@ __device__ __forceinline__ float decay_pow(float g, float n) {
   return g > -87.0f && v < kMinNormal ? kMinNormal : v;
 }
 
+// A tile in LDS, row-major, the 16-byte pieces of a row permuted by the row so that
+// no access of the kernel meets a bank twice: 16 rows of one piece (operands
+// contracted along the rows), 8 rows of two pieces (bf16, along the columns by
+// transposing reads), 4 rows of four (float32, along the columns), whole rows
+// (staging).
+template <typename T, int W>
+struct Tile {
+  static constexpr int kPiece = 16 / (int)sizeof(T);  // elements
+  static constexpr int kPieces = W / kPiece;
+  __device__ __forceinline__ static int order(int row) {
+    if constexpr (kPieces >= 16) {
+      const int r = row & 15;
+      return sizeof(T) == 2 ? ((r << 1) | (r >> 3)) & 15 : r;
+    } else {
+      const int r = (row >> 1) & 7;
+      return sizeof(T) == 2 ? ((r << 1) | (r >> 2)) & 7 : r;
+    }
+  }
+  __device__ __forceinline__ static int at(int row, int col) {
+    return row * W + ((col / kPiece) ^ order(row)) * kPiece + col % kPiece;
+  }
+};
+
 // The matrix cores' operands for storage type T.  A fragment is what a lane
 // supplies of CK contracted elements: with q = lane / 16, m = lane % 16, of row (or
-// column) m the elements 8 q + e of 32 (bf16, e < 8) or 4 q + e of 16 (float32,
-// e < 4, four products).  A product's lane receives D[4 q + r][m], r < 4.
+// column) m the elements 4 q + e and 16 + 4 q + e of 32 (bf16, e < 4) or 4 q + e of
+// 16 (float32, four products): the order in which a product's result, D[4 q + r][m],
+// r < 4, holds S.
 template <typename T>
 struct Mat;
 
@@ -67,31 +107,35 @@ struct Mat<uint16_t> {
   static constexpr int C = 64;    // steps of a chunk
   static constexpr int CK = 32;
   static constexpr int E = 8;     // elements of a fragment
-  static constexpr int kPad = 8;  // elements behind a row in LDS
   typedef bf16x8 Frag;
   __device__ __forceinline__ static f32x4 mma(const Frag& a, const Frag& b, f32x4 c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
   }
-  // of a row-major tile, contracted along its rows
-  __device__ __forceinline__ static Frag row(const uint16_t* tile, int ld, int r0, int c0, int lane) {
-    return *reinterpret_cast<const Frag*>(tile + (r0 + (lane & 15)) * ld + c0 + 8 * (lane >> 4));
-  }
-  // the same, in the order in which the accumulators hold S: 4 q + r of the first 16, then of the second
-  __device__ __forceinline__ static Frag row_as_state(const uint16_t* tile, int ld, int r0, int c0, int lane) {
-    const uint16_t* p = tile + (r0 + (lane & 15)) * ld + c0 + 4 * (lane >> 4);
-    const uint2 a = *reinterpret_cast<const uint2*>(p), b = *reinterpret_cast<const uint2*>(p + 16);
+  // contracted along the tile's rows
+  template <int W>
+  __device__ __forceinline__ static Frag row(const uint16_t* tile, int r0, int c0, int lane) {
+    const int r = r0 + (lane & 15), c = c0 + 4 * (lane >> 4);
+    const uint2 a = *reinterpret_cast<const uint2*>(tile + Tile<uint16_t, W>::at(r, c));
+    const uint2 b = *reinterpret_cast<const uint2*>(tile + Tile<uint16_t, W>::at(r, c + 16));
     return __builtin_bit_cast(Frag, make_uint4(a.x, a.y, b.x, b.y));
   }
-  // contracted along its columns: the transposing LDS read gives 4 rows of a column to a lane
-  __device__ __forceinline__ static Frag col(const uint16_t* tile, int ld, int r0, int c0, int lane) {
-    const uint16_t* p = tile + (r0 + 8 * (lane >> 4) + ((lane & 15) >> 2)) * ld + c0 + 4 * (lane & 3);
-    const s16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)p);
-    const s16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(p + 4 * ld));
+  // the same where both operands come from here: 8 q + e of 32, one access
+  template <int W>
+  __device__ __forceinline__ static Frag run(const uint16_t* tile, int r0, int c0, int lane) {
+    return *reinterpret_cast<const Frag*>(tile + Tile<uint16_t, W>::at(r0 + (lane & 15), c0 + 8 * (lane >> 4)));
+  }
+  // contracted along its columns: the transposing read gives 4 rows of a column to a lane
+  template <int W>
+  __device__ __forceinline__ static Frag col(const uint16_t* tile, int r0, int c0, int lane) {
+    const int r = r0 + 4 * (lane >> 4) + ((lane & 15) >> 2), c = c0 + 4 * (lane & 3);
+    const s16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(tile + Tile<uint16_t, W>::at(r, c)));
+    const s16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(tile + Tile<uint16_t, W>::at(r + 16, c)));
     const s16x4 ab[2] = {a, b};
     return __builtin_bit_cast(Frag, ab);
   }
   __device__ __forceinline__ static float at(const Frag& f, int e) { return (float)f[e]; }
   __device__ __forceinline__ static void zero(Frag& f, int e) { f[e] = (__bf16)0.0f; }
+  __device__ __forceinline__ static void set(Frag& f, int e, float v) { f[e] = (__bf16)v; }
 };
 
 template <>
@@ -99,26 +143,33 @@ struct Mat<float> {
   static constexpr int C = 32;
   static constexpr int CK = 16;
   static constexpr int E = 4;
-  static constexpr int kPad = 4;
   typedef f32x4 Frag;
   __device__ __forceinline__ static f32x4 mma(const Frag& a, const Frag& b, f32x4 c) {
 #pragma unroll
     for (int r = 0; r < 4; ++r) c = __builtin_amdgcn_mfma_f32_16x16x4f32(a[r], b[r], c, 0, 0, 0);
     return c;
   }
-  __device__ __forceinline__ static Frag row(const float* tile, int ld, int r0, int c0, int lane) {
-    return *reinterpret_cast<const Frag*>(tile + (r0 + (lane & 15)) * ld + c0 + 4 * (lane >> 4));
+  template <int W>
+  __device__ __forceinline__ static Frag row(const float* tile, int r0, int c0, int lane) {
+    return *reinterpret_cast<const Frag*>(tile + Tile<float, W>::at(r0 + (lane & 15), c0 + 4 * (lane >> 4)));
   }
-  __device__ __forceinline__ static Frag row_as_state(const float* tile, int ld, int r0, int c0, int lane) {
-    return row(tile, ld, r0, c0, lane);
+  template <int W>
+  __device__ __forceinline__ static Frag run(const float* tile, int r0, int c0, int lane) {
+    return row<W>(tile, r0, c0, lane);
   }
-  __device__ __forceinline__ static Frag col(const float* tile, int ld, int r0, int c0, int lane) {
-    const float* p = tile + (r0 + 4 * (lane >> 4)) * ld + c0 + (lane & 15);
-    return Frag{p[0], p[ld], p[2 * ld], p[3 * ld]};
+  template <int W>
+  __device__ __forceinline__ static Frag col(const float* tile, int r0, int c0, int lane) {
+    const int r = r0 + 4 * (lane >> 4), c = c0 + (lane & 15);
+    return Frag{tile[Tile<float, W>::at(r, c)], tile[Tile<float, W>::at(r + 1, c)], tile[Tile<float, W>::at(r + 2, c)],
+                tile[Tile<float, W>::at(r + 3, c)]};
   }
   __device__ __forceinline__ static float at(const Frag& f, int e) { return f[e]; }
   __device__ __forceinline__ static void zero(Frag& f, int e) { f[e] = 0.0f; }
+  __device__ __forceinline__ static void set(Frag& f, int e, float v) { f[e] = v; }
 };
+
+// The step (of CK) that element e of a lane's fragment is, q4 = 4 (lane / 16).
+__device__ __forceinline__ int step_of(int e, int q4) { return 16 * (e / 4) + q4 + e % 4; }
 
 // A float32 as a sum of N bf16 fragments' elements: the leading bits cut off, what
 // is left cut off again, the last rounded.  Three hold a float32 exactly, two to
@@ -154,69 +205,138 @@ __device__ __forceinline__ Parts<float, 1> parts_of(const float (&x)[4]) {
   return p;
 }
 
+constexpr uint32_t kNowhere = 0x80000000u;  // an offset behind every extent
+
 // ---- staging ----------------------------------------------------------------------
-// Rows u0 .. u0 + C of a (batch, head) slice into LDS, `WIDTH` columns: zeros from
-// column `width` and from row n on.  Step u is at row base + u * st (st < 0 backward
-// in time).
-template <typename T, int ROWS, int WIDTH, int LD, int THREADS>
-__device__ __forceinline__ void stage(T* lds, const T* base, int64_t st, int width, int n, bool vec) {
+// Rows of a (batch, head) slice in the order of the sweep: step u at p + u * st bytes
+// (st < 0 backward in time).
+struct Slice {
+  const char* p;
+  int64_t st;
+  bool vec;  // aligned to 16 bytes with its strides and width
+};
+
+template <typename T>
+__device__ __forceinline__ Slice slice_of(const AttnView& w, int64_t b, int h, int64_t first, int64_t dir, int width) {
   constexpr int VE = 16 / (int)sizeof(T);
-  constexpr int kPerRow = WIDTH / VE;
-  for (int i = threadIdx.x; i < ROWS * kPerRow; i += THREADS) {
-    const int r = i / kPerRow, c = (i % kPerRow) * VE;
-    const T* p = base + r * st + c;
-    uint4 w = make_uint4(0, 0, 0, 0);
-    if (r < n && c < width) {
-      if (vec && c + VE <= width) {
-        w = *reinterpret_cast<const uint4*>(p);
-      } else {
-        T e[VE];
+  // (a chunk's offsets are 32 bits wide)
+  const bool vec = reinterpret_cast<uintptr_t>(w.p) % 16 == 0 && ((w.sb | w.st | w.sh | (int64_t)width) % VE) == 0 &&
+                   w.st < (int64_t)1 << 22;
+  return Slice{static_cast<const char*>(w.p) + (b * w.sb + (h / w.share) * w.sh + first * w.st) * (int64_t)sizeof(T),
+               dir * w.st * (int64_t)sizeof(T), vec};
+}
+
+// ROWS x W elements of a slice into LDS: zeros from column `width` and from row n on.
+// The copies go past the registers, 1 KiB of LDS in one piece for a wave's access,
+// whose lanes name what belongs there; an offset behind the extent gives zeros.
+// They are under way until landed().  Slices that cannot be read in vectors are
+// copied element by element.
+template <typename T, int ROWS, int W>
+__device__ __forceinline__ void stage(T* lds, const Slice& s, int u, int width, int n, int wave) {
+  using At = Tile<T, W>;
+  constexpr int kAccesses = ROWS * W * (int)sizeof(T) / 1024 / kWaves;  // of a wave
+  static_assert(kAccesses >= 1, "an access for every wave");
+  const int lane = own(threadIdx.x & 63);
+  if (s.vec) {
+    // the lowest address first: row n - 1 backward in time
+    const bool rev = s.st < 0;
+    const uint32_t st = (uint32_t)(rev ? -s.st : s.st);
+    const uint64_t low = reinterpret_cast<uint64_t>(s.p) + (uint64_t)((int64_t)(rev ? u + n - 1 : u) * s.st);
+    u32x4_t buf;
+    buf.x = __builtin_amdgcn_readfirstlane((uint32_t)low);
+    buf.y = __builtin_amdgcn_readfirstlane((uint32_t)(low >> 32) & 0xffffu);
+    buf.z = 0x7fffffffu;
+    buf.w = 0x00020000u;
+    const uint32_t to = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(lds_char*)lds);
 #pragma unroll
-        for (int k = 0; k < VE; ++k) e[k] = c + k < width ? p[k] : (T)0;
-        __builtin_memcpy(&w, e, 16);
-      }
+    for (int k = 0; k < kAccesses; ++k) {
+      const int piece = (wave * kAccesses + k) * 64 + lane;
+      const int r = piece / At::kPieces, c = ((piece % At::kPieces) ^ At::order(r)) * At::kPiece;
+      const uint32_t at = (uint32_t)(rev ? n - 1 - r : r) * st + (uint32_t)(c * (int)sizeof(T));
+      asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
+                   :
+                   : "s"(to + (uint32_t)(wave * kAccesses + k) * 1024u), "v"(r < n && c < width ? at : kNowhere), "s"(buf)
+                   : "memory", "m0");
     }
-    *reinterpret_cast<uint4*>(lds + r * LD + c) = w;
+  } else {
+#pragma unroll 1
+    for (int i = threadIdx.x; i < ROWS * W; i += kThreads) {
+      const int r = i / W, c = i % W;
+      T e = (T)0;
+      if (r < n && c < width) e = reinterpret_cast<const T*>(s.p + (int64_t)(u + r) * s.st)[c];
+      lds[At::at(r, c)] = e;
+    }
   }
 }
+
+__device__ __forceinline__ void landed() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
+
+// Where the elements of S lie in memory, (kd, vd) or turned: a lane's offset, and what
+// is the same for every lane.  Rows and columns that pad S lie nowhere.
+struct StateAt {
+  int row0, col0, kd, vd, row_step, col_step;
+  __device__ __forceinline__ StateAt(const AttnSweep& a, bool turned, int col, int row)
+      : row0(row), col0(col), kd(a.kd), vd(a.vd), row_step(turned ? 1 : a.vd), col_step(turned ? a.kd : 1) {}
+  __device__ __forceinline__ bool in(int row, int col) const { return row0 + row < kd && col0 + col < vd; }
+  __device__ __forceinline__ uint32_t lane(int row, int col) const {
+    return in(row, col) ? 4u * (uint32_t)(row0 * row_step + col0 * col_step) : kNowhere;
+  }
+  __device__ __forceinline__ uint32_t fixed(int row, int col) const {
+    return 4u * (uint32_t)(row * row_step + col * col_step);
+  }
+};
 
 }  // namespace
 
 enum AttnMode { kAttnOut = 0, kAttnSegments = 1, kAttnDecay = 2 };
 
-// One workgroup: NW waves, 16 value columns each.  kAttnSegments: only the state that
-// a segment adds, and what it leaves of the one before.  kAttnDecay: the forward
-// sweep with R = dS/dg beside S, and dg = scale sum_t q_t R_t dy_t + <R_L, dlast>;
-// R_u = e^g (R_{u-1} + S_{u-1}) gives, of a chunk,
+// One workgroup: kWaves waves, CT tiles of 16 value columns each.  kAttnSegments: only
+// the state that a segment adds, and what it leaves of the one before.  kAttnDecay:
+// the forward sweep with R = dS/dg beside S, and dg = scale sum_t q_t R_t dy_t +
+// <R_L, dlast>; R_u = e^g (R_{u-1} + S_{u-1}) gives, of a chunk,
 //   diag(e^{g (i+1)}) Q (R + (i+1) S) + ((i-j) W o Q K^T) V
 //   R <- e^{g C} (R + C S) + (diag((C-1-j) e^{g (C-1-j)}) K)^T V
-template <typename T, int KD, int NW, int MODE>
-__global__ __launch_bounds__(64 * NW) void attn_sweep_kernel(const AttnSweep a, const float* __restrict__ dlast) {
+//
+// The next chunk's tiles are copied to LDS while this one is worked on: K, wanted to
+// the end, into a second buffer, V and Q into their own once every wave has done with
+// them.  (Through registers the state would not fit beside them.)
+template <typename T, int KD, int CT, int MODE>
+__global__ __launch_bounds__(kThreads, KD <= 128 ? 2 : 1) void attn_sweep_kernel(const AttnSweep a,
+                                                                                const float* __restrict__ dlast,
+                                                                                int64_t groups) {
   using M = Mat<T>;
   using Frag = typename M::Frag;
   constexpr int C = M::C, IT = C / 16, CK = M::CK, E = M::E;
-  constexpr int NV = 16 * NW, THREADS = 64 * NW;
-  constexpr int LDK = KD + M::kPad, LDV = NV + M::kPad, LDP = C + M::kPad;
-  constexpr int KT = KD / 16;  // tiles of S in a wave
+  constexpr int NV = 16 * CT * kWaves;
+  constexpr int KT = KD / 16;  // tiles of S above one another
   constexpr bool kDecay = MODE == kAttnDecay, kOut = MODE != kAttnSegments;
   constexpr int NU = sizeof(T) == 2 ? 3 : 1;  // parts of the decayed v, exact
   constexpr int NS = sizeof(T) == 2 ? 2 : 1;  // parts of S as an operand, to 2^-16
+  constexpr int kTiles = IT * (IT + 1) / 2;   // of P, on and below the diagonal
+  constexpr int kMyTiles = (kTiles + kWaves - 1) / kWaves;
+  constexpr bool kLow = kDecay && sizeof(T) == 2;  // P in two parts
 
-  __shared__ __attribute__((aligned(16))) T s_q[kOut ? C * LDK : 1];
-  __shared__ __attribute__((aligned(16))) T s_k[C * LDK];
-  __shared__ __attribute__((aligned(16))) T s_v[C * LDV];
-  __shared__ __attribute__((aligned(16))) T s_p[kOut ? C * LDP : 1];
-  __shared__ __attribute__((aligned(16))) T s_p2[kDecay && sizeof(T) == 2 ? C * LDP : 1];  // second parts
-  __shared__ __attribute__((aligned(16))) T s_dy[kDecay ? C * LDV : 1];
+  __shared__ __attribute__((aligned(16))) T s_q[kOut ? C * KD : 1];
+  __shared__ __attribute__((aligned(16))) T s_keys[2][C * KD];
+  __shared__ __attribute__((aligned(16))) T s_v[C * NV];
+  __shared__ __attribute__((aligned(16))) T s_p[kOut ? C * C : 1];
+  __shared__ __attribute__((aligned(16))) T s_p2[kLow ? C * C : 1];
+  __shared__ __attribute__((aligned(16))) T s_dy[kDecay ? C * NV : 1];
   __shared__ float s_pw[C + 1];
-  __shared__ double s_sum[NW];
+  __shared__ __attribute__((aligned(16))) float s_enter[C], s_leave[C], s_left[kDecay ? C : 1];
+  __shared__ double s_sum[kWaves];
 
-  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int m = lane & 15, q4 = 4 * (lane >> 4);
+  int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  int m = lane & 15, q4 = 4 * (lane >> 4);
   const int nvb = (a.vd + NV - 1) / NV;
   const int nsegs = MODE == kAttnSegments ? a.nseg - 1 : MODE == kAttnDecay ? 1 : a.nseg;
+  // consecutive workgroups go to the 8 dies in turn: a die takes consecutive numbers,
+  // whose column blocks, and heads that share q, k or v, read the same lines
   int64_t id = group_index();
-  if (id >= (int64_t)a.batch * a.heads * nvb * nsegs) return;
+  const int64_t per = (groups + 7) / 8;
+  id = (id & 7) * per + (id >> 3);
+  if ((group_index() >> 3) >= per || id >= groups) return;
   const int vb = (int)(id % nvb);
   id /= nvb;
   const int h = (int)(id % a.heads);
@@ -225,63 +345,97 @@ __global__ __launch_bounds__(64 * NW) void attn_sweep_kernel(const AttnSweep a, 
 
   const float g = a.g[h];
   const int L = (int)a.seqlen;
-  const int len = a.lengths == nullptr ? L : min(max(a.lengths[b], 0), L);
+  const int len =
+      a.lengths == nullptr ? L : __builtin_amdgcn_readfirstlane(min(max(a.lengths[b], 0), L));
   const int sh = a.rev ? 1 : 0;
-  for (int i = threadIdx.x; i <= C; i += THREADS) s_pw[i] = decay_pow(g, (float)i);
+  for (int i = threadIdx.x; i <= C; i += kThreads) s_pw[i] = decay_pow(g, (float)i);
 
-  const int v0 = vb * NV;                     // first value column of the workgroup
-  const int vw = min(NV, a.vd - v0);          // its columns
-  const int col = v0 + 16 * wave + m;         // of S, this lane's
+  const int v0 = vb * NV;             // first value column of the workgroup
+  const int vw = min(NV, a.vd - v0);  // its columns
+  const int c0 = 16 * CT * wave;      // first of the wave, in the workgroup's
   const int64_t head = (int64_t)b * a.heads + h;
   const int64_t dir = a.rev ? -1 : 1, first = a.rev ? len - 1 : 0;
-  const auto base = [&](const AttnView& w) {
-    return static_cast<const T*>(w.p) + b * w.sb + (h / w.share) * w.sh + first * w.st;
-  };
-  const T *pq = base(a.q), *pk = base(a.k), *pv = base(a.v) + v0, *pdy = kDecay ? base(a.dy) + v0 : nullptr;
-  const auto vectors = [](const AttnView& w, int width) {
-    constexpr int VE = 16 / (int)sizeof(T);
-    return reinterpret_cast<uintptr_t>(w.p) % 16 == 0 && ((w.sb | w.st | w.sh | (int64_t)width) % VE) == 0;
-  };
-  const bool vec_q = vectors(a.q, 0), vec_k = vectors(a.k, 0), vec_v = vectors(a.v, 0),
-             vec_dy = kDecay && vectors(a.dy, 0);
+  const auto slice = [&](const AttnView& w, int width) { return slice_of<T>(w, b, h, first, dir, width); };
+  const Slice sq = slice(a.q, a.kd), sk = slice(a.k, a.kd);
+  Slice sv = slice(a.v, a.vd), sd{};
+  sv.p += v0 * (int)sizeof(T);
+  if constexpr (kDecay) {
+    sd = slice(a.dy, a.vd);
+    sd.p += v0 * (int)sizeof(T);
+  }
 
-  // S: rows 16 t + q4 + r, column `col`
-  f32x4 S[KT], R[kDecay ? KT : 1];
+  // S: rows 16 t + q4 + r, column v0 + c0 + 16 ct + m
+  f32x4 S[CT][KT], R[kDecay ? CT : 1][kDecay ? KT : 1];
+  const int64_t mat = (int64_t)a.kd * a.vd;
+  const float* from = nullptr;
+  if (kOut && seg > 0) from = a.seg_state + (head * a.nseg + seg) * mat;
+  else if (kOut && a.state_in != nullptr) from = a.state_in + head * mat;
+  const bool turned = kOut && a.transposed && seg == 0;
 #pragma unroll
-  for (int t = 0; t < KT; ++t) {
-    if constexpr (kDecay) R[t] = f32x4{0, 0, 0, 0};
+  for (int ct = 0; ct < CT; ++ct)
 #pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      const int row = 16 * t + q4 + r;
-      float v = 0.0f;
-      if (kOut && row < a.kd && col < a.vd) {
-        const int64_t mat = (int64_t)a.kd * a.vd;
-        if (seg > 0)
-          v = a.seg_state[(head * a.nseg + seg) * mat + (int64_t)row * a.vd + col];
-        else if (a.state_in != nullptr)
-          v = a.state_in[head * mat + (a.transposed ? (int64_t)col * a.kd + row : (int64_t)row * a.vd + col)];
-      }
-      S[t][r] = v;
+    for (int t = 0; t < KT; ++t) {
+      S[ct][t] = f32x4{0, 0, 0, 0};
+      if constexpr (kDecay) R[ct][t] = f32x4{0, 0, 0, 0};
     }
+  if (from != nullptr) {
+    const Buf buf = make_buf(from, mat * 4);
+    const StateAt at(a, turned, v0 + c0 + m, q4);
+#pragma unroll
+    for (int ct = 0; ct < CT; ++ct)
+#pragma unroll
+      for (int t = 0; t < KT; ++t)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          uint32_t w[1];
+          buf_load_words<1>(buf, at.lane(16 * t + r, 16 * ct), at.fixed(16 * t + r, 16 * ct), w);
+          S[ct][t][r] = __uint_as_float(w[0]);
+        }
   }
   if constexpr (kOut) {  // the masked halves of pairs of tiles stay zero
-    for (int i = threadIdx.x; i < C * LDP; i += THREADS) {
+    for (int i = threadIdx.x; i < C * C; i += kThreads) {
       s_p[i] = (T)0;
-      if constexpr (kDecay && sizeof(T) == 2) s_p2[i] = (T)0;
+      if constexpr (kLow) s_p2[i] = (T)0;
     }
   }
   double dg = 0.0;
-  float through = 1.0f;  // kAttnSegments: of the whole segment
   bool cut = false;
+  // whole chunks of whole columns are stored four columns at a time (offsets in 32 bits)
+  const bool whole_out = vw == NV && a.vd % 4 == 0 && (sizeof(T) == 4 || !a.out_f32) &&
+                         reinterpret_cast<uintptr_t>(a.out) % (4 * sizeof(T)) == 0 &&
+                         (int64_t)a.heads * a.vd <= (int64_t)1 << 22;
 
   const int u_begin = (int)(seg * a.seglen);
   const int u_end = MODE == kAttnDecay ? L : (int)min((int64_t)L, u_begin + a.seglen);
   T* out = static_cast<T*>(a.out);
+  const auto valid = [&](int u) { return min(max(len - u, 0), C); };  // (u is at most seqlen + C, below 2^31)
+
+  const auto stage_q = [&](int u) {
+    if (kOut && u < u_end) stage<T, C, KD>(s_q, sq, u, a.kd, valid(u), wave);
+  };
+  const auto stage_k = [&](int u, int into) {
+    if (u < u_end) stage<T, C, KD>(s_keys[into], sk, u, a.kd, valid(u), wave);
+  };
+  const auto stage_v = [&](int u) {
+    if (u < u_end) stage<T, C, NV>(s_v, sv, u, vw, valid(u), wave);
+  };
+  const auto stage_dy = [&](int u) {
+    if constexpr (kDecay) {
+      if (u < u_end) stage<T, C, NV>(s_dy, sd, u, vw, valid(u), wave);
+    }
+  };
+  stage_k(u_begin, 0);
+  stage_q(u_begin);
+  stage_v(u_begin);
+  stage_dy(u_begin);
+  int turn = 0;
+
   for (int u0 = u_begin; u0 < u_end; u0 += C) {
-    const int n = min(max(len - u0, 0), C);
+    const int n = valid(u0);
     if (n == 0 && MODE != kAttnOut) break;
+    lane = own(lane);
     if (kOut && n == 0) {  // steps behind the row's length
-      for (int64_t i = threadIdx.x; i < (int64_t)(u_end - u0) * vw; i += THREADS) {
+      for (int64_t i = threadIdx.x; i < (int64_t)(u_end - u0) * vw; i += kThreads) {
         const int64_t at = (((int64_t)b * L + u0 + i / vw) * a.heads + h) * a.vd + v0 + i % vw;
         if (a.out_f32) static_cast<float*>(a.out)[at] = 0.0f;
         else out[at] = (T)0;
@@ -297,255 +451,383 @@ __global__ __launch_bounds__(64 * NW) void attn_sweep_kernel(const AttnSweep a, 
       B = __ballot(f);
     }
     const auto seen = [&](int i) { return __popcll(B & (~0ull >> (63 - i))); };  // starts up to and with step i
+    const int total = seen(n - 1);
 
-    __syncthreads();  // the chunk before is done with LDS
-    if constexpr (kOut) stage<T, C, KD, LDK, THREADS>(s_q, pq + u0 * dir * a.q.st, dir * a.q.st, a.kd, n, vec_q);
-    stage<T, C, KD, LDK, THREADS>(s_k, pk + u0 * dir * a.k.st, dir * a.k.st, a.kd, n, vec_k);
-    stage<T, C, NV, LDV, THREADS>(s_v, pv + u0 * dir * a.v.st, dir * a.v.st, vw, n, vec_v);
-    if constexpr (kDecay) stage<T, C, NV, LDV, THREADS>(s_dy, pdy + u0 * a.dy.st, a.dy.st, vw, n, vec_dy);
-    __syncthreads();
+    landed();
+    __syncthreads();  // the tiles are there, and the chunk before is done with LDS
+    const T* s_k = s_keys[turn];
+    turn ^= 1;
+    stage_k(u0 + C, turn);
+    if (threadIdx.x < C) {  // the weights of the state that enters, and of each step in the one that leaves
+      const int i = threadIdx.x, left = n - 1 - i;
+      if constexpr (kOut) s_enter[i] = B == 0 || seen(i) == 0 ? s_pw[i + 1 - sh] * a.scale_in : 0.0f;
+      const float w = left >= 0 && (B == 0 || seen(i) == total) ? s_pw[left + sh] * a.scale_upd : 0.0f;
+      s_leave[i] = w;
+      if constexpr (kDecay) s_left[i] = w * (float)left;
+    }
 
     if constexpr (kOut) {
       // P = W o Q K^T, tile (it, jt) at a time, transposed so that a lane holds 4 steps j of a row i
-      for (int tile = wave; tile < IT * (IT + 1) / 2; tile += NW) {
-        int it = 0, jt = tile;
-        while (jt > it) jt -= ++it;
-        f32x4 acc = {0, 0, 0, 0};
+      const auto products = [&](auto packed) {
+        const int lane = own(threadIdx.x & 63), m = lane & 15, q4 = 4 * (lane >> 4);
 #pragma unroll
-        for (int kk = 0; kk < KD; kk += CK)
-          acc = M::mma(M::row(s_k, LDK, 16 * jt, kk, lane), M::row(s_q, LDK, 16 * it, kk, lane), acc);
-        const int i = 16 * it + m;
-        float p[4];
+        for (int k = 0; k < kMyTiles; ++k) {
+          const int tile = wave + k * kWaves;
+          if (tile >= kTiles) break;
+          in_order();
+          const int it = (0xffa94 >> (2 * tile)) & 3, jt = (0xe4910 >> (2 * tile)) & 3;  // row by row
+          f32x4 acc = {0, 0, 0, 0};
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const int j = 16 * jt + q4 + r;
-          const bool kept = j <= i && (B == 0 || seen(i) == seen(j));
-          float w = s_pw[kept ? i - j : 0] * a.scale_p;
-          if (kDecay) w *= (float)(i - j);
-          p[r] = kept ? acc[r] * w : 0.0f;
-        }
-        T* dst = s_p + i * LDP + 16 * jt + q4;
-        if constexpr (sizeof(T) == 2) {
-          if constexpr (kDecay) {
-            float lo[4];
+          for (int kk = 0; kk < KD; kk += CK)
+            acc = M::mma(M::template run<KD>(s_k, 16 * jt, kk, lane), M::template run<KD>(s_q, 16 * it, kk, lane), acc);
+          const int i = 16 * it + m;
+          float p[4];
 #pragma unroll
-            for (int r = 0; r < 4; ++r) {
-              const float hi = cut16(p[r]);
-              lo[r] = p[r] - hi;
-              p[r] = hi;
-            }
-            *reinterpret_cast<uint2*>(s_p2 + i * LDP + 16 * jt + q4) =
-                make_uint2(pack_bf16x2(lo[0], lo[1]), pack_bf16x2(lo[2], lo[3]));
+          for (int r = 0; r < 4; ++r) {
+            const int j = 16 * jt + q4 + r;
+            const bool kept = j <= i && (!packed || seen(i) == seen(j));
+            float w = s_pw[j <= i ? i - j : 0] * a.scale_p;
+            if (kDecay) w *= (float)(i - j);
+            p[r] = kept ? acc[r] * w : 0.0f;
           }
-          *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16x2(p[0], p[1]), pack_bf16x2(p[2], p[3]));
-        } else {
-          *reinterpret_cast<f32x4*>(dst) = f32x4{p[0], p[1], p[2], p[3]};
+          const int dst = Tile<T, C>::at(i, 16 * jt + q4);
+          if constexpr (sizeof(T) == 2) {
+            if constexpr (kLow) {
+              float lo[4];
+#pragma unroll
+              for (int r = 0; r < 4; ++r) {
+                const float hi = cut16(p[r]);
+                lo[r] = p[r] - hi;
+                p[r] = hi;
+              }
+              *reinterpret_cast<uint2*>(s_p2 + dst) = make_uint2(pack_bf16x2(lo[0], lo[1]), pack_bf16x2(lo[2], lo[3]));
+            }
+            *reinterpret_cast<uint2*>(s_p + dst) = make_uint2(pack_bf16x2(p[0], p[1]), pack_bf16x2(p[2], p[3]));
+          } else {
+            *reinterpret_cast<f32x4*>(s_p + dst) = f32x4{p[0], p[1], p[2], p[3]};
+          }
         }
-      }
-      __syncthreads();
+      };
+      if (B == 0) products(std::false_type{});
+      else products(std::true_type{});
     }
 
     // this wave's columns of V, contracted over the steps
-    Frag vf[C / CK];
-    float x[C / CK][E], x2[kDecay ? C / CK : 1][E];
+    Frag vf[CT][C / CK];
     float odd = 0.0f;  // NaN if any of the values is not finite
-    const int total = seen(n - 1);
 #pragma unroll
-    for (int s = 0; s < C / CK; ++s) {
-      vf[s] = M::col(s_v, LDV, CK * s, 16 * wave, lane);
+    for (int ct = 0; ct < CT; ++ct)
 #pragma unroll
-      for (int e = 0; e < E; ++e) {
-        const int j = CK * s + E * (lane >> 4) + e;
-        const int left = n - 1 - j;
-        const float v = M::at(vf[s], e) * (s_pw[left < 0 ? 0 : left + sh] * a.scale_upd);
-        odd = __builtin_fmaf(v, 0.0f, odd);
-        const bool kept = left >= 0 && (B == 0 || seen(j) == total);
-        x[s][e] = kept ? v : 0.0f;
-        if constexpr (kDecay) x2[s][e] = kept ? v * (float)left : 0.0f;
+      for (int s = 0; s < C / CK; ++s) {
+        vf[ct][s] = M::template col<NV>(s_v, CK * s, c0 + 16 * ct, lane);
+#pragma unroll
+        for (int e = 0; e < E; ++e) odd = __builtin_fmaf(M::at(vf[ct][s], e), 0.0f, odd);
       }
-    }
-    // Values that are not finite are left out of the product with P, whose zeros
-    // above the diagonal they would turn into NaN, and added apart.
     const bool careful = __any(!(odd == 0.0f));
-    if (careful) {
-#pragma unroll
-      for (int s = 0; s < C / CK; ++s)
-#pragma unroll
-        for (int e = 0; e < E; ++e)
-          if (!finite_f32(M::at(vf[s], e))) M::zero(vf[s], e);
-    }
+    __syncthreads();  // P and the weights are there, V is in registers
+    stage_v(u0 + C);
 
-    if constexpr (kOut) {
-      f32x4 acc[IT], acc_r[kDecay ? IT : 1];
+    // The outputs and the state behind the chunk.  `special`: a sequence starts in the
+    // chunk, or one of the wave's values is not finite.
+    const auto finish = [&](auto special) {
+      if constexpr (kOut) {
+        const int lane = own(threadIdx.x & 63), m = lane & 15, q4 = 4 * (lane >> 4);
+        f32x4 acc[CT][IT], acc_r[kDecay ? CT : 1][kDecay ? IT : 1];
 #pragma unroll
-      for (int it = 0; it < IT; ++it) {
-        acc[it] = f32x4{0, 0, 0, 0};
-        if constexpr (kDecay) acc_r[it] = f32x4{0, 0, 0, 0};
-      }
-      // (Q S)^T: a lane holds 4 value columns of a step
+        for (int ct = 0; ct < CT; ++ct)
 #pragma unroll
-      for (int kk = 0; kk < KD / CK; ++kk) {
-        float sv[E], rv[E];
+          for (int it = 0; it < IT; ++it) {
+            acc[ct][it] = f32x4{0, 0, 0, 0};
+            if constexpr (kDecay) acc_r[ct][it] = f32x4{0, 0, 0, 0};
+          }
+        // (Q S)^T: a lane holds 4 value columns of a step
 #pragma unroll
-        for (int e = 0; e < E; ++e) {
-          sv[e] = S[kk * (CK / 16) + e / 4][e % 4];
-          if constexpr (kDecay) rv[e] = R[kk * (CK / 16) + e / 4][e % 4];
+        for (int kk = 0; kk < KD / CK; ++kk) {
+          in_order();
+          Parts<T, NS> ps[CT], pr[kDecay ? CT : 1];
+          Frag fq[IT];
+#pragma unroll
+          for (int it = 0; it < IT; ++it) fq[it] = M::template row<KD>(s_q, 16 * it, kk * CK, lane);
+#pragma unroll
+          for (int ct = 0; ct < CT; ++ct) {
+            float sv[E], rv[E];
+#pragma unroll
+            for (int e = 0; e < E; ++e) {
+              sv[e] = S[ct][kk * (CK / 16) + e / 4][e % 4];
+              if constexpr (kDecay) rv[e] = R[ct][kk * (CK / 16) + e / 4][e % 4];
+            }
+            ps[ct] = parts_of<NS>(sv);
+            if constexpr (kDecay) pr[ct] = parts_of<NS>(rv);
+          }
+#pragma unroll
+          for (int k = 0; k < NS; ++k)
+#pragma unroll
+            for (int it = 0; it < IT; ++it)
+#pragma unroll
+              for (int ct = 0; ct < CT; ++ct) {
+                acc[ct][it] = M::mma(ps[ct].f[k], fq[it], acc[ct][it]);
+                if constexpr (kDecay) acc_r[ct][it] = M::mma(pr[ct].f[k], fq[it], acc_r[ct][it]);
+              }
         }
-        const auto ps = parts_of<NS>(sv);
 #pragma unroll
         for (int it = 0; it < IT; ++it) {
-          const Frag fq = M::row_as_state(s_q, LDK, 16 * it, kk * CK, lane);
+          const int i = 16 * it + m;
+          const float w = s_enter[i];
+          const bool dropped = special && B != 0 && seen(i) != 0;
 #pragma unroll
-          for (int k = 0; k < NS; ++k) acc[it] = M::mma(ps.f[k], fq, acc[it]);
-          if constexpr (kDecay) {
-            const auto pr = parts_of<NS>(rv);
+          for (int ct = 0; ct < CT; ++ct)
 #pragma unroll
-            for (int k = 0; k < NS; ++k) acc_r[it] = M::mma(pr.f[k], fq, acc_r[it]);
-          }
+            for (int r = 0; r < 4; ++r) {
+              float o = acc[ct][it][r];
+              if constexpr (kDecay) o = __builtin_fmaf(o, (float)(i + 1), acc_r[ct][it][r]);
+              acc[ct][it][r] = dropped ? 0.0f : o * w;
+            }
         }
-      }
-#pragma unroll
-      for (int it = 0; it < IT; ++it) {
-        const int i = 16 * it + m;
-        const bool kept = B == 0 || seen(i) == 0;
-        const float w = s_pw[i + 1 - sh] * a.scale_in;
-        f32x4 o;
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          o[r] = acc[it][r];
-          if constexpr (kDecay) o[r] = __builtin_fmaf(o[r], (float)(i + 1), acc_r[it][r]);
-          o[r] = kept ? o[r] * w : 0.0f;
-        }
+        in_order();
 #pragma unroll
         for (int s = 0; s < C / CK; ++s) {
-          if (CK * s >= 16 * (it + 1)) continue;
-          o = M::mma(vf[s], M::row(s_p, LDP, 16 * it, CK * s, lane), o);
-          if constexpr (kDecay && sizeof(T) == 2) o = M::mma(vf[s], M::row(s_p2, LDP, 16 * it, CK * s, lane), o);
-        }
-        if (careful) {  // the values left out of vf, to the steps that take them
-          for (int j = 0; j <= min(i, n - 1); ++j) {
-            if (B != 0 && seen(j) != seen(i)) continue;
-            const float p = Elem<T>::load(s_p + i * LDP + j);
+          Frag fv[CT];
 #pragma unroll
-            for (int r = 0; r < 4; ++r) {
-              const float v = Elem<T>::load(s_v + j * LDV + 16 * wave + q4 + r);
-              if (!finite_f32(v)) o[r] = __builtin_fmaf(p, v, o[r]);
+          for (int ct = 0; ct < CT; ++ct) {
+            fv[ct] = vf[ct][s];
+            if (special && careful) {
+#pragma unroll
+              for (int e = 0; e < E; ++e)
+                if (!finite_f32(M::at(fv[ct], e))) M::zero(fv[ct], e);
+            }
+          }
+#pragma unroll
+          for (int it = 0; it < IT; ++it) {
+            if (CK * s >= 16 * (it + 1)) continue;
+            const Frag fp = M::template row<C>(s_p, 16 * it, CK * s, lane);
+#pragma unroll
+            for (int ct = 0; ct < CT; ++ct) acc[ct][it] = M::mma(fv[ct], fp, acc[ct][it]);
+            if constexpr (kLow) {
+              const Frag fl = M::template row<C>(s_p2, 16 * it, CK * s, lane);
+#pragma unroll
+              for (int ct = 0; ct < CT; ++ct) acc[ct][it] = M::mma(fv[ct], fl, acc[ct][it]);
             }
           }
         }
-        acc[it] = o;
-      }
-      if constexpr (kDecay) {
-        float sum = 0.0f;
+        // Values that are not finite were left out of the product with P, whose zeros above
+        // the diagonal they would turn into NaN.  Products of ones in their places with ones
+        // where P has its steps count what each output takes of them.
+        if (special && careful) {
 #pragma unroll
-        for (int it = 0; it < IT; ++it)
+          for (int it = 0; it < IT; ++it) {
+            const int i = 16 * it + m;
+            f32x4 bad[CT];
 #pragma unroll
-          for (int r = 0; r < 4; ++r) {
-            const int i = 16 * it + m, c = 16 * wave + q4 + r;
-            if (i < n && c < vw)
-              sum = __builtin_fmaf(acc[it][r], Elem<T>::load(s_dy + i * LDV + c), sum);
-          }
-        dg += (double)sum;
-      } else {
+            for (int ct = 0; ct < CT; ++ct) bad[ct] = f32x4{0, 0, 0, 0};
 #pragma unroll
-        for (int it = 0; it < IT; ++it) {
-          const int i = 16 * it + m, u = u0 + i;
-          if (u < u_end) {
-            const int t = u < len && a.rev ? len - 1 - u : u;
-            const int64_t at = (((int64_t)b * L + t) * a.heads + h) * a.vd + v0 + 16 * wave + q4;
+            for (int s = 0; s < C / CK; ++s) {
+              if (CK * s >= 16 * (it + 1)) continue;
+              Frag taken;
 #pragma unroll
-            for (int r = 0; r < 4; ++r) {
-              const float v = i < n ? acc[it][r] : 0.0f;
-              if (16 * wave + q4 + r < vw) {
-                if (a.out_f32) static_cast<float*>(a.out)[at + r] = v;
-                else Elem<T>::store(out + at + r, v);
+              for (int e = 0; e < E; ++e) {
+                const int j = CK * s + step_of(e, q4);
+                M::set(taken, e, j <= i && (B == 0 || seen(i) == seen(j)) ? 1.0f : 0.0f);
+              }
+#pragma unroll
+              for (int ct = 0; ct < CT; ++ct) {
+                Frag one;
+#pragma unroll
+                for (int e = 0; e < E; ++e) M::set(one, e, finite_f32(M::at(vf[ct][s], e)) ? 0.0f : 1.0f);
+                bad[ct] = M::mma(one, taken, bad[ct]);
               }
             }
+#pragma unroll
+            for (int ct = 0; ct < CT; ++ct)
+#pragma unroll
+              for (int r = 0; r < 4; ++r)
+                if (bad[ct][r] != 0.0f) acc[ct][it][r] = __builtin_nanf("");
+          }
+        }
+        if constexpr (kDecay) {
+          float sum = 0.0f;
+#pragma unroll
+          for (int ct = 0; ct < CT; ++ct)
+#pragma unroll
+            for (int it = 0; it < IT; ++it)
+#pragma unroll
+              for (int r = 0; r < 4; ++r) {
+                const int i = 16 * it + m, c = c0 + 16 * ct + q4 + r;
+                if (i < n && c < vw)
+                  sum = __builtin_fmaf(acc[ct][it][r], Elem<T>::load(s_dy + Tile<T, NV>::at(i, c)), sum);
+              }
+          dg += (double)sum;
+        } else if (whole_out && n == C) {
+          // the chunk's lowest row first
+          const int64_t t0 = a.rev ? len - C - u0 : u0;
+          const Buf buf = make_buf(out + (((int64_t)b * L + t0) * a.heads + h) * a.vd + v0, 0x7fffffff);
+          const uint32_t step = (uint32_t)(a.heads * a.vd) * (uint32_t)sizeof(T);
+#pragma unroll
+          for (int it = 0; it < IT; ++it)
+#pragma unroll
+            for (int ct = 0; ct < CT; ++ct) {
+              const uint32_t at =
+                  (uint32_t)(a.rev ? C - 1 - 16 * it - m : 16 * it + m) * step + (uint32_t)(c0 + 16 * ct + q4) * (uint32_t)sizeof(T);
+              const f32x4 o = acc[ct][it];
+              if constexpr (sizeof(T) == 2) {
+                const uint32_t words[2] = {pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3])};
+                buf_store_words<2>(buf, at, 0, words);
+              } else {
+                const uint32_t words[4] = {__float_as_uint(o[0]), __float_as_uint(o[1]), __float_as_uint(o[2]),
+                                           __float_as_uint(o[3])};
+                buf_store_words<4>(buf, at, 0, words);
+              }
+            }
+        } else {
+#pragma unroll
+          for (int it = 0; it < IT; ++it) {
+            const int i = 16 * it + m, u = u0 + i;
+            if (u >= u_end) continue;
+            const int t = u < len && a.rev ? len - 1 - u : u;
+            const int64_t at = (((int64_t)b * L + t) * a.heads + h) * a.vd + v0;
+#pragma unroll
+            for (int ct = 0; ct < CT; ++ct)
+#pragma unroll
+              for (int r = 0; r < 4; ++r) {
+                const int c = c0 + 16 * ct + q4 + r;
+                const float o = i < n ? acc[ct][it][r] : 0.0f;
+                if (c < vw) {
+                  if (a.out_f32) static_cast<float*>(a.out)[at + c] = o;
+                  else Elem<T>::store(out + at + c, o);
+                }
+              }
           }
         }
       }
-    }
 
-    // the state behind the chunk
-    const float pass = s_pw[n];
+      in_order();
+      if constexpr (kOut) {
+        __syncthreads();  // Q (and dy) have been read
+        stage_q(u0 + C);
+        stage_dy(u0 + C);
+      }
+      const int lane = own(threadIdx.x & 63), q4 = 4 * (lane >> 4);
+      // the state behind the chunk
+      const float pass = s_pw[n];
+#pragma unroll
+      for (int ct = 0; ct < CT; ++ct)
+#pragma unroll
+        for (int t = 0; t < KT; ++t)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            if constexpr (kDecay) {
+              R[ct][t][r] = __builtin_fmaf(S[ct][t][r], (float)n, R[ct][t][r]) * pass;
+              if (special && total != 0) R[ct][t][r] = 0.0f;
+            }
+            S[ct][t][r] *= pass;
+            if (special && total != 0) S[ct][t][r] = 0.0f;
+          }
+#pragma unroll
+      for (int s = 0; s < C / CK; ++s) {
+        Parts<T, NU> px[CT], px2[kDecay ? CT : 1];
+        float w[E], w2[E];
+#pragma unroll
+        for (int e = 0; e < E; e += 4) {
+          const f32x4 f = *reinterpret_cast<const f32x4*>(s_leave + CK * s + step_of(e, q4));
+#pragma unroll
+          for (int r = 0; r < 4; ++r) w[e + r] = f[r];
+          if constexpr (kDecay) {
+            const f32x4 f2 = *reinterpret_cast<const f32x4*>(s_left + CK * s + step_of(e, q4));
+#pragma unroll
+            for (int r = 0; r < 4; ++r) w2[e + r] = f2[r];
+          }
+        }
+#pragma unroll
+        for (int ct = 0; ct < CT; ++ct) {
+          float x[E], x2[E];
+#pragma unroll
+          for (int e = 0; e < E; ++e) {
+            const float v = M::at(vf[ct][s], e);
+            x[e] = v * w[e];
+            if constexpr (kDecay) x2[e] = v * w2[e];
+            if (special && B != 0 && w[e] == 0.0f) {  // not even a NaN of the steps before the last start
+              x[e] = 0.0f;
+              if constexpr (kDecay) x2[e] = 0.0f;
+            }
+          }
+          px[ct] = parts_of<NU>(x);
+          if constexpr (kDecay) px2[ct] = parts_of<NU>(x2);
+        }
+        constexpr int TT = 4;  // tiles at a time: products that do not wait for one another
+#pragma unroll
+        for (int t = 0; t < KT; t += TT) {
+          in_order();
+          Frag kf[TT];
+#pragma unroll
+          for (int i = 0; i < TT; ++i) {
+            kf[i] = M::template col<KD>(s_k, CK * s, 16 * (t + i), lane);
+            if (special && B != 0) {
+#pragma unroll
+              for (int e = 0; e < E; ++e)
+                if (w[e] == 0.0f) M::zero(kf[i], e);
+            }
+          }
+#pragma unroll
+          for (int k = 0; k < NU; ++k)
+#pragma unroll
+            for (int i = 0; i < TT; ++i)
+#pragma unroll
+              for (int ct = 0; ct < CT; ++ct) {
+                S[ct][t + i] = M::mma(kf[i], px[ct].f[k], S[ct][t + i]);
+                if constexpr (kDecay) R[ct][t + i] = M::mma(kf[i], px2[ct].f[k], R[ct][t + i]);
+              }
+        }
+      }
+    };
     if (MODE == kAttnSegments) cut |= B != 0;
-#pragma unroll
-    for (int t = 0; t < KT; ++t)
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        if constexpr (kDecay) R[t][r] = total == 0 ? __builtin_fmaf(S[t][r], (float)n, R[t][r]) * pass : 0.0f;
-        S[t][r] = total == 0 ? S[t][r] * pass : 0.0f;
-      }
-#pragma unroll
-    for (int s = 0; s < C / CK; ++s) {
-      const auto px = parts_of<NU>(x[s]);
-      const auto px2 = parts_of<NU>(x2[kDecay ? s : 0]);
-#pragma unroll
-      for (int t = 0; t < KT; ++t) {
-        Frag kf = M::col(s_k, LDK, CK * s, 16 * t, lane);
-        if (B != 0) {  // not even a NaN of the steps before the last start
-#pragma unroll
-          for (int e = 0; e < E; ++e)
-            if (seen(CK * s + E * (lane >> 4) + e) != total) M::zero(kf, e);
-        }
-#pragma unroll
-        for (int k = 0; k < NU; ++k) S[t] = M::mma(kf, px.f[k], S[t]);
-        if constexpr (kDecay) {
-#pragma unroll
-          for (int k = 0; k < NU; ++k) R[t] = M::mma(kf, px2.f[k], R[t]);
-        }
-      }
-    }
+    if (B == 0 && !careful) finish(std::false_type{});
+    else finish(std::true_type{});
   }
 
-  const int64_t mat = (int64_t)a.kd * a.vd;
+  lane = own(lane);
+  m = lane & 15;
+  q4 = 4 * (lane >> 4);
   if constexpr (MODE == kAttnSegments) {
     const int steps = min(max(len - u_begin, 0), u_end - u_begin);
-    through = cut ? 0.0f : decay_pow(g, (float)steps);
-    if (vb == 0 && threadIdx.x == 0) a.seg_through[head * a.nseg + seg] = through;
+    if (vb == 0 && threadIdx.x == 0) a.seg_through[head * a.nseg + seg] = cut ? 0.0f : decay_pow(g, (float)steps);
+  } else if constexpr (MODE == kAttnDecay) {
+    float sum = 0.0f;
+    if (dlast != nullptr) {
+      const Buf buf = make_buf(dlast + head * mat, mat * 4);
+      const StateAt at(a, false, v0 + c0 + m, q4);
+#pragma unroll
+      for (int ct = 0; ct < CT; ++ct)
+#pragma unroll
+        for (int t = 0; t < KT; ++t)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            uint32_t w[1];
+            buf_load_words<1>(buf, at.lane(16 * t + r, 16 * ct), at.fixed(16 * t + r, 16 * ct), w);
+            if (at.in(16 * t + r, 16 * ct)) sum = __builtin_fmaf(R[ct][t][r], __uint_as_float(w[0]), sum);
+          }
+    }
+    dg = wave_sum(dg + (double)sum);
+    if (lane == 0) s_sum[wave] = dg;
+    __syncthreads();
+    if (threadIdx.x == 0) a.part[((int64_t)h * a.batch + b) * nvb + vb] = (s_sum[0] + s_sum[1]) + (s_sum[2] + s_sum[3]);
+    return;
+  }
+  float* to = nullptr;
+  if (MODE == kAttnSegments) to = a.seg_state + (head * a.nseg + seg + 1) * mat;
+  else if (a.state_out != nullptr && seg == a.nseg - 1) to = a.state_out + head * mat;
+  if (to == nullptr) return;
+  // backward in time nothing passes a first step that starts a sequence
+  const bool gone = MODE == kAttnOut && a.rev && a.starts != nullptr && len > 0 && a.starts[(int64_t)b * L] != 0;
+  const Buf buf = make_buf(to, mat * 4);
+  const StateAt at(a, MODE == kAttnOut && a.transposed, v0 + c0 + m, q4);
+#pragma unroll
+  for (int ct = 0; ct < CT; ++ct)
 #pragma unroll
     for (int t = 0; t < KT; ++t)
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
-        const int row = 16 * t + q4 + r;
-        if (row < a.kd && col < a.vd)
-          a.seg_state[(head * a.nseg + seg + 1) * mat + (int64_t)row * a.vd + col] = S[t][r];
+        const uint32_t w[1] = {gone ? 0u : __float_as_uint(S[ct][t][r])};
+        buf_store_words<1>(buf, at.lane(16 * t + r, 16 * ct), at.fixed(16 * t + r, 16 * ct), w);
       }
-  } else if constexpr (MODE == kAttnOut) {
-    if (a.state_out != nullptr && seg == a.nseg - 1) {
-      // backward in time nothing passes a first step that starts a sequence
-      const bool gone = a.rev && a.starts != nullptr && len > 0 && a.starts[(int64_t)b * L] != 0;
-#pragma unroll
-      for (int t = 0; t < KT; ++t)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const int row = 16 * t + q4 + r;
-          if (row < a.kd && col < a.vd)
-            a.state_out[head * mat + (a.transposed ? (int64_t)col * a.kd + row : (int64_t)row * a.vd + col)] =
-                gone ? 0.0f : S[t][r];
-        }
-    }
-  } else {
-    if (dlast != nullptr) {
-      float sum = 0.0f;
-#pragma unroll
-      for (int t = 0; t < KT; ++t)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const int row = 16 * t + q4 + r;
-          if (row < a.kd && col < a.vd) sum = __builtin_fmaf(R[t][r], dlast[head * mat + (int64_t)row * a.vd + col], sum);
-        }
-      dg += (double)sum;
-    }
-    dg = wave_sum(dg);
-    if (lane == 0) s_sum[wave] = dg;
-    __syncthreads();
-    if (threadIdx.x == 0) {
-      double sum = 0.0;
-      for (int w = 0; w < NW; ++w) sum += s_sum[w];
-      a.part[((int64_t)h * a.batch + b) * nvb + vb] = sum;
-    }
-  }
 }
 
 // The states entering the segments from what each adds: S <- through S + added, a
@@ -632,34 +914,34 @@ __global__ __launch_bounds__(256) void attn_step_kernel(const AttnStep a) {
 
 namespace {
 
-constexpr int kColumns = 128;  // value columns of a workgroup of 8 waves
+// Tiles of value columns of a wave: 128 columns to a workgroup, or 64.
+int column_tiles(int vd) { return vd <= 64 ? 1 : 2; }
 
-template <typename T, int KD, int NW, int MODE>
+template <typename T, int KD, int CT, int MODE>
 hipError_t sweep(const AttnSweep& a, const float* dlast, hipStream_t stream) {
-  const int nvb = (a.vd + 16 * NW - 1) / (16 * NW);
+  const int nvb = (a.vd + 64 * CT - 1) / (64 * CT);
   const int nsegs = MODE == kAttnSegments ? a.nseg - 1 : MODE == kAttnDecay ? 1 : a.nseg;
-  attn_sweep_kernel<T, KD, NW, MODE>
-      <<<grid_of((int64_t)a.batch * a.heads * nvb * nsegs, 64 * NW), 64 * NW, 0, stream>>>(a, dlast);
+  const int64_t groups = (int64_t)a.batch * a.heads * nvb * nsegs;
+  attn_sweep_kernel<T, KD, CT, MODE><<<grid_of((groups + 7) / 8 * 8, kThreads), kThreads, 0, stream>>>(a, dlast, groups);
   return hipGetLastError();
 }
 
-template <typename T, int MODE>
+template <typename T, int CT, int MODE>
 hipError_t sweep_of(const AttnSweep& a, const float* dlast, hipStream_t stream) {
-  const int kd = a.kd <= 64 ? 64 : a.kd <= 128 ? 128 : 256;
-  if (a.vd <= 64) {
-    if (kd == 64) return sweep<T, 64, 4, MODE>(a, dlast, stream);
-    if (kd == 128) return sweep<T, 128, 4, MODE>(a, dlast, stream);
-    return sweep<T, 256, 4, MODE>(a, dlast, stream);
-  }
-  if (kd == 64) return sweep<T, 64, 8, MODE>(a, dlast, stream);
-  if (kd == 128) return sweep<T, 128, 8, MODE>(a, dlast, stream);
-  return sweep<T, 256, 8, MODE>(a, dlast, stream);
+  if (a.kd <= 64) return sweep<T, 64, CT, MODE>(a, dlast, stream);
+  if (a.kd <= 128) return sweep<T, 128, CT, MODE>(a, dlast, stream);
+  return sweep<T, 256, CT, MODE>(a, dlast, stream);
+}
+
+template <typename T, int MODE>
+hipError_t sweep_of(const AttnSweep& a, hipStream_t stream) {
+  return column_tiles(a.vd) == 1 ? sweep_of<T, 1, MODE>(a, nullptr, stream) : sweep_of<T, 2, MODE>(a, nullptr, stream);
 }
 
 template <typename T>
 hipError_t run_sweep(const AttnSweep& a, hipStream_t stream) {
   if (a.nseg > 1) {
-    hipError_t e = sweep_of<T, kAttnSegments>(a, nullptr, stream);
+    hipError_t e = sweep_of<T, kAttnSegments>(a, stream);
     if (e != hipSuccess) return e;
     const int64_t n = (int64_t)a.batch * a.heads * a.kd * a.vd;
     attn_carry_kernel<<<grid_of((n + 255) / 256, 256), 256, 0, stream>>>(a.seg_state, a.seg_through, a.state_in, a.kd,
@@ -667,12 +949,14 @@ hipError_t run_sweep(const AttnSweep& a, hipStream_t stream) {
     e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
-  return sweep_of<T, kAttnOut>(a, nullptr, stream);
+  return sweep_of<T, kAttnOut>(a, stream);
 }
 
 }  // namespace
 
-int attn_column_blocks(int vd) { return vd <= 64 ? 1 : (vd + kColumns - 1) / kColumns; }
+int attn_column_blocks(int vd) { return (vd + 64 * column_tiles(vd) - 1) / (64 * column_tiles(vd)); }
+
+int attn_decay_blocks(int vd) { return (vd + 63) / 64; }
 
 AttnSplit attn_split(int batch, int heads, int64_t seqlen, int vd) {
   // two workgroups for each of the 256 CUs, segments of 4 chunks at least
@@ -690,10 +974,10 @@ hipError_t launch_attn_sweep(const AttnSweep& a, hipStream_t stream) {
 }
 
 hipError_t launch_attn_decay_grad(const AttnSweep& a, const float* dlast, float* dlog_decay, hipStream_t stream) {
-  const hipError_t e = a.dtype == Dtype::BF16 ? sweep_of<uint16_t, kAttnDecay>(a, dlast, stream)
-                                              : sweep_of<float, kAttnDecay>(a, dlast, stream);
+  const hipError_t e = a.dtype == Dtype::BF16 ? sweep_of<uint16_t, 1, kAttnDecay>(a, dlast, stream)
+                                              : sweep_of<float, 1, kAttnDecay>(a, dlast, stream);
   if (e != hipSuccess) return e;
-  attn_decay_sum_kernel<<<a.heads, 64, 0, stream>>>(a.part, dlog_decay, a.batch * attn_column_blocks(a.vd));
+  attn_decay_sum_kernel<<<a.heads, 64, 0, stream>>>(a.part, dlog_decay, a.batch * attn_decay_blocks(a.vd));
   return hipGetLastError();
 }
 

@@ -52,8 +52,9 @@ struct AttnSplit {
   int64_t seglen;
 };
 AttnSplit attn_split(int batch, int heads, int64_t seqlen, int vd);
-// Blocks of value columns.
+// Blocks of value columns, of a sweep and of the decay's gradient.
 int attn_column_blocks(int vd);
+int attn_decay_blocks(int vd);
 
 struct AttnStep {
   AttnView q, k, v;  // (batch, head, width): st is not used
