@@ -136,6 +136,14 @@ struct Mat<uint16_t> {
   __device__ __forceinline__ static float at(const Frag& f, int e) { return (float)f[e]; }
   __device__ __forceinline__ static void zero(Frag& f, int e) { f[e] = (__bf16)0.0f; }
   __device__ __forceinline__ static void set(Frag& f, int e, float v) { f[e] = (__bf16)v; }
+  // sum + 0 f: NaN if an element is not finite
+  __device__ __forceinline__ static float times_zero(const Frag& f, float sum) {
+    typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+    const bf16x2 nil = {(__bf16)0.0f, (__bf16)0.0f};
+#pragma unroll
+    for (int e = 0; e < E; e += 2) sum = __builtin_amdgcn_fdot2_f32_bf16(bf16x2{f[e], f[e + 1]}, nil, sum, false);
+    return sum;
+  }
 };
 
 template <>
@@ -166,6 +174,11 @@ struct Mat<float> {
   __device__ __forceinline__ static float at(const Frag& f, int e) { return f[e]; }
   __device__ __forceinline__ static void zero(Frag& f, int e) { f[e] = 0.0f; }
   __device__ __forceinline__ static void set(Frag& f, int e, float v) { f[e] = v; }
+  __device__ __forceinline__ static float times_zero(const Frag& f, float sum) {
+#pragma unroll
+    for (int e = 0; e < E; ++e) sum = __builtin_fmaf(f[e], 0.0f, sum);
+    return sum;
+  }
 };
 
 // The step (of CK) that element e of a lane's fragment is, q4 = 4 (lane / 16).
@@ -231,6 +244,14 @@ __device__ __forceinline__ Slice slice_of(const AttnView& w, int64_t b, int h, i
 // whose lanes name what belongs there; an offset behind the extent gives zeros.
 // They are under way until landed().  Slices that cannot be read in vectors are
 // copied element by element.
+__device__ __forceinline__ void copy_to_lds(uint32_t to, uint32_t at, u32x4_t buf, uint32_t base) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
+               :
+               : "s"(__builtin_amdgcn_readfirstlane(to)), "v"(at), "s"(buf),
+                 "s"(__builtin_amdgcn_readfirstlane(base))
+               : "memory", "m0");
+}
+
 template <typename T, int ROWS, int W>
 __device__ __forceinline__ void stage(T* lds, const Slice& s, int u, int width, int n, int wave) {
   using At = Tile<T, W>;
@@ -248,15 +269,25 @@ __device__ __forceinline__ void stage(T* lds, const Slice& s, int u, int width, 
     buf.z = 0x7fffffffu;
     buf.w = 0x00020000u;
     const uint32_t to = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(lds_char*)lds);
+    // access k of a wave: rows kStep k and more, whose pieces are in one order for every k
+    // (but with 32 and 64 pieces to a row)
+    constexpr int kStep = ROWS / kAccesses;
+    const int r0 = (wave * 64 + lane) / At::kPieces;
+    if (n == ROWS) {
 #pragma unroll
-    for (int k = 0; k < kAccesses; ++k) {
-      const int piece = (wave * kAccesses + k) * 64 + lane;
-      const int r = piece / At::kPieces, c = ((piece % At::kPieces) ^ At::order(r)) * At::kPiece;
-      const uint32_t at = (uint32_t)(rev ? n - 1 - r : r) * st + (uint32_t)(c * (int)sizeof(T));
-      asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
-                   :
-                   : "s"(to + (uint32_t)(wave * kAccesses + k) * 1024u), "v"(r < n && c < width ? at : kNowhere), "s"(buf)
-                   : "memory", "m0");
+      for (int k = 0; k < kAccesses; ++k) {
+        const int c = (lane % At::kPieces ^ At::order(r0 + k * kStep)) * At::kPiece;
+        const uint32_t at = (uint32_t)(rev ? kStep - 1 - r0 : r0) * st + (uint32_t)(c * (int)sizeof(T));
+        copy_to_lds(to + (uint32_t)(k * kWaves + wave) * 1024u, c < width ? at : kNowhere, buf,
+                    (uint32_t)((rev ? kAccesses - 1 - k : k) * kStep) * st);
+      }
+    } else {
+#pragma unroll 1
+      for (int k = 0; k < kAccesses; ++k) {
+        const int r = r0 + k * kStep, c = (lane % At::kPieces ^ At::order(r)) * At::kPiece;
+        const uint32_t at = (uint32_t)(rev ? n - 1 - r : r) * st + (uint32_t)(c * (int)sizeof(T));
+        copy_to_lds(to + (uint32_t)(k * kWaves + wave) * 1024u, r < n && c < width ? at : kNowhere, buf, 0);
+      }
     }
   } else {
 #pragma unroll 1
@@ -288,6 +319,10 @@ struct StateAt {
 
 }  // namespace
 
+// Tiles of P on and below the diagonal, row by row: 2 bits of each one's row and column.
+__device__ __forceinline__ int tile_row(int tile) { return (0xffa94 >> (2 * tile)) & 3; }
+__device__ __forceinline__ int tile_col(int tile) { return (0xe4910 >> (2 * tile)) & 3; }
+
 enum AttnMode { kAttnOut = 0, kAttnSegments = 1, kAttnDecay = 2 };
 
 // One workgroup: kWaves waves, CT tiles of 16 value columns each.  kAttnSegments: only
@@ -300,7 +335,7 @@ enum AttnMode { kAttnOut = 0, kAttnSegments = 1, kAttnDecay = 2 };
 // The next chunk's tiles are copied to LDS while this one is worked on: K, wanted to
 // the end, into a second buffer, V and Q into their own once every wave has done with
 // them.  (Through registers the state would not fit beside them.)
-template <typename T, int KD, int CT, int MODE>
+template <typename T, int KD, int CT, int MODE, bool PACKED>
 __global__ __launch_bounds__(kThreads, KD <= 128 ? 2 : 1) void attn_sweep_kernel(const AttnSweep a,
                                                                                 const float* __restrict__ dlast,
                                                                                 int64_t groups) {
@@ -430,6 +465,21 @@ __global__ __launch_bounds__(kThreads, KD <= 128 ? 2 : 1) void attn_sweep_kernel
   stage_dy(u_begin);
   int turn = 0;
 
+  // this wave's tiles of P: e^{g (i-j)} of the lane's steps, 0 above the diagonal
+  float wp[kOut ? kMyTiles : 1][4];
+  if constexpr (kOut) {
+#pragma unroll
+    for (int k = 0; k < kMyTiles; ++k) {
+      const int tile = min(wave + k * kWaves, kTiles - 1);
+      const int apart = 16 * (tile_row(tile) - tile_col(tile)) + m - q4;
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        wp[k][r] = apart >= r ? decay_pow(g, (float)(apart - r)) * a.scale_p : 0.0f;
+        if (kDecay) wp[k][r] *= (float)(apart - r);
+      }
+    }
+  }
+
   for (int u0 = u_begin; u0 < u_end; u0 += C) {
     const int n = valid(u0);
     if (n == 0 && MODE != kAttnOut) break;
@@ -444,7 +494,7 @@ __global__ __launch_bounds__(kThreads, KD <= 128 ? 2 : 1) void attn_sweep_kernel
     }
     // bit i: no state and no product crosses from step i-1 to step i
     uint64_t B = 0;
-    if (a.starts != nullptr) {
+    if constexpr (PACKED) {
       const int u = u0 + lane;
       bool f = false;
       if (lane < n && !(a.rev && u == 0)) f = a.starts[(int64_t)b * L + (a.rev ? len - u : u)] != 0;
@@ -468,48 +518,42 @@ __global__ __launch_bounds__(kThreads, KD <= 128 ? 2 : 1) void attn_sweep_kernel
 
     if constexpr (kOut) {
       // P = W o Q K^T, tile (it, jt) at a time, transposed so that a lane holds 4 steps j of a row i
-      const auto products = [&](auto packed) {
-        const int lane = own(threadIdx.x & 63), m = lane & 15, q4 = 4 * (lane >> 4);
+      const int lane = own(threadIdx.x & 63), m = lane & 15, q4 = 4 * (lane >> 4);
 #pragma unroll
-        for (int k = 0; k < kMyTiles; ++k) {
-          const int tile = wave + k * kWaves;
-          if (tile >= kTiles) break;
-          in_order();
-          const int it = (0xffa94 >> (2 * tile)) & 3, jt = (0xe4910 >> (2 * tile)) & 3;  // row by row
-          f32x4 acc = {0, 0, 0, 0};
+      for (int k = 0; k < kMyTiles; ++k) {
+        const int tile = wave + k * kWaves;
+        if (tile >= kTiles) break;
+        in_order();
+        const int it = tile_row(tile), jt = tile_col(tile);
+        f32x4 acc = {0, 0, 0, 0};
 #pragma unroll
-          for (int kk = 0; kk < KD; kk += CK)
-            acc = M::mma(M::template run<KD>(s_k, 16 * jt, kk, lane), M::template run<KD>(s_q, 16 * it, kk, lane), acc);
-          const int i = 16 * it + m;
-          float p[4];
+        for (int kk = 0; kk < KD; kk += CK)
+          acc = M::mma(M::template run<KD>(s_k, 16 * jt, kk, lane), M::template run<KD>(s_q, 16 * it, kk, lane), acc);
+        const int i = 16 * it + m;
+        float p[4];
 #pragma unroll
-          for (int r = 0; r < 4; ++r) {
-            const int j = 16 * jt + q4 + r;
-            const bool kept = j <= i && (!packed || seen(i) == seen(j));
-            float w = s_pw[j <= i ? i - j : 0] * a.scale_p;
-            if (kDecay) w *= (float)(i - j);
-            p[r] = kept ? acc[r] * w : 0.0f;
-          }
-          const int dst = Tile<T, C>::at(i, 16 * jt + q4);
-          if constexpr (sizeof(T) == 2) {
-            if constexpr (kLow) {
-              float lo[4];
-#pragma unroll
-              for (int r = 0; r < 4; ++r) {
-                const float hi = cut16(p[r]);
-                lo[r] = p[r] - hi;
-                p[r] = hi;
-              }
-              *reinterpret_cast<uint2*>(s_p2 + dst) = make_uint2(pack_bf16x2(lo[0], lo[1]), pack_bf16x2(lo[2], lo[3]));
-            }
-            *reinterpret_cast<uint2*>(s_p + dst) = make_uint2(pack_bf16x2(p[0], p[1]), pack_bf16x2(p[2], p[3]));
-          } else {
-            *reinterpret_cast<f32x4*>(s_p + dst) = f32x4{p[0], p[1], p[2], p[3]};
-          }
+        for (int r = 0; r < 4; ++r) {
+          bool kept = wp[k][r] != 0.0f;
+          if (PACKED && B != 0) kept = kept && seen(i) == seen(16 * jt + q4 + r);
+          p[r] = kept ? acc[r] * wp[k][r] : 0.0f;
         }
-      };
-      if (B == 0) products(std::false_type{});
-      else products(std::true_type{});
+        const int dst = Tile<T, C>::at(i, 16 * jt + q4);
+        if constexpr (sizeof(T) == 2) {
+          if constexpr (kLow) {
+            float lo[4];
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+              const float hi = cut16(p[r]);
+              lo[r] = p[r] - hi;
+              p[r] = hi;
+            }
+            *reinterpret_cast<uint2*>(s_p2 + dst) = make_uint2(pack_bf16x2(lo[0], lo[1]), pack_bf16x2(lo[2], lo[3]));
+          }
+          *reinterpret_cast<uint2*>(s_p + dst) = make_uint2(pack_bf16x2(p[0], p[1]), pack_bf16x2(p[2], p[3]));
+        } else {
+          *reinterpret_cast<f32x4*>(s_p + dst) = f32x4{p[0], p[1], p[2], p[3]};
+        }
+      }
     }
 
     // this wave's columns of V, contracted over the steps
@@ -520,16 +564,66 @@ __global__ __launch_bounds__(kThreads, KD <= 128 ? 2 : 1) void attn_sweep_kernel
 #pragma unroll
       for (int s = 0; s < C / CK; ++s) {
         vf[ct][s] = M::template col<NV>(s_v, CK * s, c0 + 16 * ct, lane);
-#pragma unroll
-        for (int e = 0; e < E; ++e) odd = __builtin_fmaf(M::at(vf[ct][s], e), 0.0f, odd);
+        odd = M::times_zero(vf[ct][s], odd);
       }
     const bool careful = __any(!(odd == 0.0f));
     __syncthreads();  // P and the weights are there, V is in registers
     stage_v(u0 + C);
 
-    // The outputs and the state behind the chunk.  `special`: a sequence starts in the
-    // chunk, or one of the wave's values is not finite.
-    const auto finish = [&](auto special) {
+    // Values that are not finite are left out of the products, where the zeros of P above
+    // its diagonal (and of the rows that pad K) would spread them.  Products of ones in their
+    // places with ones where P has its steps count what each output takes of them: those
+    // are NaN, and the columns of S that one reaches.
+    uint32_t nan_out = 0, nan_state = 0;  // bits 16 ct + 4 it + r, and ct
+    if (careful) {
+      const int m = lane & 15, q4 = 4 * (lane >> 4);
+      if constexpr (kOut) {
+#pragma unroll 1
+        for (int it = 0; it < IT; ++it) {
+          const int i = 16 * it + m;
+          f32x4 bad[CT];
+#pragma unroll
+          for (int ct = 0; ct < CT; ++ct) bad[ct] = f32x4{0, 0, 0, 0};
+#pragma unroll
+          for (int s = 0; s < C / CK; ++s) {
+            Frag taken, one;
+#pragma unroll
+            for (int e = 0; e < E; ++e) {
+              const int j = CK * s + step_of(e, q4);
+              M::set(taken, e, j <= i && (!PACKED || seen(i) == seen(j)) ? 1.0f : 0.0f);
+            }
+#pragma unroll
+            for (int ct = 0; ct < CT; ++ct) {
+#pragma unroll
+              for (int e = 0; e < E; ++e) M::set(one, e, finite_f32(M::at(vf[ct][s], e)) ? 0.0f : 1.0f);
+              bad[ct] = M::mma(one, taken, bad[ct]);
+            }
+          }
+#pragma unroll
+          for (int ct = 0; ct < CT; ++ct)
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+              if (bad[ct][r] != 0.0f) nan_out |= 1u << (16 * ct + 4 * it + r);
+        }
+      }
+#pragma unroll
+      for (int ct = 0; ct < CT; ++ct) {
+        int any = 0;
+#pragma unroll
+        for (int s = 0; s < C / CK; ++s)
+#pragma unroll
+          for (int e = 0; e < E; ++e)
+            if (!finite_f32(M::at(vf[ct][s], e))) {
+              if (!PACKED || seen(CK * s + step_of(e, q4)) == total) any = 1;
+              M::zero(vf[ct][s], e);
+            }
+        any |= __shfl_xor(any, 16);
+        any |= __shfl_xor(any, 32);
+        nan_state |= (uint32_t)any << ct;
+      }
+    }
+
+    {
       if constexpr (kOut) {
         const int lane = own(threadIdx.x & 63), m = lane & 15, q4 = 4 * (lane >> 4);
         f32x4 acc[CT][IT], acc_r[kDecay ? CT : 1][kDecay ? IT : 1];
@@ -573,75 +667,39 @@ __global__ __launch_bounds__(kThreads, KD <= 128 ? 2 : 1) void attn_sweep_kernel
         for (int it = 0; it < IT; ++it) {
           const int i = 16 * it + m;
           const float w = s_enter[i];
-          const bool dropped = special && B != 0 && seen(i) != 0;
 #pragma unroll
           for (int ct = 0; ct < CT; ++ct)
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
               float o = acc[ct][it][r];
               if constexpr (kDecay) o = __builtin_fmaf(o, (float)(i + 1), acc_r[ct][it][r]);
-              acc[ct][it][r] = dropped ? 0.0f : o * w;
+              acc[ct][it][r] = PACKED && w == 0.0f ? 0.0f : o * w;
             }
         }
         in_order();
 #pragma unroll
         for (int s = 0; s < C / CK; ++s) {
-          Frag fv[CT];
-#pragma unroll
-          for (int ct = 0; ct < CT; ++ct) {
-            fv[ct] = vf[ct][s];
-            if (special && careful) {
-#pragma unroll
-              for (int e = 0; e < E; ++e)
-                if (!finite_f32(M::at(fv[ct], e))) M::zero(fv[ct], e);
-            }
-          }
 #pragma unroll
           for (int it = 0; it < IT; ++it) {
             if (CK * s >= 16 * (it + 1)) continue;
             const Frag fp = M::template row<C>(s_p, 16 * it, CK * s, lane);
 #pragma unroll
-            for (int ct = 0; ct < CT; ++ct) acc[ct][it] = M::mma(fv[ct], fp, acc[ct][it]);
+            for (int ct = 0; ct < CT; ++ct) acc[ct][it] = M::mma(vf[ct][s], fp, acc[ct][it]);
             if constexpr (kLow) {
               const Frag fl = M::template row<C>(s_p2, 16 * it, CK * s, lane);
 #pragma unroll
-              for (int ct = 0; ct < CT; ++ct) acc[ct][it] = M::mma(fv[ct], fl, acc[ct][it]);
+              for (int ct = 0; ct < CT; ++ct) acc[ct][it] = M::mma(vf[ct][s], fl, acc[ct][it]);
             }
           }
         }
-        // Values that are not finite were left out of the product with P, whose zeros above
-        // the diagonal they would turn into NaN.  Products of ones in their places with ones
-        // where P has its steps count what each output takes of them.
-        if (special && careful) {
+        if (careful) {
 #pragma unroll
-          for (int it = 0; it < IT; ++it) {
-            const int i = 16 * it + m;
-            f32x4 bad[CT];
+          for (int ct = 0; ct < CT; ++ct)
 #pragma unroll
-            for (int ct = 0; ct < CT; ++ct) bad[ct] = f32x4{0, 0, 0, 0};
-#pragma unroll
-            for (int s = 0; s < C / CK; ++s) {
-              if (CK * s >= 16 * (it + 1)) continue;
-              Frag taken;
-#pragma unroll
-              for (int e = 0; e < E; ++e) {
-                const int j = CK * s + step_of(e, q4);
-                M::set(taken, e, j <= i && (B == 0 || seen(i) == seen(j)) ? 1.0f : 0.0f);
-              }
-#pragma unroll
-              for (int ct = 0; ct < CT; ++ct) {
-                Frag one;
-#pragma unroll
-                for (int e = 0; e < E; ++e) M::set(one, e, finite_f32(M::at(vf[ct][s], e)) ? 0.0f : 1.0f);
-                bad[ct] = M::mma(one, taken, bad[ct]);
-              }
-            }
-#pragma unroll
-            for (int ct = 0; ct < CT; ++ct)
+            for (int it = 0; it < IT; ++it)
 #pragma unroll
               for (int r = 0; r < 4; ++r)
-                if (bad[ct][r] != 0.0f) acc[ct][it][r] = __builtin_nanf("");
-          }
+                if (nan_out >> (16 * ct + 4 * it + r) & 1) acc[ct][it][r] = __builtin_nanf("");
         }
         if constexpr (kDecay) {
           float sum = 0.0f;
@@ -716,10 +774,10 @@ __global__ __launch_bounds__(kThreads, KD <= 128 ? 2 : 1) void attn_sweep_kernel
           for (int r = 0; r < 4; ++r) {
             if constexpr (kDecay) {
               R[ct][t][r] = __builtin_fmaf(S[ct][t][r], (float)n, R[ct][t][r]) * pass;
-              if (special && total != 0) R[ct][t][r] = 0.0f;
+              if (PACKED && total != 0) R[ct][t][r] = 0.0f;
             }
             S[ct][t][r] *= pass;
-            if (special && total != 0) S[ct][t][r] = 0.0f;
+            if (PACKED && total != 0) S[ct][t][r] = 0.0f;
           }
 #pragma unroll
       for (int s = 0; s < C / CK; ++s) {
@@ -744,10 +802,6 @@ __global__ __launch_bounds__(kThreads, KD <= 128 ? 2 : 1) void attn_sweep_kernel
             const float v = M::at(vf[ct][s], e);
             x[e] = v * w[e];
             if constexpr (kDecay) x2[e] = v * w2[e];
-            if (special && B != 0 && w[e] == 0.0f) {  // not even a NaN of the steps before the last start
-              x[e] = 0.0f;
-              if constexpr (kDecay) x2[e] = 0.0f;
-            }
           }
           px[ct] = parts_of<NU>(x);
           if constexpr (kDecay) px2[ct] = parts_of<NU>(x2);
@@ -760,7 +814,7 @@ __global__ __launch_bounds__(kThreads, KD <= 128 ? 2 : 1) void attn_sweep_kernel
 #pragma unroll
           for (int i = 0; i < TT; ++i) {
             kf[i] = M::template col<KD>(s_k, CK * s, 16 * (t + i), lane);
-            if (special && B != 0) {
+            if constexpr (PACKED) {  // not even a NaN of the steps before the last start
 #pragma unroll
               for (int e = 0; e < E; ++e)
                 if (w[e] == 0.0f) M::zero(kf[i], e);
@@ -777,10 +831,20 @@ __global__ __launch_bounds__(kThreads, KD <= 128 ? 2 : 1) void attn_sweep_kernel
               }
         }
       }
-    };
+      if (careful) {
+#pragma unroll
+        for (int ct = 0; ct < CT; ++ct)
+          if (nan_state >> ct & 1) {
+#pragma unroll
+            for (int t = 0; t < KT; ++t) {
+              const float v = __builtin_nanf("");
+              S[ct][t] = f32x4{v, v, v, v};
+              if constexpr (kDecay) R[ct][t] = S[ct][t];
+            }
+          }
+      }
+    }
     if (MODE == kAttnSegments) cut |= B != 0;
-    if (B == 0 && !careful) finish(std::false_type{});
-    else finish(std::true_type{});
   }
 
   lane = own(lane);
@@ -922,7 +986,9 @@ hipError_t sweep(const AttnSweep& a, const float* dlast, hipStream_t stream) {
   const int nvb = (a.vd + 64 * CT - 1) / (64 * CT);
   const int nsegs = MODE == kAttnSegments ? a.nseg - 1 : MODE == kAttnDecay ? 1 : a.nseg;
   const int64_t groups = (int64_t)a.batch * a.heads * nvb * nsegs;
-  attn_sweep_kernel<T, KD, CT, MODE><<<grid_of((groups + 7) / 8 * 8, kThreads), kThreads, 0, stream>>>(a, dlast, groups);
+  const dim3 grid = grid_of((groups + 7) / 8 * 8, kThreads);
+  if (a.starts != nullptr) attn_sweep_kernel<T, KD, CT, MODE, true><<<grid, kThreads, 0, stream>>>(a, dlast, groups);
+  else attn_sweep_kernel<T, KD, CT, MODE, false><<<grid, kThreads, 0, stream>>>(a, dlast, groups);
   return hipGetLastError();
 }
 
