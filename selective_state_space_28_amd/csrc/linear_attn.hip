@@ -38,6 +38,9 @@ typedef __attribute__((address_space(3))) char lds_char;
 // take registers that the state needs.
 __device__ __forceinline__ void in_order() { __builtin_amdgcn_sched_barrier(0); }
 
+// Keeps what is seldom done a branch, not a selection that every pass makes.
+__device__ __forceinline__ void in_branch() { asm volatile(""); }
+
 // A lane's number as a value of its own: LDS addresses formed from it, one
 // instruction each, are neither formed before the loop nor shared with other code,
 // and held in registers meanwhile.
@@ -242,7 +245,7 @@ __device__ __forceinline__ Slice slice_of(const AttnView& w, int64_t b, int h, i
 // ROWS x W elements of a slice into LDS: zeros from column `width` and from row n on.
 // The copies go past the registers, 1 KiB of LDS in one piece for a wave's access,
 // whose lanes name what belongs there; an offset behind the extent gives zeros.
-// They are under way until landed().  Slices that cannot be read in vectors are
+// They are under way until a wait for them.  Slices that cannot be read in vectors are
 // copied element by element.
 __device__ __forceinline__ void copy_to_lds(uint32_t to, uint32_t at, u32x4_t buf, uint32_t base) {
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
@@ -299,8 +302,6 @@ __device__ __forceinline__ void stage(T* lds, const Slice& s, int u, int width, 
     }
   }
 }
-
-__device__ __forceinline__ void landed() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
 
 // Where the elements of S lie in memory, (kd, vd) or turned: a lane's offset, and what
 // is the same for every lane.  Rows and columns that pad S lie nowhere.
@@ -464,6 +465,7 @@ __global__ __launch_bounds__(kThreads, KD <= 128 ? 2 : 1) void attn_sweep_kernel
   stage_v(u_begin);
   stage_dy(u_begin);
   int turn = 0;
+  bool stored = false;
 
   // this wave's tiles of P: e^{g (i-j)} of the lane's steps, 0 above the diagonal
   float wp[kOut ? kMyTiles : 1][4];
@@ -503,7 +505,11 @@ __global__ __launch_bounds__(kThreads, KD <= 128 ? 2 : 1) void attn_sweep_kernel
     const auto seen = [&](int i) { return __popcll(B & (~0ull >> (63 - i))); };  // starts up to and with step i
     const int total = seen(n - 1);
 
-    landed();
+    // (the accesses of a wave end in the order in which they began: of those after its
+    // copies, the stores of whole chunks, none is waited for)
+    if (stored) asm volatile("s_waitcnt vmcnt(%0)" : : "n"(IT * CT) : "memory");
+    else asm volatile("s_waitcnt vmcnt(0)" : : : "memory");
+    stored = false;
     __syncthreads();  // the tiles are there, and the chunk before is done with LDS
     const T* s_k = s_keys[turn];
     turn ^= 1;
@@ -521,7 +527,8 @@ __global__ __launch_bounds__(kThreads, KD <= 128 ? 2 : 1) void attn_sweep_kernel
       const int lane = own(threadIdx.x & 63), m = lane & 15, q4 = 4 * (lane >> 4);
 #pragma unroll
       for (int k = 0; k < kMyTiles; ++k) {
-        const int tile = wave + k * kWaves;
+        int tile = wave + k * kWaves;
+        asm volatile("" : "+s"(tile));  // (as `own`)
         if (tile >= kTiles) break;
         in_order();
         const int it = tile_row(tile), jt = tile_col(tile);
@@ -567,9 +574,49 @@ __global__ __launch_bounds__(kThreads, KD <= 128 ? 2 : 1) void attn_sweep_kernel
         odd = M::times_zero(vf[ct][s], odd);
       }
     const bool careful = __any(!(odd == 0.0f));
-    __syncthreads();  // P and the weights are there, V is in registers
+    f32x4 acc[kOut ? CT : 1][kOut ? IT : 1], acc_r[kDecay ? CT : 1][kDecay ? IT : 1];
+    if constexpr (kOut) {
+      const int lane = own(threadIdx.x & 63);
+#pragma unroll
+      for (int ct = 0; ct < CT; ++ct)
+#pragma unroll
+        for (int it = 0; it < IT; ++it) {
+          acc[ct][it] = f32x4{0, 0, 0, 0};
+          if constexpr (kDecay) acc_r[ct][it] = f32x4{0, 0, 0, 0};
+        }
+      // (Q S)^T: a lane holds 4 value columns of a step
+#pragma unroll
+      for (int kk = 0; kk < KD / CK; ++kk) {
+        in_order();
+        Parts<T, NS> ps[CT], pr[kDecay ? CT : 1];
+        Frag fq[IT];
+#pragma unroll
+        for (int it = 0; it < IT; ++it) fq[it] = M::template row<KD>(s_q, 16 * it, kk * CK, lane);
+#pragma unroll
+        for (int ct = 0; ct < CT; ++ct) {
+          float sv[E], rv[E];
+#pragma unroll
+          for (int e = 0; e < E; ++e) {
+            sv[e] = S[ct][kk * (CK / 16) + e / 4][e % 4];
+            if constexpr (kDecay) rv[e] = R[ct][kk * (CK / 16) + e / 4][e % 4];
+          }
+          ps[ct] = parts_of<NS>(sv);
+          if constexpr (kDecay) pr[ct] = parts_of<NS>(rv);
+        }
+#pragma unroll
+        for (int k = 0; k < NS; ++k)
+#pragma unroll
+          for (int it = 0; it < IT; ++it)
+#pragma unroll
+            for (int ct = 0; ct < CT; ++ct) {
+              acc[ct][it] = M::mma(ps[ct].f[k], fq[it], acc[ct][it]);
+              if constexpr (kDecay) acc_r[ct][it] = M::mma(pr[ct].f[k], fq[it], acc_r[ct][it]);
+            }
+      }
+    }
+    __syncthreads();  // P and the weights are there, Q has been read, V is in registers
+    stage_q(u0 + C);
     stage_v(u0 + C);
-
     // Values that are not finite are left out of the products, where the zeros of P above
     // its diagonal (and of the rows that pad K) would spread them.  Products of ones in their
     // places with ones where P has its steps count what each output takes of them: those
@@ -626,43 +673,6 @@ __global__ __launch_bounds__(kThreads, KD <= 128 ? 2 : 1) void attn_sweep_kernel
     {
       if constexpr (kOut) {
         const int lane = own(threadIdx.x & 63), m = lane & 15, q4 = 4 * (lane >> 4);
-        f32x4 acc[CT][IT], acc_r[kDecay ? CT : 1][kDecay ? IT : 1];
-#pragma unroll
-        for (int ct = 0; ct < CT; ++ct)
-#pragma unroll
-          for (int it = 0; it < IT; ++it) {
-            acc[ct][it] = f32x4{0, 0, 0, 0};
-            if constexpr (kDecay) acc_r[ct][it] = f32x4{0, 0, 0, 0};
-          }
-        // (Q S)^T: a lane holds 4 value columns of a step
-#pragma unroll
-        for (int kk = 0; kk < KD / CK; ++kk) {
-          in_order();
-          Parts<T, NS> ps[CT], pr[kDecay ? CT : 1];
-          Frag fq[IT];
-#pragma unroll
-          for (int it = 0; it < IT; ++it) fq[it] = M::template row<KD>(s_q, 16 * it, kk * CK, lane);
-#pragma unroll
-          for (int ct = 0; ct < CT; ++ct) {
-            float sv[E], rv[E];
-#pragma unroll
-            for (int e = 0; e < E; ++e) {
-              sv[e] = S[ct][kk * (CK / 16) + e / 4][e % 4];
-              if constexpr (kDecay) rv[e] = R[ct][kk * (CK / 16) + e / 4][e % 4];
-            }
-            ps[ct] = parts_of<NS>(sv);
-            if constexpr (kDecay) pr[ct] = parts_of<NS>(rv);
-          }
-#pragma unroll
-          for (int k = 0; k < NS; ++k)
-#pragma unroll
-            for (int it = 0; it < IT; ++it)
-#pragma unroll
-              for (int ct = 0; ct < CT; ++ct) {
-                acc[ct][it] = M::mma(ps[ct].f[k], fq[it], acc[ct][it]);
-                if constexpr (kDecay) acc_r[ct][it] = M::mma(pr[ct].f[k], fq[it], acc_r[ct][it]);
-              }
-        }
 #pragma unroll
         for (int it = 0; it < IT; ++it) {
           const int i = 16 * it + m;
@@ -693,6 +703,7 @@ __global__ __launch_bounds__(kThreads, KD <= 128 ? 2 : 1) void attn_sweep_kernel
           }
         }
         if (careful) {
+          in_branch();
 #pragma unroll
           for (int ct = 0; ct < CT; ++ct)
 #pragma unroll
@@ -715,6 +726,7 @@ __global__ __launch_bounds__(kThreads, KD <= 128 ? 2 : 1) void attn_sweep_kernel
               }
           dg += (double)sum;
         } else if (whole_out && n == C) {
+          stored = true;
           // the chunk's lowest row first
           const int64_t t0 = a.rev ? len - C - u0 : u0;
           const Buf buf = make_buf(out + (((int64_t)b * L + t0) * a.heads + h) * a.vd + v0, 0x7fffffff);
@@ -758,9 +770,8 @@ __global__ __launch_bounds__(kThreads, KD <= 128 ? 2 : 1) void attn_sweep_kernel
       }
 
       in_order();
-      if constexpr (kOut) {
-        __syncthreads();  // Q (and dy) have been read
-        stage_q(u0 + C);
+      if constexpr (kDecay) {
+        __syncthreads();  // dy has been read
         stage_dy(u0 + C);
       }
       const int lane = own(threadIdx.x & 63), q4 = 4 * (lane >> 4);
@@ -832,6 +843,7 @@ __global__ __launch_bounds__(kThreads, KD <= 128 ? 2 : 1) void attn_sweep_kernel
         }
       }
       if (careful) {
+        in_branch();
 #pragma unroll
         for (int ct = 0; ct < CT; ++ct)
           if (nan_state >> ct & 1) {
