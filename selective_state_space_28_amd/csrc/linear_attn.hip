@@ -29,6 +29,7 @@ namespace ssm {
 namespace {
 
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
@@ -39,7 +40,7 @@ typedef __attribute__((address_space(3))) char lds_char;
 __device__ __forceinline__ void in_order() { __builtin_amdgcn_sched_barrier(0); }
 
 // Keeps what is seldom done a branch, not a selection that every pass makes.
-__device__ __forceinline__ void in_branch() { asm volatile(""); }
+__device__ __forceinline__ void in_branch(uint32_t& v) { asm volatile("" : "+v"(v)); }
 
 // A lane's number as a value of its own: LDS addresses formed from it, one
 // instruction each, are neither formed before the loop nor shared with other code,
@@ -141,7 +142,6 @@ struct Mat<uint16_t> {
   __device__ __forceinline__ static void set(Frag& f, int e, float v) { f[e] = (__bf16)v; }
   // sum + 0 f: NaN if an element is not finite
   __device__ __forceinline__ static float times_zero(const Frag& f, float sum) {
-    typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
     const bf16x2 nil = {(__bf16)0.0f, (__bf16)0.0f};
 #pragma unroll
     for (int e = 0; e < E; e += 2) sum = __builtin_amdgcn_fdot2_f32_bf16(bf16x2{f[e], f[e + 1]}, nil, sum, false);
@@ -201,15 +201,19 @@ template <int N>
 __device__ __forceinline__ Parts<uint16_t, N> parts_of(const float (&x)[8]) {
   Parts<uint16_t, N> p;
 #pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    float v = x[e];
+  for (int e = 0; e < 8; e += 2) {
+    float v0 = x[e], v1 = x[e + 1];
 #pragma unroll
-    for (int k = 0; k < N - 1; ++k) {
-      const float hi = cut16(v);
-      p.f[k][e] = (__bf16)hi;
-      v -= hi;
+    for (int k = 0; k < N; ++k) {
+      bf16x2 hi = {(__bf16)v0, (__bf16)v1};
+      if (k + 1 < N) {  // the upper halves of both, one instruction
+        hi = __builtin_bit_cast(bf16x2, __builtin_amdgcn_perm(__float_as_uint(v1), __float_as_uint(v0), 0x07060302u));
+        v0 -= cut16(v0);
+        v1 -= cut16(v1);
+      }
+      p.f[k][e] = hi.x;
+      p.f[k][e + 1] = hi.y;
     }
-    p.f[N - 1][e] = (__bf16)v;
   }
   return p;
 }
@@ -584,14 +588,14 @@ __global__ __launch_bounds__(kThreads, KD <= 128 ? 2 : 1) void attn_sweep_kernel
           acc[ct][it] = f32x4{0, 0, 0, 0};
           if constexpr (kDecay) acc_r[ct][it] = f32x4{0, 0, 0, 0};
         }
-      // (Q S)^T: a lane holds 4 value columns of a step
+      // (Q S)^T: a lane holds 4 value columns of a step.  The next operands are on their way
+      // while these are multiplied.
+      constexpr int KK = KD / CK;
+      Frag fq[2][IT];
+      Parts<T, NS> ps[2][CT], pr[2][kDecay ? CT : 1];
+      const auto operands = [&](int kk) {
 #pragma unroll
-      for (int kk = 0; kk < KD / CK; ++kk) {
-        in_order();
-        Parts<T, NS> ps[CT], pr[kDecay ? CT : 1];
-        Frag fq[IT];
-#pragma unroll
-        for (int it = 0; it < IT; ++it) fq[it] = M::template row<KD>(s_q, 16 * it, kk * CK, lane);
+        for (int it = 0; it < IT; ++it) fq[kk & 1][it] = M::template row<KD>(s_q, 16 * it, kk * CK, lane);
 #pragma unroll
         for (int ct = 0; ct < CT; ++ct) {
           float sv[E], rv[E];
@@ -600,17 +604,23 @@ __global__ __launch_bounds__(kThreads, KD <= 128 ? 2 : 1) void attn_sweep_kernel
             sv[e] = S[ct][kk * (CK / 16) + e / 4][e % 4];
             if constexpr (kDecay) rv[e] = R[ct][kk * (CK / 16) + e / 4][e % 4];
           }
-          ps[ct] = parts_of<NS>(sv);
-          if constexpr (kDecay) pr[ct] = parts_of<NS>(rv);
+          ps[kk & 1][ct] = parts_of<NS>(sv);
+          if constexpr (kDecay) pr[kk & 1][ct] = parts_of<NS>(rv);
         }
+      };
+      operands(0);
+#pragma unroll
+      for (int kk = 0; kk < KK; ++kk) {
+        in_order();
+        if (kk + 1 < KK) operands(kk + 1);
 #pragma unroll
         for (int k = 0; k < NS; ++k)
 #pragma unroll
           for (int it = 0; it < IT; ++it)
 #pragma unroll
             for (int ct = 0; ct < CT; ++ct) {
-              acc[ct][it] = M::mma(ps[ct].f[k], fq[it], acc[ct][it]);
-              if constexpr (kDecay) acc_r[ct][it] = M::mma(pr[ct].f[k], fq[it], acc_r[ct][it]);
+              acc[ct][it] = M::mma(ps[kk & 1][ct].f[k], fq[kk & 1][it], acc[ct][it]);
+              if constexpr (kDecay) acc_r[ct][it] = M::mma(pr[kk & 1][ct].f[k], fq[kk & 1][it], acc_r[ct][it]);
             }
       }
     }
@@ -703,14 +713,14 @@ __global__ __launch_bounds__(kThreads, KD <= 128 ? 2 : 1) void attn_sweep_kernel
           }
         }
         if (careful) {
-          in_branch();
+          in_branch(nan_out);
 #pragma unroll
           for (int ct = 0; ct < CT; ++ct)
 #pragma unroll
             for (int it = 0; it < IT; ++it)
 #pragma unroll
               for (int r = 0; r < 4; ++r)
-                if (nan_out >> (16 * ct + 4 * it + r) & 1) acc[ct][it][r] = __builtin_nanf("");
+                acc[ct][it][r] += __uint_as_float(nan_out >> (16 * ct + 4 * it + r) & 1 ? 0x7fc00000u : 0u);
         }
         if constexpr (kDecay) {
           float sum = 0.0f;
@@ -790,20 +800,33 @@ __global__ __launch_bounds__(kThreads, KD <= 128 ? 2 : 1) void attn_sweep_kernel
             S[ct][t][r] *= pass;
             if (PACKED && total != 0) S[ct][t][r] = 0.0f;
           }
+      constexpr int TT = 4;  // tiles at a time: products that do not wait for one another
+      constexpr int kGroups = KT / TT;
+      Parts<T, NU> px[CT], px2[kDecay ? CT : 1];
+      Frag kf[2][TT];
+      const auto keys = [&](int i) {  // group i: steps CK (i / kGroups), tiles TT (i % kGroups)
+        const int s = i / kGroups, t = i % kGroups * TT;
+        f32x4 w[E / 4];
+        if constexpr (PACKED) {
 #pragma unroll
-      for (int s = 0; s < C / CK; ++s) {
-        Parts<T, NU> px[CT], px2[kDecay ? CT : 1];
-        float w[E], w2[E];
+          for (int e = 0; e < E; e += 4) w[e / 4] = *reinterpret_cast<const f32x4*>(s_leave + CK * s + step_of(e, q4));
+        }
+#pragma unroll
+        for (int j = 0; j < TT; ++j) {
+          kf[i & 1][j] = M::template col<KD>(s_k, CK * s, 16 * (t + j), lane);
+          if constexpr (PACKED) {  // not even a NaN of the steps before the last start
+#pragma unroll
+            for (int e = 0; e < E; ++e)
+              if (w[e / 4][e % 4] == 0.0f) M::zero(kf[i & 1][j], e);
+          }
+        }
+      };
+      const auto values = [&](int s) {
+        f32x4 w[E / 4], w2[E / 4];
 #pragma unroll
         for (int e = 0; e < E; e += 4) {
-          const f32x4 f = *reinterpret_cast<const f32x4*>(s_leave + CK * s + step_of(e, q4));
-#pragma unroll
-          for (int r = 0; r < 4; ++r) w[e + r] = f[r];
-          if constexpr (kDecay) {
-            const f32x4 f2 = *reinterpret_cast<const f32x4*>(s_left + CK * s + step_of(e, q4));
-#pragma unroll
-            for (int r = 0; r < 4; ++r) w2[e + r] = f2[r];
-          }
+          w[e / 4] = *reinterpret_cast<const f32x4*>(s_leave + CK * s + step_of(e, q4));
+          if constexpr (kDecay) w2[e / 4] = *reinterpret_cast<const f32x4*>(s_left + CK * s + step_of(e, q4));
         }
 #pragma unroll
         for (int ct = 0; ct < CT; ++ct) {
@@ -811,39 +834,32 @@ __global__ __launch_bounds__(kThreads, KD <= 128 ? 2 : 1) void attn_sweep_kernel
 #pragma unroll
           for (int e = 0; e < E; ++e) {
             const float v = M::at(vf[ct][s], e);
-            x[e] = v * w[e];
-            if constexpr (kDecay) x2[e] = v * w2[e];
+            x[e] = v * w[e / 4][e % 4];
+            if constexpr (kDecay) x2[e] = v * w2[e / 4][e % 4];
           }
           px[ct] = parts_of<NU>(x);
           if constexpr (kDecay) px2[ct] = parts_of<NU>(x2);
         }
-        constexpr int TT = 4;  // tiles at a time: products that do not wait for one another
+      };
+      keys(0);
 #pragma unroll
-        for (int t = 0; t < KT; t += TT) {
-          in_order();
-          Frag kf[TT];
+      for (int i = 0; i < kGroups * (C / CK); ++i) {
+        const int t = i % kGroups * TT;
+        if (t == 0) values(i / kGroups);
+        in_order();
+        if (i + 1 < kGroups * (C / CK)) keys(i + 1);
 #pragma unroll
-          for (int i = 0; i < TT; ++i) {
-            kf[i] = M::template col<KD>(s_k, CK * s, 16 * (t + i), lane);
-            if constexpr (PACKED) {  // not even a NaN of the steps before the last start
+        for (int k = 0; k < NU; ++k)
 #pragma unroll
-              for (int e = 0; e < E; ++e)
-                if (w[e] == 0.0f) M::zero(kf[i], e);
+          for (int j = 0; j < TT; ++j)
+#pragma unroll
+            for (int ct = 0; ct < CT; ++ct) {
+              S[ct][t + j] = M::mma(kf[i & 1][j], px[ct].f[k], S[ct][t + j]);
+              if constexpr (kDecay) R[ct][t + j] = M::mma(kf[i & 1][j], px2[ct].f[k], R[ct][t + j]);
             }
-          }
-#pragma unroll
-          for (int k = 0; k < NU; ++k)
-#pragma unroll
-            for (int i = 0; i < TT; ++i)
-#pragma unroll
-              for (int ct = 0; ct < CT; ++ct) {
-                S[ct][t + i] = M::mma(kf[i], px[ct].f[k], S[ct][t + i]);
-                if constexpr (kDecay) R[ct][t + i] = M::mma(kf[i], px2[ct].f[k], R[ct][t + i]);
-              }
-        }
       }
       if (careful) {
-        in_branch();
+        in_branch(nan_state);
 #pragma unroll
         for (int ct = 0; ct < CT; ++ct)
           if (nan_state >> ct & 1) {
