@@ -39,9 +39,6 @@ typedef __attribute__((address_space(3))) char lds_char;
 // take registers that the state needs.
 __device__ __forceinline__ void in_order() { __builtin_amdgcn_sched_barrier(0); }
 
-// Keeps what is seldom done a branch, not a selection that every pass makes.
-__device__ __forceinline__ void in_branch(uint32_t& v) { asm volatile("" : "+v"(v)); }
-
 // A lane's number as a value of its own: LDS addresses formed from it, one
 // instruction each, are neither formed before the loop nor shared with other code,
 // and held in registers meanwhile.
@@ -115,25 +112,39 @@ struct Mat<uint16_t> {
   __device__ __forceinline__ static f32x4 mma(const Frag& a, const Frag& b, f32x4 c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
   }
-  // contracted along the tile's rows
+  // Contracted along the tile's rows: row r0 + m, columns from c0 on (r0 a multiple of 16,
+  // c0 of CK).  A lane's place in a row of pieces is kept, and moved by c0's bits, which
+  // its own do not touch.
   template <int W>
-  __device__ __forceinline__ static Frag row(const uint16_t* tile, int r0, int c0, int lane) {
-    const int r = r0 + (lane & 15), c = c0 + 4 * (lane >> 4);
-    const uint2 a = *reinterpret_cast<const uint2*>(tile + Tile<uint16_t, W>::at(r, c));
-    const uint2 b = *reinterpret_cast<const uint2*>(tile + Tile<uint16_t, W>::at(r, c + 16));
+  __device__ __forceinline__ static int row_base(int lane) {
+    return Tile<uint16_t, W>::at(lane & 15, 4 * (lane >> 4));
+  }
+  template <int W>
+  __device__ __forceinline__ static Frag row(const uint16_t* tile, int base, int r0, int c0) {
+    const uint2 a = *reinterpret_cast<const uint2*>(tile + (base ^ c0) + r0 * W);
+    const uint2 b = *reinterpret_cast<const uint2*>(tile + (base ^ (c0 + 16)) + r0 * W);
     return __builtin_bit_cast(Frag, make_uint4(a.x, a.y, b.x, b.y));
   }
   // the same where both operands come from here: 8 q + e of 32, one access
   template <int W>
-  __device__ __forceinline__ static Frag run(const uint16_t* tile, int r0, int c0, int lane) {
-    return *reinterpret_cast<const Frag*>(tile + Tile<uint16_t, W>::at(r0 + (lane & 15), c0 + 8 * (lane >> 4)));
+  __device__ __forceinline__ static int run_base(int lane) {
+    return Tile<uint16_t, W>::at(lane & 15, 8 * (lane >> 4));
   }
-  // contracted along its columns: the transposing read gives 4 rows of a column to a lane
   template <int W>
-  __device__ __forceinline__ static Frag col(const uint16_t* tile, int r0, int c0, int lane) {
-    const int r = r0 + 4 * (lane >> 4) + ((lane & 15) >> 2), c = c0 + 4 * (lane & 3);
-    const s16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(tile + Tile<uint16_t, W>::at(r, c)));
-    const s16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(tile + Tile<uint16_t, W>::at(r + 16, c)));
+  __device__ __forceinline__ static Frag run(const uint16_t* tile, int base, int r0, int c0) {
+    return *reinterpret_cast<const Frag*>(tile + (base ^ c0) + r0 * W);
+  }
+  // Contracted along its columns, from column c0 (a multiple of 16) on: the transposing read
+  // gives 4 rows of a column to a lane.
+  template <int W>
+  __device__ __forceinline__ static int col_base(int lane) {
+    return Tile<uint16_t, W>::at(4 * (lane >> 4) + ((lane & 15) >> 2), 4 * (lane & 3));
+  }
+  template <int W>
+  __device__ __forceinline__ static Frag col(const uint16_t* tile, int base, int r0, int c0) {
+    const uint16_t* p = tile + (base ^ c0) + r0 * W;
+    const s16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)p);
+    const s16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(p + 16 * W));
     const s16x4 ab[2] = {a, b};
     return __builtin_bit_cast(Frag, ab);
   }
@@ -161,18 +172,33 @@ struct Mat<float> {
     return c;
   }
   template <int W>
-  __device__ __forceinline__ static Frag row(const float* tile, int r0, int c0, int lane) {
-    return *reinterpret_cast<const Frag*>(tile + Tile<float, W>::at(r0 + (lane & 15), c0 + 4 * (lane >> 4)));
+  __device__ __forceinline__ static int row_base(int lane) {
+    return Tile<float, W>::at(lane & 15, 4 * (lane >> 4));
   }
   template <int W>
-  __device__ __forceinline__ static Frag run(const float* tile, int r0, int c0, int lane) {
-    return row<W>(tile, r0, c0, lane);
+  __device__ __forceinline__ static Frag row(const float* tile, int base, int r0, int c0) {
+    return *reinterpret_cast<const Frag*>(tile + (base ^ c0) + r0 * W);
   }
   template <int W>
-  __device__ __forceinline__ static Frag col(const float* tile, int r0, int c0, int lane) {
-    const int r = r0 + 4 * (lane >> 4), c = c0 + (lane & 15);
-    return Frag{tile[Tile<float, W>::at(r, c)], tile[Tile<float, W>::at(r + 1, c)], tile[Tile<float, W>::at(r + 2, c)],
-                tile[Tile<float, W>::at(r + 3, c)]};
+  __device__ __forceinline__ static int run_base(int lane) {
+    return row_base<W>(lane);
+  }
+  template <int W>
+  __device__ __forceinline__ static Frag run(const float* tile, int base, int r0, int c0) {
+    return row<W>(tile, base, r0, c0);
+  }
+  // (rows r0 + 4 q and the three after it: the order of their pieces differs in two bits)
+  template <int W>
+  __device__ __forceinline__ static int col_base(int lane) {
+    return Tile<float, W>::at(4 * (lane >> 4), lane & 15);
+  }
+  template <int W>
+  __device__ __forceinline__ static Frag col(const float* tile, int base, int r0, int c0) {
+    const float* p = tile + r0 * W;
+    Frag f;
+#pragma unroll
+    for (int r = 0; r < 4; ++r) f[r] = p[(base ^ c0 ^ (Tile<float, W>::order(r) * 4)) + r * W];
+    return f;
   }
   __device__ __forceinline__ static float at(const Frag& f, int e) { return f[e]; }
   __device__ __forceinline__ static void zero(Frag& f, int e) { f[e] = 0.0f; }
@@ -471,6 +497,10 @@ __global__ __launch_bounds__(kThreads, KD <= 128 ? 2 : 1) void attn_sweep_kernel
   int turn = 0;
   bool stored = false;
 
+  // a lane's places in the tiles
+  const int run_at = M::template run_base<KD>(lane), row_at = M::template row_base<KD>(lane),
+            key_at = M::template col_base<KD>(lane), value_at = M::template col_base<NV>(lane) ^ c0,
+            p_at = M::template row_base<C>(lane);
   // this wave's tiles of P: e^{g (i-j)} of the lane's steps, 0 above the diagonal
   float wp[kOut ? kMyTiles : 1][4];
   if constexpr (kOut) {
@@ -539,7 +569,7 @@ __global__ __launch_bounds__(kThreads, KD <= 128 ? 2 : 1) void attn_sweep_kernel
         f32x4 acc = {0, 0, 0, 0};
 #pragma unroll
         for (int kk = 0; kk < KD; kk += CK)
-          acc = M::mma(M::template run<KD>(s_k, 16 * jt, kk, lane), M::template run<KD>(s_q, 16 * it, kk, lane), acc);
+          acc = M::mma(M::template run<KD>(s_k, run_at, 16 * jt, kk), M::template run<KD>(s_q, run_at, 16 * it, kk), acc);
         const int i = 16 * it + m;
         float p[4];
 #pragma unroll
@@ -574,20 +604,14 @@ __global__ __launch_bounds__(kThreads, KD <= 128 ? 2 : 1) void attn_sweep_kernel
     for (int ct = 0; ct < CT; ++ct)
 #pragma unroll
       for (int s = 0; s < C / CK; ++s) {
-        vf[ct][s] = M::template col<NV>(s_v, CK * s, c0 + 16 * ct, lane);
+        vf[ct][s] = M::template col<NV>(s_v, value_at, CK * s, 16 * ct);
         odd = M::times_zero(vf[ct][s], odd);
       }
     const bool careful = __any(!(odd == 0.0f));
     f32x4 acc[kOut ? CT : 1][kOut ? IT : 1], acc_r[kDecay ? CT : 1][kDecay ? IT : 1];
     if constexpr (kOut) {
       const int lane = own(threadIdx.x & 63);
-#pragma unroll
-      for (int ct = 0; ct < CT; ++ct)
-#pragma unroll
-        for (int it = 0; it < IT; ++it) {
-          acc[ct][it] = f32x4{0, 0, 0, 0};
-          if constexpr (kDecay) acc_r[ct][it] = f32x4{0, 0, 0, 0};
-        }
+      const f32x4 nil = {0, 0, 0, 0};
       // (Q S)^T: a lane holds 4 value columns of a step.  The next operands are on their way
       // while these are multiplied.
       constexpr int KK = KD / CK;
@@ -595,7 +619,7 @@ __global__ __launch_bounds__(kThreads, KD <= 128 ? 2 : 1) void attn_sweep_kernel
       Parts<T, NS> ps[2][CT], pr[2][kDecay ? CT : 1];
       const auto operands = [&](int kk) {
 #pragma unroll
-        for (int it = 0; it < IT; ++it) fq[kk & 1][it] = M::template row<KD>(s_q, 16 * it, kk * CK, lane);
+        for (int it = 0; it < IT; ++it) fq[kk & 1][it] = M::template row<KD>(s_q, row_at, 16 * it, kk * CK);
 #pragma unroll
         for (int ct = 0; ct < CT; ++ct) {
           float sv[E], rv[E];
@@ -619,67 +643,15 @@ __global__ __launch_bounds__(kThreads, KD <= 128 ? 2 : 1) void attn_sweep_kernel
           for (int it = 0; it < IT; ++it)
 #pragma unroll
             for (int ct = 0; ct < CT; ++ct) {
-              acc[ct][it] = M::mma(ps[kk & 1][ct].f[k], fq[kk & 1][it], acc[ct][it]);
-              if constexpr (kDecay) acc_r[ct][it] = M::mma(pr[kk & 1][ct].f[k], fq[kk & 1][it], acc_r[ct][it]);
+              acc[ct][it] = M::mma(ps[kk & 1][ct].f[k], fq[kk & 1][it], kk == 0 && k == 0 ? nil : acc[ct][it]);
+              if constexpr (kDecay)
+                acc_r[ct][it] = M::mma(pr[kk & 1][ct].f[k], fq[kk & 1][it], kk == 0 && k == 0 ? nil : acc_r[ct][it]);
             }
       }
     }
     __syncthreads();  // P and the weights are there, Q has been read, V is in registers
     stage_q(u0 + C);
     stage_v(u0 + C);
-    // Values that are not finite are left out of the products, where the zeros of P above
-    // its diagonal (and of the rows that pad K) would spread them.  Products of ones in their
-    // places with ones where P has its steps count what each output takes of them: those
-    // are NaN, and the columns of S that one reaches.
-    uint32_t nan_out = 0, nan_state = 0;  // bits 16 ct + 4 it + r, and ct
-    if (careful) {
-      const int m = lane & 15, q4 = 4 * (lane >> 4);
-      if constexpr (kOut) {
-#pragma unroll 1
-        for (int it = 0; it < IT; ++it) {
-          const int i = 16 * it + m;
-          f32x4 bad[CT];
-#pragma unroll
-          for (int ct = 0; ct < CT; ++ct) bad[ct] = f32x4{0, 0, 0, 0};
-#pragma unroll
-          for (int s = 0; s < C / CK; ++s) {
-            Frag taken, one;
-#pragma unroll
-            for (int e = 0; e < E; ++e) {
-              const int j = CK * s + step_of(e, q4);
-              M::set(taken, e, j <= i && (!PACKED || seen(i) == seen(j)) ? 1.0f : 0.0f);
-            }
-#pragma unroll
-            for (int ct = 0; ct < CT; ++ct) {
-#pragma unroll
-              for (int e = 0; e < E; ++e) M::set(one, e, finite_f32(M::at(vf[ct][s], e)) ? 0.0f : 1.0f);
-              bad[ct] = M::mma(one, taken, bad[ct]);
-            }
-          }
-#pragma unroll
-          for (int ct = 0; ct < CT; ++ct)
-#pragma unroll
-            for (int r = 0; r < 4; ++r)
-              if (bad[ct][r] != 0.0f) nan_out |= 1u << (16 * ct + 4 * it + r);
-        }
-      }
-#pragma unroll
-      for (int ct = 0; ct < CT; ++ct) {
-        int any = 0;
-#pragma unroll
-        for (int s = 0; s < C / CK; ++s)
-#pragma unroll
-          for (int e = 0; e < E; ++e)
-            if (!finite_f32(M::at(vf[ct][s], e))) {
-              if (!PACKED || seen(CK * s + step_of(e, q4)) == total) any = 1;
-              M::zero(vf[ct][s], e);
-            }
-        any |= __shfl_xor(any, 16);
-        any |= __shfl_xor(any, 32);
-        nan_state |= (uint32_t)any << ct;
-      }
-    }
-
     {
       if constexpr (kOut) {
         const int lane = own(threadIdx.x & 63), m = lane & 15, q4 = 4 * (lane >> 4);
@@ -697,30 +669,57 @@ __global__ __launch_bounds__(kThreads, KD <= 128 ? 2 : 1) void attn_sweep_kernel
             }
         }
         in_order();
+        // P V, of the values `of` gives
+        const auto product = [&](auto of) {
 #pragma unroll
-        for (int s = 0; s < C / CK; ++s) {
+          for (int s = 0; s < C / CK; ++s)
 #pragma unroll
-          for (int it = 0; it < IT; ++it) {
-            if (CK * s >= 16 * (it + 1)) continue;
-            const Frag fp = M::template row<C>(s_p, 16 * it, CK * s, lane);
+            for (int it = 0; it < IT; ++it) {
+              if (CK * s >= 16 * (it + 1)) continue;
+              const Frag fp = M::template row<C>(s_p, p_at, 16 * it, CK * s);
 #pragma unroll
-            for (int ct = 0; ct < CT; ++ct) acc[ct][it] = M::mma(vf[ct][s], fp, acc[ct][it]);
-            if constexpr (kLow) {
-              const Frag fl = M::template row<C>(s_p2, 16 * it, CK * s, lane);
+              for (int ct = 0; ct < CT; ++ct) acc[ct][it] = M::mma(of(vf[ct][s]), fp, acc[ct][it]);
+              if constexpr (kLow) {
+                const Frag fl = M::template row<C>(s_p2, p_at, 16 * it, CK * s);
 #pragma unroll
-              for (int ct = 0; ct < CT; ++ct) acc[ct][it] = M::mma(vf[ct][s], fl, acc[ct][it]);
+                for (int ct = 0; ct < CT; ++ct) acc[ct][it] = M::mma(of(vf[ct][s]), fl, acc[ct][it]);
+              }
             }
-          }
-        }
-        if (careful) {
-          in_branch(nan_out);
+        };
+        if (!careful) {
+          product([](const Frag& f) { return f; });
+        } else {
+          // Values that are not finite are left out: the zeros of P above its diagonal would
+          // spread them.  Products of ones in their places with ones where P has its steps
+          // count what each output takes of them: those are NaN.
+          product([](Frag f) {
 #pragma unroll
-          for (int ct = 0; ct < CT; ++ct)
+            for (int e = 0; e < E; ++e)
+              if (!finite_f32(M::at(f, e))) M::zero(f, e);
+            return f;
+          });
 #pragma unroll
-            for (int it = 0; it < IT; ++it)
+          for (int it = 0; it < IT; ++it)
 #pragma unroll
-              for (int r = 0; r < 4; ++r)
-                acc[ct][it][r] += __uint_as_float(nan_out >> (16 * ct + 4 * it + r) & 1 ? 0x7fc00000u : 0u);
+            for (int s = 0; s < C / CK; ++s) {
+              if (CK * s >= 16 * (it + 1)) continue;
+              in_order();
+              const int i = 16 * it + m;
+              Frag taken, one;
+#pragma unroll
+              for (int e = 0; e < E; ++e) {
+                const int j = CK * s + step_of(e, q4);
+                M::set(taken, e, j <= i && (!PACKED || seen(i) == seen(j)) ? 1.0f : 0.0f);
+              }
+#pragma unroll
+              for (int ct = 0; ct < CT; ++ct) {
+#pragma unroll
+                for (int e = 0; e < E; ++e) M::set(one, e, finite_f32(M::at(vf[ct][s], e)) ? 0.0f : 1.0f);
+                const f32x4 bad = M::mma(one, taken, f32x4{0, 0, 0, 0});
+#pragma unroll
+                for (int r = 0; r < 4; ++r) acc[ct][it][r] = bad[r] != 0.0f ? __builtin_nanf("") : acc[ct][it][r];
+              }
+            }
         }
         if constexpr (kDecay) {
           float sum = 0.0f;
@@ -813,8 +812,8 @@ __global__ __launch_bounds__(kThreads, KD <= 128 ? 2 : 1) void attn_sweep_kernel
         }
 #pragma unroll
         for (int j = 0; j < TT; ++j) {
-          kf[i & 1][j] = M::template col<KD>(s_k, CK * s, 16 * (t + j), lane);
-          if constexpr (PACKED) {  // not even a NaN of the steps before the last start
+          kf[i & 1][j] = M::template col<KD>(s_k, key_at, CK * s, 16 * (t + j));
+          if constexpr (PACKED) {
 #pragma unroll
             for (int e = 0; e < E; ++e)
               if (w[e / 4][e % 4] == 0.0f) M::zero(kf[i & 1][j], e);
@@ -836,6 +835,10 @@ __global__ __launch_bounds__(kThreads, KD <= 128 ? 2 : 1) void attn_sweep_kernel
             const float v = M::at(vf[ct][s], e);
             x[e] = v * w[e / 4][e % 4];
             if constexpr (kDecay) x2[e] = v * w2[e / 4][e % 4];
+            if (PACKED && w[e / 4][e % 4] == 0.0f) {  // not even a NaN of the steps before the last start
+              x[e] = 0.0f;
+              if constexpr (kDecay) x2[e] = 0.0f;
+            }
           }
           px[ct] = parts_of<NU>(x);
           if constexpr (kDecay) px2[ct] = parts_of<NU>(x2);
@@ -857,19 +860,6 @@ __global__ __launch_bounds__(kThreads, KD <= 128 ? 2 : 1) void attn_sweep_kernel
               S[ct][t + j] = M::mma(kf[i & 1][j], px[ct].f[k], S[ct][t + j]);
               if constexpr (kDecay) R[ct][t + j] = M::mma(kf[i & 1][j], px2[ct].f[k], R[ct][t + j]);
             }
-      }
-      if (careful) {
-        in_branch(nan_state);
-#pragma unroll
-        for (int ct = 0; ct < CT; ++ct)
-          if (nan_state >> ct & 1) {
-#pragma unroll
-            for (int t = 0; t < KT; ++t) {
-              const float v = __builtin_nanf("");
-              S[ct][t] = f32x4{v, v, v, v};
-              if constexpr (kDecay) R[ct][t] = S[ct][t];
-            }
-          }
       }
     }
     if (MODE == kAttnSegments) cut |= B != 0;
