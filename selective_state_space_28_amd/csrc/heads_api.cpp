@@ -4,6 +4,7 @@
 #include <climits>
 #include <cmath>
 #include <cstdint>
+#include <initializer_list>
 
 #include "api_checks.hpp"
 #include "linear_attn.hpp"
@@ -73,43 +74,55 @@ Span attn_span(const AttnView& w, int batch, int64_t seqlen, int n, int width, s
   return span(w.p, (size_t)(w.sb * (batch - 1) + w.st * (seqlen - 1) + w.sh * (n - 1) + width) * es);
 }
 
-// Workspace of one sweep: the states entering the segments, and what they leave of them.
+// Workspace of one sweep: the states entering the segments, and what they leave of
+// them; of the decay's gradient also their derivatives, and the segments' steps.
 struct SweepBytes {
-  size_t state, through;
-  size_t all() const { return state + through; }
+  size_t state, through, rate, steps, part;
+  size_t all() const { return state + through + rate + steps + part; }
 };
 
-SweepBytes sweep_bytes(const AttnSizes& s, int vd) {
-  const AttnSplit sp = attn_split(s.batch, s.heads, s.seqlen, vd);
-  if (sp.nseg < 2) return SweepBytes{0, 0};
+SweepBytes sweep_bytes(const AttnSizes& s, int blocks, bool decay) {
+  SweepBytes w{};
+  const AttnSplit sp = attn_split(s.batch, s.heads, s.seqlen, blocks);
   const size_t segs = (size_t)s.batch * (size_t)s.heads * (size_t)sp.nseg;
-  return SweepBytes{round256(segs * (size_t)s.kd * (size_t)s.vd * 4), round256(segs * 4)};
+  if (sp.nseg > 1) {
+    w.state = round256(segs * (size_t)s.kd * (size_t)s.vd * 4);
+    w.through = round256(segs * 4);
+    if (decay) {
+      w.rate = w.state;
+      w.steps = w.through;
+    }
+  }
+  if (decay) w.part = round256(segs * (size_t)blocks * 8);
+  return w;
 }
 
 // Of the backward: the sweeps one after another in the same place, then the heads'
-// gradients (float32) where several share one, then the decay's parts.
+// gradients (float32) where several share one.
 struct BwdBytes {
-  size_t sweep, dq, dk, dv, decay;
-  size_t all() const { return sweep + dq + dk + dv + decay; }
+  size_t sweep, dq, dk, dv;
+  size_t all() const { return sweep + dq + dk + dv; }
 };
 
 BwdBytes bwd_bytes(const AttnSizes& s) {
-  const size_t a = sweep_bytes(s, s.kd).all(), b = sweep_bytes(s, s.vd).all();
   const size_t steps = (size_t)s.batch * (size_t)s.seqlen * (size_t)s.heads * 4;
   BwdBytes w{};
-  w.sweep = a > b ? a : b;
+  for (const size_t b : {sweep_bytes(s, attn_column_blocks(s.kd), false).all(), sweep_bytes(s, attn_column_blocks(s.vd), false).all(),
+                         sweep_bytes(s, attn_decay_blocks(s.vd), true).all()})
+    w.sweep = w.sweep > b ? w.sweep : b;
   if (s.hq != s.heads) w.dq = round256(steps * (size_t)s.kd);
   if (s.hk != s.heads) w.dk = round256(steps * (size_t)s.kd);
   if (s.hv != s.heads) w.dv = round256(steps * (size_t)s.vd);
-  w.decay = round256((size_t)s.batch * (size_t)s.heads * (size_t)attn_decay_blocks(s.vd) * 8);
   return w;
 }
 
 // A sweep with contraction width kd and value width vd over the workspace.
 AttnSweep attn_sweep(const AttnSizes& s, const float* g, const uint8_t* starts, const int32_t* lengths, int dtype, int kd,
-                     int vd, void* workspace) {
+                     int vd, void* workspace, bool decay = false) {
   AttnSweep a{};
-  const AttnSplit sp = attn_split(s.batch, s.heads, s.seqlen, vd);
+  const int blocks = decay ? attn_decay_blocks(vd) : attn_column_blocks(vd);
+  const AttnSplit sp = attn_split(s.batch, s.heads, s.seqlen, blocks);
+  const SweepBytes w = sweep_bytes(s, blocks, decay);
   a.kd = kd;
   a.vd = vd;
   a.batch = s.batch;
@@ -120,10 +133,12 @@ AttnSweep attn_sweep(const AttnSizes& s, const float* g, const uint8_t* starts, 
   a.lengths = lengths;
   a.nseg = sp.nseg;
   a.seglen = sp.seglen;
-  if (sp.nseg > 1) {
-    a.seg_state = static_cast<float*>(workspace);
-    a.seg_through = reinterpret_cast<float*>(static_cast<char*>(workspace) + sweep_bytes(s, vd).state);
-  }
+  char* p = static_cast<char*>(workspace);
+  a.seg_state = reinterpret_cast<float*>(p);
+  a.seg_through = reinterpret_cast<float*>(p + w.state);
+  a.seg_rate = reinterpret_cast<float*>(p + w.state + w.through);
+  a.seg_steps = reinterpret_cast<float*>(p + w.state + w.through + w.rate);
+  a.part = reinterpret_cast<double*>(p + w.state + w.through + w.rate + w.steps);
   a.dtype = dtype_of(dtype);
   return a;
 }
@@ -171,7 +186,7 @@ extern "C" {
 size_t ssm_linear_attn_fwd_workspace_bytes(int batch, int64_t seqlen, int heads, int key_dim, int value_dim, int dtype) {
   const AttnSizes s{batch, seqlen, heads, 1, 1, 1, key_dim, value_dim};
   if (!dtype_ok(dtype) || !attn_shape_ok(s) || batch == 0 || heads == 0 || seqlen == 0) return 0;
-  return sweep_bytes(s, value_dim).all();
+  return sweep_bytes(s, attn_column_blocks(value_dim), false).all();
 }
 
 int ssm_linear_attn_fwd(const void* q, const void* k, const void* v, const int64_t* strides, const float* log_decay,
@@ -196,7 +211,7 @@ int ssm_linear_attn_fwd(const void* q, const void* k, const void* v, const int64
       !aligned(lengths, 4) || !aligned(h0, 4) || !aligned(last_state, 4) || !aligned(workspace, 256))
     return SSM_ERR_ALIGN;
   if (none) return SSM_OK;
-  const size_t need = empty ? 0 : sweep_bytes(s, value_dim).all();
+  const size_t need = empty ? 0 : sweep_bytes(s, attn_column_blocks(value_dim), false).all();
   if (need > 0 && (workspace == nullptr || workspace_bytes < need)) return SSM_ERR_WORKSPACE;
   const size_t rows = (size_t)batch * (size_t)seqlen;
   const size_t state = (size_t)batch * (size_t)heads * (size_t)key_dim * (size_t)value_dim * 4;
@@ -333,15 +348,15 @@ int ssm_linear_attn_bwd(const void* q, const void* k, const void* v, const int64
   if (e == hipSuccess && a.out_f32) e = launch_attn_gather(part_v, dv, (int64_t)rows, heads, v_heads, value_dim, a.dtype, st);
 
   if (e == hipSuccess && dlog_decay != nullptr) {
+    a = attn_sweep(s, log_decay, starts, lengths, dtype, key_dim, value_dim, ws, true);
     a.q = vq;
     a.k = vk;
     a.v = vv;
     a.dy = vdy;
+    a.scale_p = scale;
     a.scale_in = scale;
     a.scale_upd = 1.0f;
     a.state_in = h0;
-    a.rev = 0;
-    a.part = reinterpret_cast<double*>(ws + w.sweep + w.dq + w.dk + w.dv);
     e = launch_attn_decay_grad(a, dlast_state, dlog_decay, st);
   }
   return status_of(e);

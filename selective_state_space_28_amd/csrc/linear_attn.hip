@@ -259,17 +259,16 @@ constexpr uint32_t kNowhere = 0x80000000u;  // an offset behind every extent
 struct Slice {
   const char* p;
   int64_t st;
-  bool vec;  // aligned to 16 bytes with its strides and width
+  int bytes;  // of a lane's copies: 16 or 4, as its alignment, strides and width are; 0: element by element
 };
 
 template <typename T>
 __device__ __forceinline__ Slice slice_of(const AttnView& w, int64_t b, int h, int64_t first, int64_t dir, int width) {
-  constexpr int VE = 16 / (int)sizeof(T);
+  const uint64_t bits = reinterpret_cast<uintptr_t>(w.p) | (uint64_t)((w.sb | w.st | w.sh | (int64_t)width) * (int)sizeof(T));
   // (a chunk's offsets are 32 bits wide)
-  const bool vec = reinterpret_cast<uintptr_t>(w.p) % 16 == 0 && ((w.sb | w.st | w.sh | (int64_t)width) % VE) == 0 &&
-                   w.st < (int64_t)1 << 22;
+  const int bytes = w.st >= (int64_t)1 << 22 ? 0 : bits % 16 == 0 ? 16 : bits % 4 == 0 ? 4 : 0;
   return Slice{static_cast<const char*>(w.p) + (b * w.sb + (h / w.share) * w.sh + first * w.st) * (int64_t)sizeof(T),
-               dir * w.st * (int64_t)sizeof(T), vec};
+               dir * w.st * (int64_t)sizeof(T), bytes};
 }
 
 // ROWS x W elements of a slice into LDS: zeros from column `width` and from row n on.
@@ -285,13 +284,20 @@ __device__ __forceinline__ void copy_to_lds(uint32_t to, uint32_t at, u32x4_t bu
                : "memory", "m0");
 }
 
+__device__ __forceinline__ void copy_word_to_lds(uint32_t to, uint32_t at, u32x4_t buf) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, 0 offen lds"
+               :
+               : "s"(__builtin_amdgcn_readfirstlane(to)), "v"(at), "s"(buf)
+               : "memory", "m0");
+}
+
 template <typename T, int ROWS, int W>
 __device__ __forceinline__ void stage(T* lds, const Slice& s, int u, int width, int n, int wave) {
   using At = Tile<T, W>;
   constexpr int kAccesses = ROWS * W * (int)sizeof(T) / 1024 / kWaves;  // of a wave
   static_assert(kAccesses >= 1, "an access for every wave");
   const int lane = own(threadIdx.x & 63);
-  if (s.vec) {
+  if (s.bytes != 0) {
     // the lowest address first: row n - 1 backward in time
     const bool rev = s.st < 0;
     const uint32_t st = (uint32_t)(rev ? -s.st : s.st);
@@ -306,7 +312,16 @@ __device__ __forceinline__ void stage(T* lds, const Slice& s, int u, int width, 
     // (but with 32 and 64 pieces to a row)
     constexpr int kStep = ROWS / kAccesses;
     const int r0 = (wave * 64 + lane) / At::kPieces;
-    if (n == ROWS) {
+    if (s.bytes == 4) {  // 64 words of LDS for an access
+      constexpr int kWord = 4 / (int)sizeof(T);  // elements
+#pragma unroll 4
+      for (int k = 0; k < 4 * kAccesses; ++k) {
+        const int piece = ((k * kWaves + wave) * 64 + lane) >> 2;
+        const int r = piece / At::kPieces, c = (piece % At::kPieces ^ At::order(r)) * At::kPiece + (lane & 3) * kWord;
+        const uint32_t at = (uint32_t)(rev ? n - 1 - r : r) * st + (uint32_t)(c * (int)sizeof(T));
+        copy_word_to_lds(to + (uint32_t)(k * kWaves + wave) * 256u, r < n && c < width ? at : kNowhere, buf);
+      }
+    } else if (n == ROWS) {
 #pragma unroll
       for (int k = 0; k < kAccesses; ++k) {
         const int c = (lane % At::kPieces ^ At::order(r0 + k * kStep)) * At::kPiece;
@@ -354,7 +369,7 @@ struct StateAt {
 __device__ __forceinline__ int tile_row(int tile) { return (0xffa94 >> (2 * tile)) & 3; }
 __device__ __forceinline__ int tile_col(int tile) { return (0xe4910 >> (2 * tile)) & 3; }
 
-enum AttnMode { kAttnOut = 0, kAttnSegments = 1, kAttnDecay = 2 };
+enum AttnMode { kAttnOut = 0, kAttnSegments = 1, kAttnDecay = 2, kAttnDecaySegments = 3 };
 
 // One workgroup: kWaves waves, CT tiles of 16 value columns each.  kAttnSegments: only
 // the state that a segment adds, and what it leaves of the one before.  kAttnDecay:
@@ -362,6 +377,7 @@ enum AttnMode { kAttnOut = 0, kAttnSegments = 1, kAttnDecay = 2 };
 // <R_L, dlast>; R_u = e^g (R_{u-1} + S_{u-1}) gives, of a chunk,
 //   diag(e^{g (i+1)}) Q (R + (i+1) S) + ((i-j) W o Q K^T) V
 //   R <- e^{g C} (R + C S) + (diag((C-1-j) e^{g (C-1-j)}) K)^T V
+// kAttnDecaySegments: what a segment adds to both.
 //
 // The next chunk's tiles are copied to LDS while this one is worked on: K, wanted to
 // the end, into a second buffer, V and Q into their own once every wave has done with
@@ -375,7 +391,9 @@ __global__ __launch_bounds__(kThreads, KD <= 128 ? 2 : 1) void attn_sweep_kernel
   constexpr int C = M::C, IT = C / 16, CK = M::CK, E = M::E;
   constexpr int NV = 16 * CT * kWaves;
   constexpr int KT = KD / 16;  // tiles of S above one another
-  constexpr bool kDecay = MODE == kAttnDecay, kOut = MODE != kAttnSegments;
+  constexpr bool kSegments = MODE == kAttnSegments || MODE == kAttnDecaySegments;
+  constexpr bool kDecay = MODE == kAttnDecay, kOut = !kSegments;
+  constexpr bool kRate = kDecay || MODE == kAttnDecaySegments;  // R beside S
   constexpr int NU = sizeof(T) == 2 ? 3 : 1;  // parts of the decayed v, exact
   constexpr int NS = sizeof(T) == 2 ? 2 : 1;  // parts of S as an operand, to 2^-16
   constexpr int kTiles = IT * (IT + 1) / 2;   // of P, on and below the diagonal
@@ -389,14 +407,14 @@ __global__ __launch_bounds__(kThreads, KD <= 128 ? 2 : 1) void attn_sweep_kernel
   __shared__ __attribute__((aligned(16))) T s_p2[kLow ? C * C : 1];
   __shared__ __attribute__((aligned(16))) T s_dy[kDecay ? C * NV : 1];
   __shared__ float s_pw[C + 1];
-  __shared__ __attribute__((aligned(16))) float s_enter[C], s_leave[C], s_left[kDecay ? C : 1];
+  __shared__ __attribute__((aligned(16))) float s_enter[C], s_leave[C], s_left[kRate ? C : 1];
   __shared__ double s_sum[kWaves];
 
   int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   int m = lane & 15, q4 = 4 * (lane >> 4);
   const int nvb = (a.vd + NV - 1) / NV;
-  const int nsegs = MODE == kAttnSegments ? a.nseg - 1 : MODE == kAttnDecay ? 1 : a.nseg;
+  const int nsegs = kSegments ? a.nseg - 1 : a.nseg;
   // consecutive workgroups go to the 8 dies in turn: a die takes consecutive numbers,
   // whose column blocks, and heads that share q, k or v, read the same lines
   int64_t id = group_index();
@@ -431,7 +449,7 @@ __global__ __launch_bounds__(kThreads, KD <= 128 ? 2 : 1) void attn_sweep_kernel
   }
 
   // S: rows 16 t + q4 + r, column v0 + c0 + 16 ct + m
-  f32x4 S[CT][KT], R[kDecay ? CT : 1][kDecay ? KT : 1];
+  f32x4 S[CT][KT], R[kRate ? CT : 1][kRate ? KT : 1];
   const int64_t mat = (int64_t)a.kd * a.vd;
   const float* from = nullptr;
   if (kOut && seg > 0) from = a.seg_state + (head * a.nseg + seg) * mat;
@@ -442,7 +460,7 @@ __global__ __launch_bounds__(kThreads, KD <= 128 ? 2 : 1) void attn_sweep_kernel
 #pragma unroll
     for (int t = 0; t < KT; ++t) {
       S[ct][t] = f32x4{0, 0, 0, 0};
-      if constexpr (kDecay) R[ct][t] = f32x4{0, 0, 0, 0};
+      if constexpr (kRate) R[ct][t] = f32x4{0, 0, 0, 0};
     }
   if (from != nullptr) {
     const Buf buf = make_buf(from, mat * 4);
@@ -456,6 +474,20 @@ __global__ __launch_bounds__(kThreads, KD <= 128 ? 2 : 1) void attn_sweep_kernel
           uint32_t w[1];
           buf_load_words<1>(buf, at.lane(16 * t + r, 16 * ct), at.fixed(16 * t + r, 16 * ct), w);
           S[ct][t][r] = __uint_as_float(w[0]);
+        }
+  }
+  if (kDecay && seg > 0) {
+    const Buf buf = make_buf(a.seg_rate + (head * a.nseg + seg) * mat, mat * 4);
+    const StateAt at(a, false, v0 + c0 + m, q4);
+#pragma unroll
+    for (int ct = 0; ct < CT; ++ct)
+#pragma unroll
+      for (int t = 0; t < KT; ++t)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          uint32_t w[1];
+          buf_load_words<1>(buf, at.lane(16 * t + r, 16 * ct), at.fixed(16 * t + r, 16 * ct), w);
+          if constexpr (kRate) R[ct][t][r] = __uint_as_float(w[0]);
         }
   }
   if constexpr (kOut) {  // the masked halves of pairs of tiles stay zero
@@ -472,7 +504,7 @@ __global__ __launch_bounds__(kThreads, KD <= 128 ? 2 : 1) void attn_sweep_kernel
                          (int64_t)a.heads * a.vd <= (int64_t)1 << 22;
 
   const int u_begin = (int)(seg * a.seglen);
-  const int u_end = MODE == kAttnDecay ? L : (int)min((int64_t)L, u_begin + a.seglen);
+  const int u_end = (int)min((int64_t)L, u_begin + a.seglen);
   T* out = static_cast<T*>(a.out);
   const auto valid = [&](int u) { return min(max(len - u, 0), C); };  // (u is at most seqlen + C, below 2^31)
 
@@ -553,7 +585,7 @@ __global__ __launch_bounds__(kThreads, KD <= 128 ? 2 : 1) void attn_sweep_kernel
       if constexpr (kOut) s_enter[i] = B == 0 || seen(i) == 0 ? s_pw[i + 1 - sh] * a.scale_in : 0.0f;
       const float w = left >= 0 && (B == 0 || seen(i) == total) ? s_pw[left + sh] * a.scale_upd : 0.0f;
       s_leave[i] = w;
-      if constexpr (kDecay) s_left[i] = w * (float)left;
+      if constexpr (kRate) s_left[i] = w * (float)left;
     }
 
     if constexpr (kOut) {
@@ -792,7 +824,7 @@ __global__ __launch_bounds__(kThreads, KD <= 128 ? 2 : 1) void attn_sweep_kernel
         for (int t = 0; t < KT; ++t)
 #pragma unroll
           for (int r = 0; r < 4; ++r) {
-            if constexpr (kDecay) {
+            if constexpr (kRate) {
               R[ct][t][r] = __builtin_fmaf(S[ct][t][r], (float)n, R[ct][t][r]) * pass;
               if (PACKED && total != 0) R[ct][t][r] = 0.0f;
             }
@@ -801,7 +833,7 @@ __global__ __launch_bounds__(kThreads, KD <= 128 ? 2 : 1) void attn_sweep_kernel
           }
       constexpr int TT = 4;  // tiles at a time: products that do not wait for one another
       constexpr int kGroups = KT / TT;
-      Parts<T, NU> px[CT], px2[kDecay ? CT : 1];
+      Parts<T, NU> px[CT], px2[kRate ? CT : 1];
       Frag kf[2][TT];
       const auto keys = [&](int i) {  // group i: steps CK (i / kGroups), tiles TT (i % kGroups)
         const int s = i / kGroups, t = i % kGroups * TT;
@@ -825,7 +857,7 @@ __global__ __launch_bounds__(kThreads, KD <= 128 ? 2 : 1) void attn_sweep_kernel
 #pragma unroll
         for (int e = 0; e < E; e += 4) {
           w[e / 4] = *reinterpret_cast<const f32x4*>(s_leave + CK * s + step_of(e, q4));
-          if constexpr (kDecay) w2[e / 4] = *reinterpret_cast<const f32x4*>(s_left + CK * s + step_of(e, q4));
+          if constexpr (kRate) w2[e / 4] = *reinterpret_cast<const f32x4*>(s_left + CK * s + step_of(e, q4));
         }
 #pragma unroll
         for (int ct = 0; ct < CT; ++ct) {
@@ -834,14 +866,14 @@ __global__ __launch_bounds__(kThreads, KD <= 128 ? 2 : 1) void attn_sweep_kernel
           for (int e = 0; e < E; ++e) {
             const float v = M::at(vf[ct][s], e);
             x[e] = v * w[e / 4][e % 4];
-            if constexpr (kDecay) x2[e] = v * w2[e / 4][e % 4];
+            if constexpr (kRate) x2[e] = v * w2[e / 4][e % 4];
             if (PACKED && w[e / 4][e % 4] == 0.0f) {  // not even a NaN of the steps before the last start
               x[e] = 0.0f;
-              if constexpr (kDecay) x2[e] = 0.0f;
+              if constexpr (kRate) x2[e] = 0.0f;
             }
           }
           px[ct] = parts_of<NU>(x);
-          if constexpr (kDecay) px2[ct] = parts_of<NU>(x2);
+          if constexpr (kRate) px2[ct] = parts_of<NU>(x2);
         }
       };
       keys(0);
@@ -858,22 +890,25 @@ __global__ __launch_bounds__(kThreads, KD <= 128 ? 2 : 1) void attn_sweep_kernel
 #pragma unroll
             for (int ct = 0; ct < CT; ++ct) {
               S[ct][t + j] = M::mma(kf[i & 1][j], px[ct].f[k], S[ct][t + j]);
-              if constexpr (kDecay) R[ct][t + j] = M::mma(kf[i & 1][j], px2[ct].f[k], R[ct][t + j]);
+              if constexpr (kRate) R[ct][t + j] = M::mma(kf[i & 1][j], px2[ct].f[k], R[ct][t + j]);
             }
       }
     }
-    if (MODE == kAttnSegments) cut |= B != 0;
+    if (kSegments) cut |= B != 0;
   }
 
   lane = own(lane);
   m = lane & 15;
   q4 = 4 * (lane >> 4);
-  if constexpr (MODE == kAttnSegments) {
+  if constexpr (kSegments) {
     const int steps = min(max(len - u_begin, 0), u_end - u_begin);
-    if (vb == 0 && threadIdx.x == 0) a.seg_through[head * a.nseg + seg] = cut ? 0.0f : decay_pow(g, (float)steps);
+    if (vb == 0 && threadIdx.x == 0) {
+      a.seg_through[head * a.nseg + seg] = cut ? 0.0f : decay_pow(g, (float)steps);
+      if constexpr (kRate) a.seg_steps[head * a.nseg + seg] = (float)steps;
+    }
   } else if constexpr (MODE == kAttnDecay) {
     float sum = 0.0f;
-    if (dlast != nullptr) {
+    if (dlast != nullptr && seg == a.nseg - 1) {
       const Buf buf = make_buf(dlast + head * mat, mat * 4);
       const StateAt at(a, false, v0 + c0 + m, q4);
 #pragma unroll
@@ -890,11 +925,12 @@ __global__ __launch_bounds__(kThreads, KD <= 128 ? 2 : 1) void attn_sweep_kernel
     dg = wave_sum(dg + (double)sum);
     if (lane == 0) s_sum[wave] = dg;
     __syncthreads();
-    if (threadIdx.x == 0) a.part[((int64_t)h * a.batch + b) * nvb + vb] = (s_sum[0] + s_sum[1]) + (s_sum[2] + s_sum[3]);
+    if (threadIdx.x == 0)
+      a.part[(((int64_t)h * a.batch + b) * nvb + vb) * a.nseg + seg] = (s_sum[0] + s_sum[1]) + (s_sum[2] + s_sum[3]);
     return;
   }
   float* to = nullptr;
-  if (MODE == kAttnSegments) to = a.seg_state + (head * a.nseg + seg + 1) * mat;
+  if (kSegments) to = a.seg_state + (head * a.nseg + seg + 1) * mat;
   else if (a.state_out != nullptr && seg == a.nseg - 1) to = a.state_out + head * mat;
   if (to == nullptr) return;
   // backward in time nothing passes a first step that starts a sequence
@@ -910,11 +946,24 @@ __global__ __launch_bounds__(kThreads, KD <= 128 ? 2 : 1) void attn_sweep_kernel
         const uint32_t w[1] = {gone ? 0u : __float_as_uint(S[ct][t][r])};
         buf_store_words<1>(buf, at.lane(16 * t + r, 16 * ct), at.fixed(16 * t + r, 16 * ct), w);
       }
+  if constexpr (MODE == kAttnDecaySegments) {
+    const Buf rate = make_buf(a.seg_rate + (head * a.nseg + seg + 1) * mat, mat * 4);
+#pragma unroll
+    for (int ct = 0; ct < CT; ++ct)
+#pragma unroll
+      for (int t = 0; t < KT; ++t)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const uint32_t w[1] = {__float_as_uint(R[ct][t][r])};
+          buf_store_words<1>(rate, at.lane(16 * t + r, 16 * ct), at.fixed(16 * t + r, 16 * ct), w);
+        }
+  }
 }
 
-// The states entering the segments from what each adds: S <- through S + added, a
-// thread an element.
-__global__ __launch_bounds__(256) void attn_carry_kernel(float* __restrict__ state, const float* __restrict__ through,
+// The states entering the segments from what each adds: S <- through S + added, and with
+// `rate`, R <- through (R + steps S) + added; a thread an element.
+__global__ __launch_bounds__(256) void attn_carry_kernel(float* __restrict__ state, float* __restrict__ rate,
+                                                         const float* __restrict__ through, const float* __restrict__ steps,
                                                          const float* __restrict__ state_in, int kd, int vd, int nseg,
                                                          int transposed, int64_t n) {
   const int64_t i = group_index() * 256 + threadIdx.x;
@@ -922,14 +971,31 @@ __global__ __launch_bounds__(256) void attn_carry_kernel(float* __restrict__ sta
   const int mat = kd * vd;
   const int64_t head = i / mat;
   const int e = (int)(i - head * mat), row = e / vd, col = e - row * vd;
-  float s = 0.0f;
+  float s = 0.0f, r = 0.0f;
   if (state_in != nullptr) s = state_in[head * mat + (transposed ? col * kd + row : e)];
-  float* p = state + head * nseg * mat + e;
+  const int64_t first = head * nseg * mat + e;
   const float* th = through + head * nseg;
-  for (int k = 0; k + 1 < nseg; ++k) {
-    const float added = p[(int64_t)(k + 1) * mat];
-    s = th[k] == 0.0f ? added : __builtin_fmaf(th[k], s, added);
-    p[(int64_t)(k + 1) * mat] = s;
+  constexpr int U = 8;  // segments on their way at once
+  for (int k0 = 0; k0 + 1 < nseg; k0 += U) {
+    float added[U], more[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const bool in = k0 + u + 1 < nseg;
+      added[u] = in ? state[first + (int64_t)(k0 + u + 1) * mat] : 0.0f;
+      more[u] = in && rate != nullptr ? rate[first + (int64_t)(k0 + u + 1) * mat] : 0.0f;
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int k = k0 + u;
+      if (k + 1 >= nseg) break;
+      const float t = th[k];
+      if (rate != nullptr) {
+        r = t == 0.0f ? more[u] : __builtin_fmaf(t, __builtin_fmaf(steps[head * nseg + k], s, r), more[u]);
+        rate[first + (int64_t)(k + 1) * mat] = r;
+      }
+      s = t == 0.0f ? added[u] : __builtin_fmaf(t, s, added[u]);
+      state[first + (int64_t)(k + 1) * mat] = s;
+    }
   }
 }
 
@@ -949,48 +1015,84 @@ __global__ __launch_bounds__(256) void attn_gather_kernel(const float* __restric
 }
 
 __global__ __launch_bounds__(64) void attn_decay_sum_kernel(const double* __restrict__ part, float* __restrict__ out,
-                                                            int per) {
+                                                            int64_t per) {
   const double* p = part + (int64_t)blockIdx.x * per;
   double s = 0.0;
-  for (int i = threadIdx.x; i < per; i += 64) s += p[i];
+  for (int64_t i = threadIdx.x; i < per; i += 64) s += p[i];
   s = wave_sum(s);
   if (threadIdx.x == 0) out[blockIdx.x] = (float)s;
 }
 
-// One token: S <- e^g S + k v^T, y = scale q S.  A workgroup takes a (batch row,
-// head) and 64 value columns, a lane one of them, a wave every fourth row.
-template <typename T>
+// One token: S <- e^g S + k v^T, y = scale q S, bound by the state, read and written
+// once.  A workgroup takes a (batch row, head) and kStepColumns value columns; V columns
+// lie side by side in a lane (4, where rows of S are aligned so, or 1), so a row takes
+// kStepColumns / V lanes, and a lane has kStepRows of its rows on their way at once.
+constexpr int kStepColumns = 64, kStepRows = 8;
+
+template <typename T, int V>
 __global__ __launch_bounds__(256) void attn_step_kernel(const AttnStep a) {
-  __shared__ float s_y[4][64];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int nvb = (a.vd + 63) / 64;
+  typedef float vecf __attribute__((ext_vector_type(V)));
+  constexpr int kLanes = kStepColumns / V, kRows = 256 / kLanes;  // rows of S side by side
+  __shared__ float s_k[kAttnMaxWidth], s_q[kAttnMaxWidth];
+  __shared__ float s_y[kRows][kStepColumns + 4];
+  const int lane = threadIdx.x % kLanes, row0 = threadIdx.x / kLanes;
+  const int nvb = (a.vd + kStepColumns - 1) / kStepColumns;
   int64_t id = group_index();
   if (id >= (int64_t)a.batch * a.heads * nvb) return;
   const int vb = (int)(id % nvb);
   id /= nvb;
   const int h = (int)(id % a.heads), b = (int)(id / a.heads);
-  const int col = vb * 64 + lane;
+  const int col = vb * kStepColumns + lane * V;
   const auto base = [&](const AttnView& w) { return static_cast<const T*>(w.p) + b * w.sb + (h / w.share) * w.sh; };
   const T *pq = base(a.q), *pk = base(a.k), *pv = base(a.v);
   const bool first = a.starts != nullptr && a.starts[b] != 0;
+  const int64_t at = ((int64_t)b * a.heads + h) * a.kd * a.vd + col;
+  const bool in = col < a.vd;
+  vecf s[kStepRows];
+  const auto load = [&](int r0) {
+#pragma unroll
+    for (int u = 0; u < kStepRows; ++u) {
+      const int row = r0 + u * kRows;
+      if (in && !first && row < a.kd) s[u] = *reinterpret_cast<const vecf*>(a.state + at + (int64_t)row * a.vd);
+      else s[u] = 0.0f;
+    }
+  };
+  load(row0);
+  if (threadIdx.x < a.kd) {
+    s_k[threadIdx.x] = Elem<T>::load(pk + threadIdx.x);
+    s_q[threadIdx.x] = Elem<T>::load(pq + threadIdx.x);
+  }
+  vecf v, y = 0.0f;
+#pragma unroll
+  for (int c = 0; c < V; ++c) v[c] = in ? Elem<T>::load(pv + col + c) : 0.0f;
   const float decay = decay_pow(a.g[h], 1.0f);
-  const int64_t at = ((int64_t)b * a.heads + h) * a.kd * a.vd;
-  float y = 0.0f;
-  if (col < a.vd) {
-    const float v = Elem<T>::load(pv + col);
-    for (int row = wave; row < a.kd; row += 4) {
-      const int64_t e = at + (int64_t)row * a.vd + col;
-      const float kv = Elem<T>::load(pk + row) * v;
-      const float s = first ? kv : __builtin_fmaf(decay, a.state[e], kv);
-      a.state_out[e] = s;
-      y = __builtin_fmaf(Elem<T>::load(pq + row), s, y);
+  __syncthreads();
+  for (int r0 = row0; r0 < a.kd; r0 += kRows * kStepRows) {
+    if (r0 != row0) load(r0);
+#pragma unroll
+    for (int u = 0; u < kStepRows; ++u) {
+      const int row = r0 + u * kRows;
+      if (!in || row >= a.kd) continue;
+      const float k = s_k[row], q = s_q[row];
+      vecf n;
+#pragma unroll
+      for (int c = 0; c < V; ++c) {
+        const float kv = k * v[c];
+        n[c] = first ? kv : __builtin_fmaf(decay, s[u][c], kv);
+        y[c] = __builtin_fmaf(q, n[c], y[c]);
+      }
+      *reinterpret_cast<vecf*>(a.state_out + at + (int64_t)row * a.vd) = n;
     }
   }
-  s_y[wave][lane] = y;
+#pragma unroll
+  for (int c = 0; c < V; ++c) s_y[row0][lane * V + c] = y[c];
   __syncthreads();
-  if (wave == 0 && col < a.vd) {
-    y = ((s_y[0][lane] + s_y[1][lane]) + (s_y[2][lane] + s_y[3][lane])) * a.scale;
-    Elem<T>::store(static_cast<T*>(a.y) + ((int64_t)b * a.heads + h) * a.vd + col, y);
+  const int c = vb * kStepColumns + (int)threadIdx.x;
+  if (threadIdx.x < kStepColumns && c < a.vd) {
+    float sum = 0.0f;
+#pragma unroll
+    for (int r = 0; r < kRows; ++r) sum += s_y[r][threadIdx.x];
+    Elem<T>::store(static_cast<T*>(a.y) + ((int64_t)b * a.heads + h) * a.vd + c, sum * a.scale);
   }
 }
 
@@ -1002,7 +1104,7 @@ int column_tiles(int vd) { return vd <= 64 ? 1 : 2; }
 template <typename T, int KD, int CT, int MODE>
 hipError_t sweep(const AttnSweep& a, const float* dlast, hipStream_t stream) {
   const int nvb = (a.vd + 64 * CT - 1) / (64 * CT);
-  const int nsegs = MODE == kAttnSegments ? a.nseg - 1 : MODE == kAttnDecay ? 1 : a.nseg;
+  const int nsegs = MODE == kAttnSegments || MODE == kAttnDecaySegments ? a.nseg - 1 : a.nseg;
   const int64_t groups = (int64_t)a.batch * a.heads * nvb * nsegs;
   const dim3 grid = grid_of((groups + 7) / 8 * 8, kThreads);
   if (a.starts != nullptr) attn_sweep_kernel<T, KD, CT, MODE, true><<<grid, kThreads, 0, stream>>>(a, dlast, groups);
@@ -1022,18 +1124,31 @@ hipError_t sweep_of(const AttnSweep& a, hipStream_t stream) {
   return column_tiles(a.vd) == 1 ? sweep_of<T, 1, MODE>(a, nullptr, stream) : sweep_of<T, 2, MODE>(a, nullptr, stream);
 }
 
+hipError_t carry(const AttnSweep& a, float* rate, hipStream_t stream) {
+  const int64_t n = (int64_t)a.batch * a.heads * a.kd * a.vd;
+  attn_carry_kernel<<<grid_of((n + 255) / 256, 256), 256, 0, stream>>>(a.seg_state, rate, a.seg_through, a.seg_steps,
+                                                                       a.state_in, a.kd, a.vd, a.nseg, a.transposed, n);
+  return hipGetLastError();
+}
+
 template <typename T>
 hipError_t run_sweep(const AttnSweep& a, hipStream_t stream) {
   if (a.nseg > 1) {
     hipError_t e = sweep_of<T, kAttnSegments>(a, stream);
-    if (e != hipSuccess) return e;
-    const int64_t n = (int64_t)a.batch * a.heads * a.kd * a.vd;
-    attn_carry_kernel<<<grid_of((n + 255) / 256, 256), 256, 0, stream>>>(a.seg_state, a.seg_through, a.state_in, a.kd,
-                                                                         a.vd, a.nseg, a.transposed, n);
-    e = hipGetLastError();
+    if (e == hipSuccess) e = carry(a, nullptr, stream);
     if (e != hipSuccess) return e;
   }
   return sweep_of<T, kAttnOut>(a, stream);
+}
+
+template <typename T>
+hipError_t run_decay(const AttnSweep& a, const float* dlast, hipStream_t stream) {
+  if (a.nseg > 1) {
+    hipError_t e = sweep_of<T, 1, kAttnDecaySegments>(a, dlast, stream);
+    if (e == hipSuccess) e = carry(a, a.seg_rate, stream);
+    if (e != hipSuccess) return e;
+  }
+  return sweep_of<T, 1, kAttnDecay>(a, dlast, stream);
 }
 
 }  // namespace
@@ -1042,9 +1157,9 @@ int attn_column_blocks(int vd) { return (vd + 64 * column_tiles(vd) - 1) / (64 *
 
 int attn_decay_blocks(int vd) { return (vd + 63) / 64; }
 
-AttnSplit attn_split(int batch, int heads, int64_t seqlen, int vd) {
+AttnSplit attn_split(int batch, int heads, int64_t seqlen, int blocks) {
   // two workgroups for each of the 256 CUs, segments of 4 chunks at least
-  const int64_t groups = (int64_t)batch * heads * attn_column_blocks(vd);
+  const int64_t groups = (int64_t)batch * heads * blocks;
   const int64_t chunks = (seqlen + kAttnChunk - 1) / kAttnChunk;
   int64_t want = groups >= 512 || groups == 0 ? 1 : 512 / groups;
   if (want > chunks / 4) want = chunks / 4;
@@ -1058,10 +1173,9 @@ hipError_t launch_attn_sweep(const AttnSweep& a, hipStream_t stream) {
 }
 
 hipError_t launch_attn_decay_grad(const AttnSweep& a, const float* dlast, float* dlog_decay, hipStream_t stream) {
-  const hipError_t e = a.dtype == Dtype::BF16 ? sweep_of<uint16_t, 1, kAttnDecay>(a, dlast, stream)
-                                              : sweep_of<float, 1, kAttnDecay>(a, dlast, stream);
+  const hipError_t e = a.dtype == Dtype::BF16 ? run_decay<uint16_t>(a, dlast, stream) : run_decay<float>(a, dlast, stream);
   if (e != hipSuccess) return e;
-  attn_decay_sum_kernel<<<a.heads, 64, 0, stream>>>(a.part, dlog_decay, a.batch * attn_decay_blocks(a.vd));
+  attn_decay_sum_kernel<<<a.heads, 64, 0, stream>>>(a.part, dlog_decay, (int64_t)a.batch * attn_decay_blocks(a.vd) * a.nseg);
   return hipGetLastError();
 }
 
@@ -1076,12 +1190,22 @@ hipError_t launch_attn_gather(const float* part, void* out, int64_t rows, int he
   return hipGetLastError();
 }
 
-hipError_t launch_attn_step(const AttnStep& a, hipStream_t stream) {
-  const int nvb = (a.vd + 63) / 64;
-  const dim3 grid = grid_of((int64_t)a.batch * a.heads * nvb, 256);
-  if (a.dtype == Dtype::BF16) attn_step_kernel<uint16_t><<<grid, 256, 0, stream>>>(a);
-  else attn_step_kernel<float><<<grid, 256, 0, stream>>>(a);
+namespace {
+
+template <typename T>
+hipError_t step(const AttnStep& a, hipStream_t stream) {
+  const int64_t groups = (int64_t)a.batch * a.heads * ((a.vd + kStepColumns - 1) / kStepColumns);
+  const dim3 grid = grid_of(groups, 256);
+  const bool vec = a.vd % 4 == 0 && (reinterpret_cast<uintptr_t>(a.state) | reinterpret_cast<uintptr_t>(a.state_out)) % 16 == 0;
+  if (vec) attn_step_kernel<T, 4><<<grid, 256, 0, stream>>>(a);
+  else attn_step_kernel<T, 1><<<grid, 256, 0, stream>>>(a);
   return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_attn_step(const AttnStep& a, hipStream_t stream) {
+  return a.dtype == Dtype::BF16 ? step<uint16_t>(a, stream) : step<float>(a, stream);
 }
 
 }  // namespace ssm

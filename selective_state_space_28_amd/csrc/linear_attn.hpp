@@ -39,19 +39,22 @@ struct AttnSweep {
   float* state_out;        // nullable
   int transposed;
   float* seg_state;   // (batch, heads, nseg, kd, vd): states entering the segments, when nseg > 1
+  float* seg_rate;    // the decay's gradient only: its derivative by g, as seg_state
+  float* seg_steps;   // and the steps of the segments, as seg_through
   float* seg_through; // (batch, heads, nseg): what a segment leaves of the state that enters it
   int64_t seglen;     // steps of a segment, a multiple of kAttnChunk
   int nseg;
-  double* part;       // decay's gradient: (heads, batch, column blocks)
+  double* part;       // decay's gradient: (heads, batch, column blocks, nseg)
   Dtype dtype;
 };
 
-// Segments that a sweep of these sizes is split into, and their steps.
+// Segments that a sweep of these sizes, with `blocks` blocks of value columns, is
+// split into, and their steps.
 struct AttnSplit {
   int nseg;
   int64_t seglen;
 };
-AttnSplit attn_split(int batch, int heads, int64_t seqlen, int vd);
+AttnSplit attn_split(int batch, int heads, int64_t seqlen, int blocks);
 // Blocks of value columns, of a sweep and of the decay's gradient.
 int attn_column_blocks(int vd);
 int attn_decay_blocks(int vd);
