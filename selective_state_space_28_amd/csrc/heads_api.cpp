@@ -81,9 +81,15 @@ struct SweepBytes {
   size_t all() const { return state + through + rate + steps + part; }
 };
 
-SweepBytes sweep_bytes(const AttnSizes& s, int blocks, bool decay) {
+// The segments of n sweeps side by side.
+AttnSplit split_of(const AttnSizes& s, int blocks, int n) {
+  const int64_t heads = (int64_t)n * s.batch * s.heads;
+  return attn_split(heads * blocks, s.seqlen, heads * s.kd * s.vd);
+}
+
+SweepBytes sweep_bytes(const AttnSizes& s, int blocks, int n, bool decay) {
   SweepBytes w{};
-  const AttnSplit sp = attn_split(s.batch, s.heads, s.seqlen, blocks);
+  const AttnSplit sp = split_of(s, blocks, n);
   const size_t segs = (size_t)s.batch * (size_t)s.heads * (size_t)sp.nseg;
   if (sp.nseg > 1) {
     w.state = round256(segs * (size_t)s.kd * (size_t)s.vd * 4);
@@ -97,18 +103,23 @@ SweepBytes sweep_bytes(const AttnSizes& s, int blocks, bool decay) {
   return w;
 }
 
-// Of the backward: the sweeps one after another in the same place, then the heads'
-// gradients (float32) where several share one.
+// Of the backward: the sweeps' (dq and dk, with dv where the widths are alike, side by
+// side; what follows in the same place), then the heads' gradients (float32) where
+// several share one.
 struct BwdBytes {
   size_t sweep, dq, dk, dv;
   size_t all() const { return sweep + dq + dk + dv; }
 };
 
+int sweeps_together(const AttnSizes& s) { return attn_alike(s.kd, s.vd) ? 3 : 2; }
+
 BwdBytes bwd_bytes(const AttnSizes& s) {
   const size_t steps = (size_t)s.batch * (size_t)s.seqlen * (size_t)s.heads * 4;
+  const int n = sweeps_together(s);
   BwdBytes w{};
-  for (const size_t b : {sweep_bytes(s, attn_column_blocks(s.kd), false).all(), sweep_bytes(s, attn_column_blocks(s.vd), false).all(),
-                         sweep_bytes(s, attn_decay_blocks(s.vd), true).all()})
+  for (const size_t b : {(size_t)n * sweep_bytes(s, attn_column_blocks(s.kd), n, false).all(),
+                         n == 3 ? (size_t)0 : sweep_bytes(s, attn_column_blocks(s.vd), 1, false).all(),
+                         sweep_bytes(s, attn_decay_blocks(s.vd), 1, true).all()})
     w.sweep = w.sweep > b ? w.sweep : b;
   if (s.hq != s.heads) w.dq = round256(steps * (size_t)s.kd);
   if (s.hk != s.heads) w.dk = round256(steps * (size_t)s.kd);
@@ -116,13 +127,13 @@ BwdBytes bwd_bytes(const AttnSizes& s) {
   return w;
 }
 
-// A sweep with contraction width kd and value width vd over the workspace.
+// The k-th of n sweeps with contraction width kd and value width vd over the workspace.
 AttnSweep attn_sweep(const AttnSizes& s, const float* g, const uint8_t* starts, const int32_t* lengths, int dtype, int kd,
-                     int vd, void* workspace, bool decay = false) {
+                     int vd, void* workspace, int k, int n, bool decay = false) {
   AttnSweep a{};
   const int blocks = decay ? attn_decay_blocks(vd) : attn_column_blocks(vd);
-  const AttnSplit sp = attn_split(s.batch, s.heads, s.seqlen, blocks);
-  const SweepBytes w = sweep_bytes(s, blocks, decay);
+  const AttnSplit sp = split_of(s, blocks, n);
+  const SweepBytes w = sweep_bytes(s, blocks, n, decay);
   a.kd = kd;
   a.vd = vd;
   a.batch = s.batch;
@@ -133,7 +144,7 @@ AttnSweep attn_sweep(const AttnSizes& s, const float* g, const uint8_t* starts, 
   a.lengths = lengths;
   a.nseg = sp.nseg;
   a.seglen = sp.seglen;
-  char* p = static_cast<char*>(workspace);
+  char* p = static_cast<char*>(workspace) + (size_t)k * w.all();
   a.seg_state = reinterpret_cast<float*>(p);
   a.seg_through = reinterpret_cast<float*>(p + w.state);
   a.seg_rate = reinterpret_cast<float*>(p + w.state + w.through);
@@ -186,7 +197,7 @@ extern "C" {
 size_t ssm_linear_attn_fwd_workspace_bytes(int batch, int64_t seqlen, int heads, int key_dim, int value_dim, int dtype) {
   const AttnSizes s{batch, seqlen, heads, 1, 1, 1, key_dim, value_dim};
   if (!dtype_ok(dtype) || !attn_shape_ok(s) || batch == 0 || heads == 0 || seqlen == 0) return 0;
-  return sweep_bytes(s, attn_column_blocks(value_dim), false).all();
+  return sweep_bytes(s, attn_column_blocks(value_dim), 1, false).all();
 }
 
 int ssm_linear_attn_fwd(const void* q, const void* k, const void* v, const int64_t* strides, const float* log_decay,
@@ -211,7 +222,7 @@ int ssm_linear_attn_fwd(const void* q, const void* k, const void* v, const int64
       !aligned(lengths, 4) || !aligned(h0, 4) || !aligned(last_state, 4) || !aligned(workspace, 256))
     return SSM_ERR_ALIGN;
   if (none) return SSM_OK;
-  const size_t need = empty ? 0 : sweep_bytes(s, attn_column_blocks(value_dim), false).all();
+  const size_t need = empty ? 0 : sweep_bytes(s, attn_column_blocks(value_dim), 1, false).all();
   if (need > 0 && (workspace == nullptr || workspace_bytes < need)) return SSM_ERR_WORKSPACE;
   const size_t rows = (size_t)batch * (size_t)seqlen;
   const size_t state = (size_t)batch * (size_t)heads * (size_t)key_dim * (size_t)value_dim * 4;
@@ -229,7 +240,10 @@ int ssm_linear_attn_fwd(const void* q, const void* k, const void* v, const int64
   hipStream_t st = static_cast<hipStream_t>(stream);
   if (empty)
     return last_state == nullptr ? SSM_OK : status_of(launch_fill_state(last_state, h0, (int64_t)(state / 4), st));
-  AttnSweep a = attn_sweep(s, log_decay, starts, lengths, dtype, key_dim, value_dim, workspace);
+  AttnSweeps all{};
+  all.n = 1;
+  AttnSweep& a = all.s[0];
+  a = attn_sweep(s, log_decay, starts, lengths, dtype, key_dim, value_dim, workspace, 0, 1);
   a.q = vq;
   a.k = vk;
   a.v = vv;
@@ -239,7 +253,7 @@ int ssm_linear_attn_fwd(const void* q, const void* k, const void* v, const int64
   a.scale_upd = 1.0f;
   a.state_in = h0;
   a.state_out = last_state;
-  return status_of(launch_attn_sweep(a, st));
+  return status_of(launch_attn_sweeps(all, st));
 }
 
 size_t ssm_linear_attn_bwd_workspace_bytes(int batch, int64_t seqlen, int heads, int q_heads, int k_heads, int v_heads,
@@ -303,8 +317,13 @@ int ssm_linear_attn_bwd(const void* q, const void* k, const void* v, const int64
   float* part_k = reinterpret_cast<float*>(ws + w.sweep + w.dq);
   float* part_v = reinterpret_cast<float*>(ws + w.sweep + w.dq + w.dk);
 
+  const int n = sweeps_together(s);
+  AttnSweeps all{}, last{};
+  all.n = n;
+  last.n = 1;
   // dq: forward in time, the state transposed
-  AttnSweep a = attn_sweep(s, log_decay, starts, lengths, dtype, value_dim, key_dim, ws);
+  AttnSweep& a = all.s[0];
+  a = attn_sweep(s, log_decay, starts, lengths, dtype, value_dim, key_dim, ws, 0, n);
   a.q = vdy;
   a.k = vv;
   a.v = vk;
@@ -315,49 +334,51 @@ int ssm_linear_attn_bwd(const void* q, const void* k, const void* v, const int64
   a.scale_upd = 1.0f;
   a.state_in = h0;
   a.transposed = 1;
-  hipError_t e = launch_attn_sweep(a, st);
-  if (e == hipSuccess && a.out_f32) e = launch_attn_gather(part_q, dq, (int64_t)rows, heads, q_heads, key_dim, a.dtype, st);
-
   // dk: backward in time, the state's gradient transposed
-  a.q = vv;
-  a.k = vdy;
-  a.v = vq;
-  a.out_f32 = w.dk > 0;
-  a.out = a.out_f32 ? part_k : dk;
-  a.scale_in = 1.0f;
-  a.scale_upd = scale;
-  a.state_in = dlast_state;
-  a.rev = 1;
-  if (e == hipSuccess) e = launch_attn_sweep(a, st);
-  if (e == hipSuccess && a.out_f32) e = launch_attn_gather(part_k, dk, (int64_t)rows, heads, k_heads, key_dim, a.dtype, st);
-
+  AttnSweep& ak = all.s[1];
+  ak = attn_sweep(s, log_decay, starts, lengths, dtype, value_dim, key_dim, ws, 1, n);
+  ak.q = vv;
+  ak.k = vdy;
+  ak.v = vq;
+  ak.out_f32 = w.dk > 0;
+  ak.out = ak.out_f32 ? part_k : dk;
+  ak.scale_p = scale;
+  ak.scale_in = 1.0f;
+  ak.scale_upd = scale;
+  ak.state_in = dlast_state;
+  ak.transposed = 1;
+  ak.rev = 1;
   // dv: backward in time
-  a = attn_sweep(s, log_decay, starts, lengths, dtype, key_dim, value_dim, ws);
-  a.q = vk;
-  a.k = vq;
-  a.v = vdy;
-  a.out_f32 = w.dv > 0;
-  a.out = a.out_f32 ? part_v : dv;
-  a.scale_p = scale;
-  a.scale_in = 1.0f;
-  a.scale_upd = scale;
-  a.state_in = dlast_state;
-  a.state_out = dh0;
-  a.rev = 1;
-  if (e == hipSuccess) e = launch_attn_sweep(a, st);
-  if (e == hipSuccess && a.out_f32) e = launch_attn_gather(part_v, dv, (int64_t)rows, heads, v_heads, value_dim, a.dtype, st);
+  AttnSweep& av = n == 3 ? all.s[2] : last.s[0];
+  av = attn_sweep(s, log_decay, starts, lengths, dtype, key_dim, value_dim, ws, n == 3 ? 2 : 0, n == 3 ? 3 : 1);
+  av.q = vk;
+  av.k = vq;
+  av.v = vdy;
+  av.out_f32 = w.dv > 0;
+  av.out = av.out_f32 ? part_v : dv;
+  av.scale_p = scale;
+  av.scale_in = 1.0f;
+  av.scale_upd = scale;
+  av.state_in = dlast_state;
+  av.state_out = dh0;
+  av.rev = 1;
+  hipError_t e = launch_attn_sweeps(all, st);
+  if (e == hipSuccess && n != 3) e = launch_attn_sweeps(last, st);
+  if (e == hipSuccess && w.dq > 0) e = launch_attn_gather(part_q, dq, (int64_t)rows, heads, q_heads, key_dim, a.dtype, st);
+  if (e == hipSuccess && w.dk > 0) e = launch_attn_gather(part_k, dk, (int64_t)rows, heads, k_heads, key_dim, a.dtype, st);
+  if (e == hipSuccess && w.dv > 0) e = launch_attn_gather(part_v, dv, (int64_t)rows, heads, v_heads, value_dim, a.dtype, st);
 
   if (e == hipSuccess && dlog_decay != nullptr) {
-    a = attn_sweep(s, log_decay, starts, lengths, dtype, key_dim, value_dim, ws, true);
-    a.q = vq;
-    a.k = vk;
-    a.v = vv;
-    a.dy = vdy;
-    a.scale_p = scale;
-    a.scale_in = scale;
-    a.scale_upd = 1.0f;
-    a.state_in = h0;
-    e = launch_attn_decay_grad(a, dlast_state, dlog_decay, st);
+    AttnSweep d = attn_sweep(s, log_decay, starts, lengths, dtype, key_dim, value_dim, ws, 0, 1, true);
+    d.q = vq;
+    d.k = vk;
+    d.v = vv;
+    d.dy = vdy;
+    d.scale_p = scale;
+    d.scale_in = scale;
+    d.scale_upd = 1.0f;
+    d.state_in = h0;
+    e = launch_attn_decay_grad(d, dlast_state, dlog_decay, st);
   }
   return status_of(e);
 }

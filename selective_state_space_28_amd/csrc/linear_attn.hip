@@ -383,7 +383,7 @@ enum AttnMode { kAttnOut = 0, kAttnSegments = 1, kAttnDecay = 2, kAttnDecaySegme
 // the end, into a second buffer, V and Q into their own once every wave has done with
 // them.  (Through registers the state would not fit beside them.)
 template <typename T, int KD, int CT, int MODE, bool PACKED>
-__global__ __launch_bounds__(kThreads, KD <= 128 ? 2 : 1) void attn_sweep_kernel(const AttnSweep a,
+__global__ __launch_bounds__(kThreads, KD <= 128 ? 2 : 1) void attn_sweep_kernel(const AttnSweeps all,
                                                                                 const float* __restrict__ dlast,
                                                                                 int64_t groups) {
   using M = Mat<T>;
@@ -413,14 +413,17 @@ __global__ __launch_bounds__(kThreads, KD <= 128 ? 2 : 1) void attn_sweep_kernel
   int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   int m = lane & 15, q4 = 4 * (lane >> 4);
-  const int nvb = (a.vd + NV - 1) / NV;
-  const int nsegs = kSegments ? a.nseg - 1 : a.nseg;
   // consecutive workgroups go to the 8 dies in turn: a die takes consecutive numbers,
   // whose column blocks, and heads that share q, k or v, read the same lines
   int64_t id = group_index();
   const int64_t per = (groups + 7) / 8;
   id = (id & 7) * per + (id >> 3);
   if ((group_index() >> 3) >= per || id >= groups) return;
+  const int64_t each = groups / all.n;
+  const AttnSweep& a = all.s[id / each];
+  id %= each;
+  const int nvb = (a.vd + NV - 1) / NV;
+  const int nsegs = kSegments ? a.nseg - 1 : a.nseg;
   const int vb = (int)(id % nvb);
   id /= nvb;
   const int h = (int)(id % a.heads);
@@ -962,19 +965,20 @@ __global__ __launch_bounds__(kThreads, KD <= 128 ? 2 : 1) void attn_sweep_kernel
 
 // The states entering the segments from what each adds: S <- through S + added, and with
 // `rate`, R <- through (R + steps S) + added; a thread an element.
-__global__ __launch_bounds__(256) void attn_carry_kernel(float* __restrict__ state, float* __restrict__ rate,
-                                                         const float* __restrict__ through, const float* __restrict__ steps,
-                                                         const float* __restrict__ state_in, int kd, int vd, int nseg,
-                                                         int transposed, int64_t n) {
-  const int64_t i = group_index() * 256 + threadIdx.x;
-  if (i >= n) return;
-  const int mat = kd * vd;
+__global__ __launch_bounds__(256) void attn_carry_kernel(const AttnSweeps all, bool rates, int64_t n) {
+  int64_t i = group_index() * 256 + threadIdx.x;
+  if (i >= n * all.n) return;
+  const AttnSweep& a = all.s[i / n];
+  i %= n;
+  const int mat = a.kd * a.vd, nseg = a.nseg;
+  float *state = a.seg_state, *rate = rates ? a.seg_rate : nullptr;
+  const float *state_in = a.state_in, *steps = a.seg_steps;
   const int64_t head = i / mat;
-  const int e = (int)(i - head * mat), row = e / vd, col = e - row * vd;
+  const int e = (int)(i - head * mat), row = e / a.vd, col = e - row * a.vd;
   float s = 0.0f, r = 0.0f;
-  if (state_in != nullptr) s = state_in[head * mat + (transposed ? col * kd + row : e)];
+  if (state_in != nullptr) s = state_in[head * mat + (a.transposed ? col * a.kd + row : e)];
   const int64_t first = head * nseg * mat + e;
-  const float* th = through + head * nseg;
+  const float* th = a.seg_through + head * nseg;
   constexpr int U = 8;  // segments on their way at once
   for (int k0 = 0; k0 + 1 < nseg; k0 += U) {
     float added[U], more[U];
@@ -1102,53 +1106,55 @@ namespace {
 int column_tiles(int vd) { return vd <= 64 ? 1 : 2; }
 
 template <typename T, int KD, int CT, int MODE>
-hipError_t sweep(const AttnSweep& a, const float* dlast, hipStream_t stream) {
+hipError_t sweep(const AttnSweeps& all, const float* dlast, hipStream_t stream) {
+  const AttnSweep& a = all.s[0];  // the others have its numbers of groups
   const int nvb = (a.vd + 64 * CT - 1) / (64 * CT);
   const int nsegs = MODE == kAttnSegments || MODE == kAttnDecaySegments ? a.nseg - 1 : a.nseg;
-  const int64_t groups = (int64_t)a.batch * a.heads * nvb * nsegs;
+  const int64_t groups = (int64_t)all.n * a.batch * a.heads * nvb * nsegs;
   const dim3 grid = grid_of((groups + 7) / 8 * 8, kThreads);
-  if (a.starts != nullptr) attn_sweep_kernel<T, KD, CT, MODE, true><<<grid, kThreads, 0, stream>>>(a, dlast, groups);
-  else attn_sweep_kernel<T, KD, CT, MODE, false><<<grid, kThreads, 0, stream>>>(a, dlast, groups);
+  if (a.starts != nullptr) attn_sweep_kernel<T, KD, CT, MODE, true><<<grid, kThreads, 0, stream>>>(all, dlast, groups);
+  else attn_sweep_kernel<T, KD, CT, MODE, false><<<grid, kThreads, 0, stream>>>(all, dlast, groups);
   return hipGetLastError();
 }
 
 template <typename T, int CT, int MODE>
-hipError_t sweep_of(const AttnSweep& a, const float* dlast, hipStream_t stream) {
-  if (a.kd <= 64) return sweep<T, 64, CT, MODE>(a, dlast, stream);
-  if (a.kd <= 128) return sweep<T, 128, CT, MODE>(a, dlast, stream);
-  return sweep<T, 256, CT, MODE>(a, dlast, stream);
+hipError_t sweep_of(const AttnSweeps& all, const float* dlast, hipStream_t stream) {
+  if (all.s[0].kd <= 64) return sweep<T, 64, CT, MODE>(all, dlast, stream);
+  if (all.s[0].kd <= 128) return sweep<T, 128, CT, MODE>(all, dlast, stream);
+  return sweep<T, 256, CT, MODE>(all, dlast, stream);
 }
 
 template <typename T, int MODE>
-hipError_t sweep_of(const AttnSweep& a, hipStream_t stream) {
-  return column_tiles(a.vd) == 1 ? sweep_of<T, 1, MODE>(a, nullptr, stream) : sweep_of<T, 2, MODE>(a, nullptr, stream);
+hipError_t sweep_of(const AttnSweeps& all, hipStream_t stream) {
+  return column_tiles(all.s[0].vd) == 1 ? sweep_of<T, 1, MODE>(all, nullptr, stream)
+                                        : sweep_of<T, 2, MODE>(all, nullptr, stream);
 }
 
-hipError_t carry(const AttnSweep& a, float* rate, hipStream_t stream) {
+hipError_t carry(const AttnSweeps& all, bool rates, hipStream_t stream) {
+  const AttnSweep& a = all.s[0];
   const int64_t n = (int64_t)a.batch * a.heads * a.kd * a.vd;
-  attn_carry_kernel<<<grid_of((n + 255) / 256, 256), 256, 0, stream>>>(a.seg_state, rate, a.seg_through, a.seg_steps,
-                                                                       a.state_in, a.kd, a.vd, a.nseg, a.transposed, n);
+  attn_carry_kernel<<<grid_of((n * all.n + 255) / 256, 256), 256, 0, stream>>>(all, rates, n);
   return hipGetLastError();
 }
 
 template <typename T>
-hipError_t run_sweep(const AttnSweep& a, hipStream_t stream) {
-  if (a.nseg > 1) {
-    hipError_t e = sweep_of<T, kAttnSegments>(a, stream);
-    if (e == hipSuccess) e = carry(a, nullptr, stream);
+hipError_t run_sweeps(const AttnSweeps& all, hipStream_t stream) {
+  if (all.s[0].nseg > 1) {
+    hipError_t e = sweep_of<T, kAttnSegments>(all, stream);
+    if (e == hipSuccess) e = carry(all, false, stream);
     if (e != hipSuccess) return e;
   }
-  return sweep_of<T, kAttnOut>(a, stream);
+  return sweep_of<T, kAttnOut>(all, stream);
 }
 
 template <typename T>
-hipError_t run_decay(const AttnSweep& a, const float* dlast, hipStream_t stream) {
-  if (a.nseg > 1) {
-    hipError_t e = sweep_of<T, 1, kAttnDecaySegments>(a, dlast, stream);
-    if (e == hipSuccess) e = carry(a, a.seg_rate, stream);
+hipError_t run_decay(const AttnSweeps& all, const float* dlast, hipStream_t stream) {
+  if (all.s[0].nseg > 1) {
+    hipError_t e = sweep_of<T, 1, kAttnDecaySegments>(all, dlast, stream);
+    if (e == hipSuccess) e = carry(all, true, stream);
     if (e != hipSuccess) return e;
   }
-  return sweep_of<T, 1, kAttnDecay>(a, dlast, stream);
+  return sweep_of<T, 1, kAttnDecay>(all, dlast, stream);
 }
 
 }  // namespace
@@ -1157,25 +1163,51 @@ int attn_column_blocks(int vd) { return (vd + 64 * column_tiles(vd) - 1) / (64 *
 
 int attn_decay_blocks(int vd) { return (vd + 63) / 64; }
 
-AttnSplit attn_split(int batch, int heads, int64_t seqlen, int blocks) {
-  // two workgroups for each of the 256 CUs, segments of 4 chunks at least
-  const int64_t groups = (int64_t)batch * heads * blocks;
+// Workgroups and segments.  A sweep of one chunk after another takes a time that a CU's
+// two workgroups share only in part (bf16, heads of 128, microseconds a chunk): 5.4 where
+// half the CUs have one, 6.3 with one on each, 8.9 with two.  Segments fill the CUs, and
+// cost the pass that finds their states (0.58 of the main one's time) with two more launches
+// and the states' traffic, some 20 us and more.  The least of these sums is taken, of
+// up to 64 segments of 4 chunks and more (batch 8, L 2048 bf16: 16 heads 173 us in one
+// piece, 133 in segments; 32 heads 202 and 244).
+AttnSplit attn_split(int64_t groups, int64_t seqlen, int64_t state_elements) {
   const int64_t chunks = (seqlen + kAttnChunk - 1) / kAttnChunk;
-  int64_t want = groups >= 512 || groups == 0 ? 1 : 512 / groups;
-  if (want > chunks / 4) want = chunks / 4;
-  if (want < 2) return AttnSplit{1, (chunks > 0 ? chunks : 1) * kAttnChunk};
-  const int64_t per = (chunks + want - 1) / want;
-  return AttnSplit{(int)((chunks + per - 1) / per), per * kAttnChunk};
+  const auto rounds = [](int64_t g) {
+    const int64_t left = g % 512;
+    return 8.9 * (double)(g / 512) + (left == 0 ? 0.0 : left <= 128 ? 5.4 : left <= 256 ? 6.3 : 8.9);
+  };
+  AttnSplit best{1, (chunks > 0 ? chunks : 1) * kAttnChunk};
+  if (groups <= 0) return best;
+  double least = (double)chunks * rounds(groups);
+  for (int64_t n = 2; n <= 64 && 4 * n <= chunks; ++n) {
+    const int64_t per = (chunks + n - 1) / n, nseg = (chunks + per - 1) / per;
+    const double states = 16e-6 / 4.0 * (double)state_elements * (double)nseg;  // four passes of float32 at 4 TB/s
+    const double t = (double)per * (rounds(groups * nseg) + 0.58 * rounds(groups * (nseg - 1))) + 20.0 + states;
+    if (t < least) {
+      least = t;
+      best = AttnSplit{(int)nseg, per * kAttnChunk};
+    }
+  }
+  return best;
 }
 
-hipError_t launch_attn_sweep(const AttnSweep& a, hipStream_t stream) {
-  return a.dtype == Dtype::BF16 ? run_sweep<uint16_t>(a, stream) : run_sweep<float>(a, stream);
+bool attn_alike(int a, int b) {
+  const auto kind = [](int width) { return width <= 64 ? 0 : width <= 128 ? 1 : 2; };
+  return kind(a) == kind(b);
+}
+
+hipError_t launch_attn_sweeps(const AttnSweeps& all, hipStream_t stream) {
+  return all.s[0].dtype == Dtype::BF16 ? run_sweeps<uint16_t>(all, stream) : run_sweeps<float>(all, stream);
 }
 
 hipError_t launch_attn_decay_grad(const AttnSweep& a, const float* dlast, float* dlog_decay, hipStream_t stream) {
-  const hipError_t e = a.dtype == Dtype::BF16 ? run_decay<uint16_t>(a, dlast, stream) : run_decay<float>(a, dlast, stream);
+  AttnSweeps all{};
+  all.s[0] = a;
+  all.n = 1;
+  const hipError_t e = a.dtype == Dtype::BF16 ? run_decay<uint16_t>(all, dlast, stream) : run_decay<float>(all, dlast, stream);
   if (e != hipSuccess) return e;
-  attn_decay_sum_kernel<<<a.heads, 64, 0, stream>>>(a.part, dlog_decay, (int64_t)a.batch * attn_decay_blocks(a.vd) * a.nseg);
+  attn_decay_sum_kernel<<<a.heads, 64, 0, stream>>>(a.part, dlog_decay,
+                                                    (int64_t)a.batch * attn_decay_blocks(a.vd) * a.nseg);
   return hipGetLastError();
 }
 

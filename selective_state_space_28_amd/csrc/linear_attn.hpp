@@ -48,13 +48,21 @@ struct AttnSweep {
   Dtype dtype;
 };
 
-// Segments that a sweep of these sizes, with `blocks` blocks of value columns, is
-// split into, and their steps.
+// Sweeps that run side by side: of the same sizes but for kd and vd, which are alike
+// (attn_alike), and with the same segments.
+struct AttnSweeps {
+  AttnSweep s[3];
+  int n;
+};
+bool attn_alike(int a, int b);
+
+// Segments that `groups` (sweeps, batch rows, heads and blocks of value columns) of
+// seqlen steps, with so many elements in their states, are split into, and their steps.
 struct AttnSplit {
   int nseg;
   int64_t seglen;
 };
-AttnSplit attn_split(int batch, int heads, int64_t seqlen, int blocks);
+AttnSplit attn_split(int64_t groups, int64_t seqlen, int64_t state_elements);
 // Blocks of value columns, of a sweep and of the decay's gradient.
 int attn_column_blocks(int vd);
 int attn_decay_blocks(int vd);
@@ -71,7 +79,7 @@ struct AttnStep {
   Dtype dtype;
 };
 
-hipError_t launch_attn_sweep(const AttnSweep& a, hipStream_t stream);
+hipError_t launch_attn_sweeps(const AttnSweeps& all, hipStream_t stream);
 // dlog_decay (heads) += over batch and steps; a.q, a.k, a.v as in the forward sweep, a.dy the gradient, a.state_out
 // the gradient of the last state (nullable).
 hipError_t launch_attn_decay_grad(const AttnSweep& a, const float* dlast, float* dlog_decay, hipStream_t stream);

@@ -63,11 +63,11 @@ BAD_SIZES = [
 
 @pytest.mark.parametrize("kw,code", BAD_SIZES + [
     (dict(y=None), NULL), (dict(y=at(4) + 1), ALIGN), (dict(last=at(9) + 2), ALIGN), (dict(ws=at(10) + 64), ALIGN),
-    (dict(batch=1, H=1, hq=1, hv=1, ws=None), WS), (dict(batch=1, H=1, hq=1, hv=1, wsb=100), WS),
+    (dict(batch=1, L=16384, H=1, hq=1, hv=1, ws=None), WS), (dict(batch=1, L=16384, H=1, hq=1, hv=1, wsb=100), WS),
     (dict(y=at(0)), ALIAS), (dict(y=at(2) + Y - 2), ALIAS), (dict(last=at(4) + 4), ALIAS), (dict(last=at(3)), ALIAS),
     (dict(h0=at(9), last=at(9) + 8), ALIAS), (dict(st=at(4) + 128), ALIAS), (dict(ln=at(4) + 128), ALIAS),
     (dict(sd=strides(0, 0, 0, 0, 0, 0, L * 1000, 1000, 64), y=at(2) + 2 * L * 1000), ALIAS),
-    (dict(batch=1, H=1, hq=1, hv=1, ws=at(4)), ALIAS),
+    (dict(batch=1, L=16384, H=1, hq=1, hv=1, ws=at(4)), ALIAS),
     (dict(batch=0), OK), (dict(H=0, q=None, y=None), OK), (dict(L=0, q=None, y=None), OK),
     (dict(batch=0, kd=300), SHAPE),
 ])
