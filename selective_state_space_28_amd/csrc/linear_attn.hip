@@ -591,20 +591,49 @@ __global__ __launch_bounds__(kThreads, KD <= 128 ? 2 : 1) void attn_sweep_kernel
       if constexpr (kRate) s_left[i] = w * (float)left;
     }
 
+    // this wave's columns of V, contracted over the steps
+    Frag vf[CT][C / CK];
+#pragma unroll
+    for (int ct = 0; ct < CT; ++ct)
+#pragma unroll
+      for (int s = 0; s < C / CK; ++s) vf[ct][s] = M::template col<NV>(s_v, value_at, CK * s, 16 * ct);
+
     if constexpr (kOut) {
-      // P = W o Q K^T, tile (it, jt) at a time, transposed so that a lane holds 4 steps j of a row i
+      // P = W o Q K^T, this wave's tiles, transposed so that a lane holds 4 steps j of a row i
       const int lane = own(threadIdx.x & 63), m = lane & 15, q4 = 4 * (lane >> 4);
+      // (a wave without a last tile forms another's again, and keeps it to itself)
+      int row0[kMyTiles], col0[kMyTiles];
+      f32x4 tiles[kMyTiles];
+      Frag fk[2][kMyTiles], fq[2][kMyTiles];
+      int w0 = wave;
+      asm volatile("" : "+s"(w0));  // (as `own`)
 #pragma unroll
       for (int k = 0; k < kMyTiles; ++k) {
-        int tile = wave + k * kWaves;
-        asm volatile("" : "+s"(tile));  // (as `own`)
-        if (tile >= kTiles) break;
-        in_order();
-        const int it = tile_row(tile), jt = tile_col(tile);
-        f32x4 acc = {0, 0, 0, 0};
+        const int tile = min(w0 + k * kWaves, kTiles - 1);
+        row0[k] = 16 * tile_row(tile);
+        col0[k] = 16 * tile_col(tile);
+        tiles[k] = f32x4{0, 0, 0, 0};
+        fk[0][k] = M::template run<KD>(s_k, run_at, col0[k], 0);
+        fq[0][k] = M::template run<KD>(s_q, run_at, row0[k], 0);
+      }
 #pragma unroll
-        for (int kk = 0; kk < KD; kk += CK)
-          acc = M::mma(M::template run<KD>(s_k, run_at, 16 * jt, kk), M::template run<KD>(s_q, run_at, 16 * it, kk), acc);
+      for (int kk = 0; kk < KD / CK; ++kk) {
+        in_order();
+#pragma unroll
+        for (int k = 0; k < kMyTiles; ++k) {
+          if (kk + 1 < KD / CK) {
+            fk[kk + 1 & 1][k] = M::template run<KD>(s_k, run_at, col0[k], (kk + 1) * CK);
+            fq[kk + 1 & 1][k] = M::template run<KD>(s_q, run_at, row0[k], (kk + 1) * CK);
+          }
+          tiles[k] = M::mma(fk[kk & 1][k], fq[kk & 1][k], tiles[k]);
+        }
+      }
+      in_order();
+#pragma unroll
+      for (int k = 0; k < kMyTiles; ++k) {
+        if (w0 + k * kWaves >= kTiles) break;
+        const f32x4 acc = tiles[k];
+        const int it = row0[k] / 16, jt = col0[k] / 16;
         const int i = 16 * it + m;
         float p[4];
 #pragma unroll
@@ -632,16 +661,11 @@ __global__ __launch_bounds__(kThreads, KD <= 128 ? 2 : 1) void attn_sweep_kernel
       }
     }
 
-    // this wave's columns of V, contracted over the steps
-    Frag vf[CT][C / CK];
     float odd = 0.0f;  // NaN if any of the values is not finite
 #pragma unroll
     for (int ct = 0; ct < CT; ++ct)
 #pragma unroll
-      for (int s = 0; s < C / CK; ++s) {
-        vf[ct][s] = M::template col<NV>(s_v, value_at, CK * s, 16 * ct);
-        odd = M::times_zero(vf[ct][s], odd);
-      }
+      for (int s = 0; s < C / CK; ++s) odd = M::times_zero(vf[ct][s], odd);
     const bool careful = __any(!(odd == 0.0f));
     f32x4 acc[kOut ? CT : 1][kOut ? IT : 1], acc_r[kDecay ? CT : 1][kDecay ? IT : 1];
     if constexpr (kOut) {
