@@ -7,6 +7,8 @@
 // times, so it is read once; its sums go over the lanes by DPP.  A wave keeps its
 // channels and goes over tokens, so that weight and bias are read once, and the
 // sums of dweight and dbias stay in registers until its last token.
+#include <algorithm>
+
 #include "gated_math.hpp"
 #include "runs.hpp"
 #include "ssm_group_norm.h"
@@ -18,6 +20,14 @@ namespace {
 
 constexpr int kWaves = 4;    // of a workgroup
 constexpr int kBlockSpan = 64 * kWaves;
+
+// Workgroups that share the tokens.  Forward: many, a few tokens a wave (32768 tokens of
+// 5120 bf16 in groups of 128, with a gate: 191 us; with 2048 of them 234, with 32768
+// 217).  Backward: each leaves a part of dweight and dbias, so fewer, with 32 tokens to a
+// part where that leaves 512 (16384 tokens of 5120: 177 us; with 1024 of them 185; but
+// 4096 tokens of 8192 in one group: 124 us with 1024, 173 with 2048, 260 with 4096).
+// Loading a token ahead cost both (191 -> 200, 176 -> 191).
+constexpr int kFwdGroups = 8192, kBwdGroups = 2048, kBwdLeast = 512, kPartTokens = 32;
 
 // Sum over the LR lanes of a group, in every lane of it; the order is fixed.
 template <int LR, typename V>
@@ -133,10 +143,15 @@ __global__ __launch_bounds__(kBlockSpan) void group_norm_fwd_kernel(const GroupN
   for (int64_t t = p.token; t < a.tokens; t += p.step) {
     if (!p.live) break;
     float v[K][kRun];
+    RunWords<T> zw[K];
     GroupSum<T> sum = 0;
 #pragma unroll
     for (int c = 0; c < K; ++c) {
       run_floats<T>(load_run(x + t * a.x_stride + at[c], valid[c]), v[c]);
+      if (z != nullptr) zw[c] = load_run(z + t * a.z_stride + at[c], valid[c]);  // on its way with x
+    }
+#pragma unroll
+    for (int c = 0; c < K; ++c) {
 #pragma unroll
       for (int k = 0; k < kRun; ++k) sum = sizeof(T) == 4 ? sum + v[c][k] : __builtin_fmaf(v[c][k], kSumScale, sum);
     }
@@ -158,13 +173,13 @@ __global__ __launch_bounds__(kBlockSpan) void group_norm_fwd_kernel(const GroupN
 #pragma unroll
     for (int c = 0; c < K; ++c) {
       float f[kRun], slope;
-      if (z != nullptr) run_floats<T>(load_run(z + t * a.z_stride + at[c], valid[c]), f);
+      if (z != nullptr) run_floats<T>(zw[c], f);
 #pragma unroll
       for (int k = 0; k < kRun; ++k) {
         const float u = __builtin_fmaf(v[c][k] * rstd, w[c][k], bias[c][k]);
         f[k] = z != nullptr ? u * act_of(a.act, f[k], slope) : act_of(a.act, u, slope);
       }
-      store_run<T>(y + t * a.dim + at[c], valid[c], f);
+      store_run<T, sizeof(T) == 2>(y + t * a.dim + at[c], valid[c], f);
     }
   }
 }
@@ -287,7 +302,7 @@ struct GroupPlan {
   int64_t slices;  // workgroups that go over the tokens of a slab
 };
 
-GroupPlan group_plan(int64_t tokens, int dim, int groups) {
+GroupPlan group_plan(int64_t tokens, int dim, int groups, bool bwd) {
   const int width = dim / groups;
   GroupPlan pl{1, 1, 1, 1};
   while (pl.LR < 64 && pl.LR * kRun < width) pl.LR *= 2;
@@ -301,7 +316,9 @@ GroupPlan group_plan(int64_t tokens, int dim, int groups) {
   const int64_t per = lanes < team ? team / lanes : 1;
   pl.slabs = (int)((lanes + team - 1) / team);
   const int64_t rounds = (tokens + teams * per - 1) / (teams * per);  // workgroups that have a token
-  pl.slices = (2048 + pl.slabs - 1) / pl.slabs;
+  const auto over = [&](int64_t n) { return (n + pl.slabs - 1) / pl.slabs; };
+  pl.slices = over(kFwdGroups);
+  if (bwd) pl.slices = std::min(over(kBwdGroups), std::max(over(kBwdLeast), tokens / kPartTokens));
   if (pl.slices > rounds) pl.slices = rounds;
   return pl;
 }
@@ -332,13 +349,13 @@ hipError_t run_plan(const GroupNormLaunch& a, const GroupPlan& pl, bool bwd, hip
 }
 
 hipError_t launch(const GroupNormLaunch& a, bool bwd, hipStream_t stream) {
-  const GroupPlan pl = group_plan(a.tokens, a.dim, a.groups);
+  const GroupPlan pl = group_plan(a.tokens, a.dim, a.groups, bwd);
   return a.dtype == Dtype::BF16 ? run_plan<uint16_t>(a, pl, bwd, stream) : run_plan<float>(a, pl, bwd, stream);
 }
 
 }  // namespace
 
-int64_t group_norm_bwd_parts(int64_t tokens, int dim, int groups) { return group_plan(tokens, dim, groups).slices; }
+int64_t group_norm_bwd_parts(int64_t tokens, int dim, int groups) { return group_plan(tokens, dim, groups, true).slices; }
 
 hipError_t launch_group_norm_fwd(const GroupNormLaunch& a, hipStream_t stream) { return launch(a, false, stream); }
 
