@@ -3,7 +3,7 @@
 //
 // Both directions are bound by HBM: some 13 and 28 operations an element against 6
 // to 10 bytes of bf16.  A group lies in the registers of 1 to 64 lanes of a wave, or
-// of a workgroup of 256 (groups of more than 2048 channels), each kRun channels K
+// of a workgroup of 256 (groups of more than 1024 channels), each kRun channels K
 // times, so it is read once; its sums go over the lanes by DPP.  A wave keeps its
 // channels and goes over tokens, so that weight and bias are read once, and the
 // sums of dweight and dbias stay in registers until its last token.
@@ -306,10 +306,10 @@ GroupPlan group_plan(int64_t tokens, int dim, int groups, bool bwd) {
   const int width = dim / groups;
   GroupPlan pl{1, 1, 1, 1};
   while (pl.LR < 64 && pl.LR * kRun < width) pl.LR *= 2;
-  while (pl.K < 4 && pl.LR * pl.K * kRun < width) pl.K *= 2;
+  while (pl.K < 2 && pl.LR * pl.K * kRun < width) pl.K *= 2;
   if (pl.LR * pl.K * kRun < width) {
     pl.LR = 256;
-    pl.K = width <= 256 * 2 * kRun ? 2 : 4;
+    pl.K = width <= 256 * kRun ? 1 : width <= 256 * 2 * kRun ? 2 : 4;
   }
   const int team = pl.LR > 64 ? pl.LR : 64, teams = kBlockSpan / team;
   const int64_t lanes = (int64_t)groups * pl.LR;
@@ -342,9 +342,9 @@ hipError_t run_plan(const GroupNormLaunch& a, const GroupPlan& pl, bool bwd, hip
     case 32: return run<T, 1, 32>(a, pl, bwd, stream);
     case 64:
       if (pl.K == 1) return run<T, 1, 64>(a, pl, bwd, stream);
-      if (pl.K == 2) return run<T, 2, 64>(a, pl, bwd, stream);
-      return run<T, 4, 64>(a, pl, bwd, stream);
+      return run<T, 2, 64>(a, pl, bwd, stream);
   }
+  if (pl.K == 1) return run<T, 1, 256>(a, pl, bwd, stream);
   return pl.K == 2 ? run<T, 2, 256>(a, pl, bwd, stream) : run<T, 4, 256>(a, pl, bwd, stream);
 }
 
