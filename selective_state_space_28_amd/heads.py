@@ -14,8 +14,8 @@ _ACTS = {"none": SSM_ACT_NONE, "silu": SSM_ACT_SILU, "sigmoid": SSM_ACT_SIGMOID}
 _MAX_WIDTH = 256
 
 
-def _strided(name, t, lead, width, dtype, dev):
-    """The address of an operand (*lead, heads, width) whose last axis is contiguous, and its number of heads."""
+def _refuse(name, t, lead, width, dtype, dev):
+    """What is wrong with an operand (*lead, heads, width), as an error."""
     if t is None:
         raise ValueError(f"{name} is required")
     if t.dim() != len(lead) + 2 or t.shape[:-2] != lead or (width is not None and t.shape[-1] != width):
@@ -27,32 +27,38 @@ def _strided(name, t, lead, width, dtype, dev):
         raise TypeError(f"{name} has dtype {t.dtype}, expected {dtype}")
     if t.stride(-1) != 1 and t.shape[-1] > 1:
         raise ValueError(f"{name} must be contiguous along its last axis")
-    return t.data_ptr(), t.shape[-2]
 
 
 def _heads_in(q, k, v, log_decay, lead, dev):
     """(addresses of q, k, v; host array of their strides or None; heads and widths; address of log_decay)."""
-    dt = q.dtype
-    pq, hq = _strided("q", q, lead, None, dt, dev)
-    kd = q.shape[-1]
-    pk, hk = _strided("k", k, lead, kd, dt, dev)
-    pv, hv = _strided("v", v, lead, None, dt, dev)
-    vd = v.shape[-1]
-    if log_decay is None or log_decay.dim() != 1:
+    dt, idx = q.dtype, dev.index
+    if k is None or v is None or log_decay is None:
+        raise ValueError("q, k, v and log_decay are required")
+    qs, ks, vs, gs = q.shape, k.shape, v.shape, log_decay.shape
+    # (a token's call is mostly host time: what fits is seen to at once)
+    whole = q.is_contiguous() and k.is_contiguous() and v.is_contiguous()
+    if not (whole and k.dtype is dt and v.dtype is dt and k.get_device() == idx and v.get_device() == idx
+            and len(ks) == len(qs) and len(vs) == len(qs) and ks[:-2] == lead and vs[:-2] == lead and ks[-1] == qs[-1]):
+        _refuse("q", q, lead, None, dt, dev)
+        _refuse("k", k, lead, qs[-1], dt, dev)
+        _refuse("v", v, lead, None, dt, dev)
+    if len(gs) != 1:
         raise ValueError("log_decay must be (heads,)")
-    heads = _int32("heads", log_decay.shape[0])
-    pg = _in("log_decay", log_decay, (heads,), _F32, dev)
-    for name, n in (("q", hq), ("k", hk), ("v", hv)):
-        if heads > 0 and (n < 1 or heads % n != 0):
-            raise ValueError(f"{name} has {n} heads, which do not divide the {heads} of log_decay")
-    for name, n in (("q and k", kd), ("v", vd)):
-        if not 1 <= n <= _MAX_WIDTH:
-            raise ValueError(f"{name} are {n} wide, not 1 to {_MAX_WIDTH}")
+    heads, hq, hk, hv, kd, vd = gs[0], qs[-2], ks[-2], vs[-2], qs[-1], vs[-1]
+    pg = _in("log_decay", log_decay, gs, _F32, dev)
+    if not (hq == hk == hv == heads and 1 <= kd <= _MAX_WIDTH and 1 <= vd <= _MAX_WIDTH):
+        _int32("heads", heads)
+        for name, n in (("q", hq), ("k", hk), ("v", hv)):
+            if heads > 0 and (n < 1 or heads % n != 0):
+                raise ValueError(f"{name} has {n} heads, which do not divide the {heads} of log_decay")
+        for name, n in (("q and k", kd), ("v", vd)):
+            if not 1 <= n <= _MAX_WIDTH:
+                raise ValueError(f"{name} are {n} wide, not 1 to {_MAX_WIDTH}")
     strides = None
-    if not (q.is_contiguous() and k.is_contiguous() and v.is_contiguous()):
+    if not whole:
         steps = q.stride()[:-1] + k.stride()[:-1] + v.stride()[:-1]
         strides = (ctypes.c_int64 * len(steps))(*steps)
-    return (pq, pk, pv), strides, (heads, hq, hk, hv, kd, vd), pg
+    return (q.data_ptr(), k.data_ptr(), v.data_ptr()), strides, (heads, hq, hk, hv, kd, vd), pg
 
 
 def _scale(scale, kd):
@@ -159,9 +165,9 @@ def ssm_linear_attn_state_update(state, q, k, v, log_decay, *, scale=None, start
     lib = load()
     dev = _gpu(q)
     code = _code(q)
+    lead = q.shape[:1]
     if q.dim() != 3:
         raise ValueError(f"q must be (batch, heads, width), not {tuple(q.shape)}")
-    lead = q.shape[:1]
     batch = _int32("batch", lead[0])
     ps = _starts_in(starts, lead, dev)
     ins, strides, sizes, pg = _heads_in(q, k, v, log_decay, lead, dev)
@@ -169,8 +175,12 @@ def ssm_linear_attn_state_update(state, q, k, v, log_decay, *, scale=None, start
     shape = (batch, heads, kd, vd)
     p0 = _in("state", state, shape, _F32, dev)
     po = _in("state_out", state_out, shape, _F32, dev, required=False)
-    y = out if out is not None else torch.empty((batch, heads, vd), dtype=q.dtype, device=dev)
-    py = _in("out", y, (batch, heads, vd), q.dtype, dev)
+    if out is None:  # (a third quicker than empty with a shape)
+        y = torch.empty_like(v) if strides is None and sizes[3] == heads else torch.empty((batch, heads, vd), dtype=q.dtype,
+                                                                                          device=dev)
+        py = y.data_ptr()
+    else:
+        y, py = out, _in("out", out, (batch, heads, vd), q.dtype, dev)
     _call(lib.ssm_linear_attn_state_update, "ssm_linear_attn_state_update", dev, p0, *ins, strides, pg, _scale(scale, kd),
           ps, py, po, batch, *sizes, code)
     return y
@@ -240,8 +250,11 @@ def ssm_group_norm_fwd(x, groups, weight=None, bias=None, z=None, *, act="none",
     pz, zs = _rows("z", z, shape, dt, dev) if z is not None else (None, 0)
     pw = _in("weight", weight, (dim,), _F32, dev, required=False)
     pb = _in("bias", bias, (dim,), _F32, dev, required=False)
-    y = out if out is not None else torch.empty(shape, dtype=dt, device=dev)
-    py = _in("out", y, shape, dt, dev)
+    if out is None:
+        y = torch.empty_like(x) if xs == dim and x.is_contiguous() else torch.empty(shape, dtype=dt, device=dev)
+        py = y.data_ptr()
+    else:
+        y, py = out, _in("out", out, shape, dt, dev)
     mean = rstd = None
     if return_stats:
         mean = torch.empty((*shape[:-1], groups), dtype=_F32, device=dev)
