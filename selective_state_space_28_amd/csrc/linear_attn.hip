@@ -339,7 +339,7 @@ __device__ __forceinline__ void stage(T* lds, const Slice& s, int u, int width, 
     }
   } else {
 #pragma unroll 1
-    for (int i = threadIdx.x; i < ROWS * W; i += kThreads) {
+    for (int i = own(threadIdx.x); i < ROWS * W; i += kThreads) {
       const int r = i / W, c = i % W;
       T e = (T)0;
       if (r < n && c < width) e = reinterpret_cast<const T*>(s.p + (int64_t)(u + r) * s.st)[c];
@@ -536,6 +536,8 @@ __global__ __launch_bounds__(kThreads, KD <= 128 ? 2 : 1) void attn_sweep_kernel
   const int run_at = M::template run_base<KD>(lane), row_at = M::template row_base<KD>(lane),
             key_at = M::template col_base<KD>(lane), value_at = M::template col_base<NV>(lane) ^ c0,
             p_at = M::template row_base<C>(lane);
+  // (where packed rows take registers too, what moves them is formed anew for every chunk)
+  const auto place = [](int at) { return PACKED ? own(at) : at; };
   // this wave's tiles of P: e^{g (i-j)} of the lane's steps, 0 above the diagonal
   float wp[kOut ? kMyTiles : 1][4];
   if constexpr (kOut) {
@@ -556,7 +558,7 @@ __global__ __launch_bounds__(kThreads, KD <= 128 ? 2 : 1) void attn_sweep_kernel
     if (n == 0 && MODE != kAttnOut) break;
     lane = own(lane);
     if (kOut && n == 0) {  // steps behind the row's length
-      for (int64_t i = threadIdx.x; i < (int64_t)(u_end - u0) * vw; i += kThreads) {
+      for (int64_t i = own(threadIdx.x); i < (int64_t)(u_end - u0) * vw; i += kThreads) {
         const int64_t at = (((int64_t)b * L + u0 + i / vw) * a.heads + h) * a.vd + v0 + i % vw;
         if (a.out_f32) static_cast<float*>(a.out)[at] = 0.0f;
         else out[at] = (T)0;
@@ -583,8 +585,8 @@ __global__ __launch_bounds__(kThreads, KD <= 128 ? 2 : 1) void attn_sweep_kernel
     const T* s_k = s_keys[turn];
     turn ^= 1;
     stage_k(u0 + C, turn);
-    if (threadIdx.x < C) {  // the weights of the state that enters, and of each step in the one that leaves
-      const int i = threadIdx.x, left = n - 1 - i;
+    if (wave * 64 < C && own(threadIdx.x) < C) {  // the weights of the state that enters, and of each step in the one that leaves
+      const int i = own(threadIdx.x), left = n - 1 - i;
       if constexpr (kOut) s_enter[i] = B == 0 || seen(i) == 0 ? s_pw[i + 1 - sh] * a.scale_in : 0.0f;
       const float w = left >= 0 && (B == 0 || seen(i) == total) ? s_pw[left + sh] * a.scale_upd : 0.0f;
       s_leave[i] = w;
@@ -592,11 +594,12 @@ __global__ __launch_bounds__(kThreads, KD <= 128 ? 2 : 1) void attn_sweep_kernel
     }
 
     // this wave's columns of V, contracted over the steps
+    const int value_now = place(value_at), run_now = place(run_at);
     Frag vf[CT][C / CK];
 #pragma unroll
     for (int ct = 0; ct < CT; ++ct)
 #pragma unroll
-      for (int s = 0; s < C / CK; ++s) vf[ct][s] = M::template col<NV>(s_v, value_at, CK * s, 16 * ct);
+      for (int s = 0; s < C / CK; ++s) vf[ct][s] = M::template col<NV>(s_v, value_now, CK * s, 16 * ct);
 
     if constexpr (kOut) {
       // P = W o Q K^T, this wave's tiles, transposed so that a lane holds 4 steps j of a row i
@@ -613,8 +616,8 @@ __global__ __launch_bounds__(kThreads, KD <= 128 ? 2 : 1) void attn_sweep_kernel
         row0[k] = 16 * tile_row(tile);
         col0[k] = 16 * tile_col(tile);
         tiles[k] = f32x4{0, 0, 0, 0};
-        fk[0][k] = M::template run<KD>(s_k, run_at, col0[k], 0);
-        fq[0][k] = M::template run<KD>(s_q, run_at, row0[k], 0);
+        fk[0][k] = M::template run<KD>(s_k, run_now, col0[k], 0);
+        fq[0][k] = M::template run<KD>(s_q, run_now, row0[k], 0);
       }
 #pragma unroll
       for (int kk = 0; kk < KD / CK; ++kk) {
@@ -622,8 +625,8 @@ __global__ __launch_bounds__(kThreads, KD <= 128 ? 2 : 1) void attn_sweep_kernel
 #pragma unroll
         for (int k = 0; k < kMyTiles; ++k) {
           if (kk + 1 < KD / CK) {
-            fk[kk + 1 & 1][k] = M::template run<KD>(s_k, run_at, col0[k], (kk + 1) * CK);
-            fq[kk + 1 & 1][k] = M::template run<KD>(s_q, run_at, row0[k], (kk + 1) * CK);
+            fk[kk + 1 & 1][k] = M::template run<KD>(s_k, run_now, col0[k], (kk + 1) * CK);
+            fq[kk + 1 & 1][k] = M::template run<KD>(s_q, run_now, row0[k], (kk + 1) * CK);
           }
           tiles[k] = M::mma(fk[kk & 1][k], fq[kk & 1][k], tiles[k]);
         }
@@ -671,6 +674,7 @@ __global__ __launch_bounds__(kThreads, KD <= 128 ? 2 : 1) void attn_sweep_kernel
     if constexpr (kOut) {
       const int lane = own(threadIdx.x & 63);
       const f32x4 nil = {0, 0, 0, 0};
+      const int row_now = place(row_at);
       // (Q S)^T: a lane holds 4 value columns of a step.  The next operands are on their way
       // while these are multiplied.
       constexpr int KK = KD / CK;
@@ -678,7 +682,7 @@ __global__ __launch_bounds__(kThreads, KD <= 128 ? 2 : 1) void attn_sweep_kernel
       Parts<T, NS> ps[2][CT], pr[2][kDecay ? CT : 1];
       const auto operands = [&](int kk) {
 #pragma unroll
-        for (int it = 0; it < IT; ++it) fq[kk & 1][it] = M::template row<KD>(s_q, row_at, 16 * it, kk * CK);
+        for (int it = 0; it < IT; ++it) fq[kk & 1][it] = M::template row<KD>(s_q, row_now, 16 * it, kk * CK);
 #pragma unroll
         for (int ct = 0; ct < CT; ++ct) {
           float sv[E], rv[E];
@@ -728,6 +732,7 @@ __global__ __launch_bounds__(kThreads, KD <= 128 ? 2 : 1) void attn_sweep_kernel
             }
         }
         in_order();
+        const int p_now = place(p_at);
         // P V, of the values `of` gives
         const auto product = [&](auto of) {
 #pragma unroll
@@ -735,11 +740,11 @@ __global__ __launch_bounds__(kThreads, KD <= 128 ? 2 : 1) void attn_sweep_kernel
 #pragma unroll
             for (int it = 0; it < IT; ++it) {
               if (CK * s >= 16 * (it + 1)) continue;
-              const Frag fp = M::template row<C>(s_p, p_at, 16 * it, CK * s);
+              const Frag fp = M::template row<C>(s_p, p_now, 16 * it, CK * s);
 #pragma unroll
               for (int ct = 0; ct < CT; ++ct) acc[ct][it] = M::mma(of(vf[ct][s]), fp, acc[ct][it]);
               if constexpr (kLow) {
-                const Frag fl = M::template row<C>(s_p2, p_at, 16 * it, CK * s);
+                const Frag fl = M::template row<C>(s_p2, p_now, 16 * it, CK * s);
 #pragma unroll
                 for (int ct = 0; ct < CT; ++ct) acc[ct][it] = M::mma(of(vf[ct][s]), fl, acc[ct][it]);
               }
@@ -858,6 +863,7 @@ __global__ __launch_bounds__(kThreads, KD <= 128 ? 2 : 1) void attn_sweep_kernel
             S[ct][t][r] *= pass;
             if (PACKED && total != 0) S[ct][t][r] = 0.0f;
           }
+      const int key_now = place(key_at);
       constexpr int TT = 4;  // tiles at a time: products that do not wait for one another
       constexpr int kGroups = KT / TT;
       Parts<T, NU> px[CT], px2[kRate ? CT : 1];
@@ -871,7 +877,7 @@ __global__ __launch_bounds__(kThreads, KD <= 128 ? 2 : 1) void attn_sweep_kernel
         }
 #pragma unroll
         for (int j = 0; j < TT; ++j) {
-          kf[i & 1][j] = M::template col<KD>(s_k, key_at, CK * s, 16 * (t + j));
+          kf[i & 1][j] = M::template col<KD>(s_k, key_now, CK * s, 16 * (t + j));
           if constexpr (PACKED) {
 #pragma unroll
             for (int e = 0; e < E; ++e)
