@@ -210,6 +210,21 @@ struct Mat<float> {
   }
 };
 
+// A fragment's elements whose weights are not 0; the others are 0, NaN or not.
+__device__ __forceinline__ uint4 weighed(const f32x4 (&w)[2]) {  // bf16: 8 halves
+  const auto two = [](float a, float b) { return (a != 0.0f ? 0xffffu : 0u) | (b != 0.0f ? 0xffff0000u : 0u); };
+  return make_uint4(two(w[0][0], w[0][1]), two(w[0][2], w[0][3]), two(w[1][0], w[1][1]), two(w[1][2], w[1][3]));
+}
+__device__ __forceinline__ uint4 weighed(const f32x4 (&w)[1]) {
+  const auto one = [](float a) { return a != 0.0f ? 0xffffffffu : 0u; };
+  return make_uint4(one(w[0][0]), one(w[0][1]), one(w[0][2]), one(w[0][3]));
+}
+template <typename Frag>
+__device__ __forceinline__ Frag only(uint4 mask, const Frag& f) {
+  const uint4 v = __builtin_bit_cast(uint4, f);
+  return __builtin_bit_cast(Frag, make_uint4(v.x & mask.x, v.y & mask.y, v.z & mask.z, v.w & mask.w));
+}
+
 // The step (of CK) that element e of a lane's fragment is, q4 = 4 (lane / 16).
 __device__ __forceinline__ int step_of(int e, int q4) { return 16 * (e / 4) + q4 + e % 4; }
 
@@ -553,6 +568,17 @@ __global__ __launch_bounds__(kThreads, KD <= 128 ? 2 : 1) void attn_sweep_kernel
     }
   }
 
+  // whether a sequence starts between this lane's step and the one before, a chunk ahead
+  const auto starts_at = [&](int u0) {
+    const int u = u0 + (threadIdx.x & 63);
+    int f = 0;
+    if (u < u_end && u < len && (int)(threadIdx.x & 63) < C && !(a.rev && u == 0))
+      f = a.starts[(int64_t)b * L + (a.rev ? len - u : u)];
+    return f;
+  };
+  int starts_here = 0;
+  if constexpr (PACKED) starts_here = starts_at(u_begin);
+
   for (int u0 = u_begin; u0 < u_end; u0 += C) {
     const int n = valid(u0);
     if (n == 0 && MODE != kAttnOut) break;
@@ -566,13 +592,8 @@ __global__ __launch_bounds__(kThreads, KD <= 128 ? 2 : 1) void attn_sweep_kernel
       break;
     }
     // bit i: no state and no product crosses from step i-1 to step i
-    uint64_t B = 0;
-    if constexpr (PACKED) {
-      const int u = u0 + lane;
-      bool f = false;
-      if (lane < n && !(a.rev && u == 0)) f = a.starts[(int64_t)b * L + (a.rev ? len - u : u)] != 0;
-      B = __ballot(f);
-    }
+    const uint64_t B = PACKED ? __ballot(starts_here != 0) : 0;
+    if constexpr (PACKED) starts_here = starts_at(u0 + C);
     const auto seen = [&](int i) { return __popcll(B & (~0ull >> (63 - i))); };  // starts up to and with step i
     const int total = seen(n - 1);
 
@@ -870,21 +891,10 @@ __global__ __launch_bounds__(kThreads, KD <= 128 ? 2 : 1) void attn_sweep_kernel
       Frag kf[2][TT];
       const auto keys = [&](int i) {  // group i: steps CK (i / kGroups), tiles TT (i % kGroups)
         const int s = i / kGroups, t = i % kGroups * TT;
-        f32x4 w[E / 4];
-        if constexpr (PACKED) {
 #pragma unroll
-          for (int e = 0; e < E; e += 4) w[e / 4] = *reinterpret_cast<const f32x4*>(s_leave + CK * s + step_of(e, q4));
-        }
-#pragma unroll
-        for (int j = 0; j < TT; ++j) {
-          kf[i & 1][j] = M::template col<KD>(s_k, key_now, CK * s, 16 * (t + j));
-          if constexpr (PACKED) {
-#pragma unroll
-            for (int e = 0; e < E; ++e)
-              if (w[e / 4][e % 4] == 0.0f) M::zero(kf[i & 1][j], e);
-          }
-        }
+        for (int j = 0; j < TT; ++j) kf[i & 1][j] = M::template col<KD>(s_k, key_now, CK * s, 16 * (t + j));
       };
+      uint4 taken = make_uint4(0, 0, 0, 0);  // packed rows: the steps that reach the state, not even a NaN of the others
       const auto values = [&](int s) {
         f32x4 w[E / 4], w2[E / 4];
 #pragma unroll
@@ -892,18 +902,15 @@ __global__ __launch_bounds__(kThreads, KD <= 128 ? 2 : 1) void attn_sweep_kernel
           w[e / 4] = *reinterpret_cast<const f32x4*>(s_leave + CK * s + step_of(e, q4));
           if constexpr (kRate) w2[e / 4] = *reinterpret_cast<const f32x4*>(s_left + CK * s + step_of(e, q4));
         }
+        if constexpr (PACKED) taken = weighed(w);
 #pragma unroll
         for (int ct = 0; ct < CT; ++ct) {
           float x[E], x2[E];
 #pragma unroll
           for (int e = 0; e < E; ++e) {
-            const float v = M::at(vf[ct][s], e);
+            const float v = M::at(PACKED ? only(taken, vf[ct][s]) : vf[ct][s], e);
             x[e] = v * w[e / 4][e % 4];
             if constexpr (kRate) x2[e] = v * w2[e / 4][e % 4];
-            if (PACKED && w[e / 4][e % 4] == 0.0f) {  // not even a NaN of the steps before the last start
-              x[e] = 0.0f;
-              if constexpr (kRate) x2[e] = 0.0f;
-            }
           }
           px[ct] = parts_of<NU>(x);
           if constexpr (kRate) px2[ct] = parts_of<NU>(x2);
@@ -916,6 +923,10 @@ __global__ __launch_bounds__(kThreads, KD <= 128 ? 2 : 1) void attn_sweep_kernel
         if (t == 0) values(i / kGroups);
         in_order();
         if (i + 1 < kGroups * (C / CK)) keys(i + 1);
+        if constexpr (PACKED) {
+#pragma unroll
+          for (int j = 0; j < TT; ++j) kf[i & 1][j] = only(taken, kf[i & 1][j]);
+        }
 #pragma unroll
         for (int k = 0; k < NU; ++k)
 #pragma unroll
