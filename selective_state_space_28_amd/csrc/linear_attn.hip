@@ -303,8 +303,10 @@ __device__ __forceinline__ Slice slice_of(const AttnView& w, int64_t b, int h, i
 // whose lanes name what belongs there; an offset behind the extent gives zeros.
 // They are under way until a wait for them.  Slices that cannot be read in vectors are
 // copied element by element.
+// (The wait stands for those that the compiler would set: 5 states between a vector
+// instruction that writes a scalar register and the access that reads it, 1 after m0.)
 __device__ __forceinline__ void copy_to_lds(uint32_t to, uint32_t at, u32x4_t buf, uint32_t base) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
                :
                : "s"(__builtin_amdgcn_readfirstlane(to)), "v"(at), "s"(buf),
                  "s"(__builtin_amdgcn_readfirstlane(base))
@@ -312,7 +314,7 @@ __device__ __forceinline__ void copy_to_lds(uint32_t to, uint32_t at, u32x4_t bu
 }
 
 __device__ __forceinline__ void copy_word_to_lds(uint32_t to, uint32_t at, u32x4_t buf) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, 0 offen lds"
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tbuffer_load_dword %1, %2, 0 offen lds"
                :
                : "s"(__builtin_amdgcn_readfirstlane(to)), "v"(at), "s"(buf)
                : "memory", "m0");
@@ -538,18 +540,19 @@ __global__ __launch_bounds__(kThreads, KD <= 128 ? 2 : 1) void attn_sweep_kernel
   T* out = static_cast<T*>(a.out);
   const auto valid = [&](int u) { return min(max(len - u, 0), C); };  // (u is at most seqlen + C, below 2^31)
 
+  const auto there = [&](int u) { return u < u_end && u < len; };
   const auto stage_q = [&](int u) {
-    if (kOut && u < u_end) stage<T, C, KD>(s_q, sq, u, a.kd, valid(u), wave);
+    if (kOut && there(u)) stage<T, C, KD>(s_q, sq, u, a.kd, valid(u), wave);
   };
   const auto stage_k = [&](int u, int into) {
-    if (u < u_end) stage<T, C, KD>(s_keys[into], sk, u, a.kd, valid(u), wave);
+    if (there(u)) stage<T, C, KD>(s_keys[into], sk, u, a.kd, valid(u), wave);
   };
   const auto stage_v = [&](int u) {
-    if (u < u_end) stage<T, C, NV>(s_v, sv, u, vw, valid(u), wave);
+    if (there(u)) stage<T, C, NV>(s_v, sv, u, vw, valid(u), wave);
   };
   const auto stage_dy = [&](int u) {
     if constexpr (kDecay) {
-      if (u < u_end) stage<T, C, NV>(s_dy, sd, u, vw, valid(u), wave);
+      if (there(u)) stage<T, C, NV>(s_dy, sd, u, vw, valid(u), wave);
     }
   };
   stage_k(u_begin, 0);
@@ -953,6 +956,7 @@ __global__ __launch_bounds__(kThreads, KD <= 128 ? 2 : 1) void attn_sweep_kernel
     if (kSegments) cut |= B != 0;
   }
 
+  asm volatile("s_waitcnt vmcnt(0)" : : : "memory");  // no copy to LDS outlives the workgroup
   lane = own(lane);
   m = lane & 15;
   q4 = 4 * (lane >> 4);
