@@ -46,7 +46,7 @@ def _heads_in(q, k, v, log_decay, lead, dev):
         raise ValueError("log_decay must be (heads,)")
     heads, hq, hk, hv, kd, vd = gs[0], qs[-2], ks[-2], vs[-2], qs[-1], vs[-1]
     pg = _in("log_decay", log_decay, gs, _F32, dev)
-    if not (hq == hk == hv == heads and 1 <= kd <= _MAX_WIDTH and 1 <= vd <= _MAX_WIDTH):
+    if not (hq == hk == hv == heads < 2 ** 31 and 1 <= kd <= _MAX_WIDTH and 1 <= vd <= _MAX_WIDTH):
         _int32("heads", heads)
         for name, n in (("q", hq), ("k", hk), ("v", hv)):
             if heads > 0 and (n < 1 or heads % n != 0):

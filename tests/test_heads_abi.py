@@ -227,6 +227,15 @@ def test_attn_reference(packed, padded):
             assert abs(slope - (want[name] * step).sum()) <= 1e-7 * (1 + abs(slope)), name
 
 
+def test_more_heads_than_an_int_holds_are_refused():
+    from selective_state_space_28_amd.heads import _heads_in
+
+    n = 2 ** 32 + 1  # 1, where it is cut to 32 bits
+    q, v = (torch.empty(1, 1, n, 1, device="meta", dtype=torch.bfloat16) for _ in range(2))
+    with pytest.raises(ValueError, match="heads is 4294967297"):
+        _heads_in(q, q, v, torch.empty(n, device="meta"), q.shape[:2], torch.device("meta"))
+
+
 @pytest.mark.parametrize("gate", [False, True])
 @pytest.mark.parametrize("kind", ["none", "silu", "sigmoid"])
 def test_group_reference(gate, kind):
