@@ -1076,12 +1076,14 @@ __global__ __launch_bounds__(256) void attn_gather_kernel(const float* __restric
 }
 
 __global__ __launch_bounds__(64) void attn_decay_sum_kernel(const double* __restrict__ part, float* __restrict__ out,
-                                                            int64_t per) {
-  const double* p = part + (int64_t)blockIdx.x * per;
+                                                            int64_t per, int heads) {
+  const int64_t h = group_index();
+  if (h >= heads) return;
+  const double* p = part + h * per;
   double s = 0.0;
   for (int64_t i = threadIdx.x; i < per; i += 64) s += p[i];
   s = wave_sum(s);
-  if (threadIdx.x == 0) out[blockIdx.x] = (float)s;
+  if (threadIdx.x == 0) out[h] = (float)s;
 }
 
 // One token: S <- e^g S + k v^T, y = scale q S, bound by the state, read and written
@@ -1267,8 +1269,8 @@ hipError_t launch_attn_decay_grad(const AttnSweep& a, const float* dlast, float*
   all.n = 1;
   const hipError_t e = a.dtype == Dtype::BF16 ? run_decay<uint16_t>(all, dlast, stream) : run_decay<float>(all, dlast, stream);
   if (e != hipSuccess) return e;
-  attn_decay_sum_kernel<<<a.heads, 64, 0, stream>>>(a.part, dlog_decay,
-                                                    (int64_t)a.batch * attn_decay_blocks(a.vd) * a.nseg);
+  attn_decay_sum_kernel<<<grid_of(a.heads, 64), 64, 0, stream>>>(
+      a.part, dlog_decay, (int64_t)a.batch * attn_decay_blocks(a.vd) * a.nseg, a.heads);
   return hipGetLastError();
 }
 
