@@ -26,7 +26,8 @@
  *    projection's output are read where they lie.  NULL -> contiguous.  Not
  *    negative, at most 2^40, SSM_ERR_SHAPE otherwise.  Everything else is contiguous.
  *  - Pointers need their element's alignment only; where q, k or v is aligned to 16
- *    bytes with all its strides it is read 16 bytes at a time.
+ *    bytes with all its strides and its width it is read 16 bytes at a time, and 4
+ *    where they are aligned to 4.
  *  - starts: (batch, seqlen) bytes, not 0 at the first step of each sequence
  *    packed into a row (a row may begin in the middle of one).  No state, no
  *    gradient and no NaN or Inf crosses a start.  NULL -> none.
