@@ -80,8 +80,8 @@ struct AttnStep {
 };
 
 hipError_t launch_attn_sweeps(const AttnSweeps& all, hipStream_t stream);
-// dlog_decay (heads) += over batch and steps; a.q, a.k, a.v as in the forward sweep, a.dy the gradient, a.state_out
-// the gradient of the last state (nullable).
+// dlog_decay (heads): the sum over batch and steps; a.q, a.k, a.v as in the forward sweep, a.dy the gradient of its
+// output, dlast that of its last state (nullable).
 hipError_t launch_attn_decay_grad(const AttnSweep& a, const float* dlast, float* dlog_decay, hipStream_t stream);
 // out (batch, seqlen, n, width) of part (batch, seqlen, heads, width): the sum over the heads / n that share a head.
 hipError_t launch_attn_gather(const float* part, void* out, int64_t rows, int heads, int n, int width, Dtype dtype,
