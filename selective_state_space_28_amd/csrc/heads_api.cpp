@@ -81,15 +81,15 @@ struct SweepBytes {
   size_t all() const { return state + through + rate + steps + part; }
 };
 
-// The segments of n sweeps side by side.
-AttnSplit split_of(const AttnSizes& s, int blocks, int n) {
+// The segments of n sweeps side by side; of the decay's gradient two states each.
+AttnSplit split_of(const AttnSizes& s, int blocks, int n, bool decay, int dtype) {
   const int64_t heads = (int64_t)n * s.batch * s.heads;
-  return attn_split(heads * blocks, s.seqlen, heads * s.kd * s.vd);
+  return attn_split(heads * blocks, s.seqlen, heads * s.kd * s.vd * (decay ? 2 : 1), dtype_of(dtype));
 }
 
-SweepBytes sweep_bytes(const AttnSizes& s, int blocks, int n, bool decay) {
+SweepBytes sweep_bytes(const AttnSizes& s, int blocks, int n, bool decay, int dtype) {
   SweepBytes w{};
-  const AttnSplit sp = split_of(s, blocks, n);
+  const AttnSplit sp = split_of(s, blocks, n, decay, dtype);
   const size_t segs = (size_t)s.batch * (size_t)s.heads * (size_t)sp.nseg;
   if (sp.nseg > 1) {
     w.state = round256(segs * (size_t)s.kd * (size_t)s.vd * 4);
@@ -113,13 +113,13 @@ struct BwdBytes {
 
 int sweeps_together(const AttnSizes& s) { return attn_alike(s.kd, s.vd) ? 3 : 2; }
 
-BwdBytes bwd_bytes(const AttnSizes& s) {
+BwdBytes bwd_bytes(const AttnSizes& s, int dtype) {
   const size_t steps = (size_t)s.batch * (size_t)s.seqlen * (size_t)s.heads * 4;
   const int n = sweeps_together(s);
   BwdBytes w{};
-  for (const size_t b : {(size_t)n * sweep_bytes(s, attn_column_blocks(s.kd), n, false).all(),
-                         n == 3 ? (size_t)0 : sweep_bytes(s, attn_column_blocks(s.vd), 1, false).all(),
-                         sweep_bytes(s, attn_decay_blocks(s.vd), 1, true).all()})
+  for (const size_t b : {(size_t)n * sweep_bytes(s, attn_column_blocks(s.kd), n, false, dtype).all(),
+                         n == 3 ? (size_t)0 : sweep_bytes(s, attn_column_blocks(s.vd), 1, false, dtype).all(),
+                         sweep_bytes(s, attn_decay_blocks(s.vd), 1, true, dtype).all()})
     w.sweep = w.sweep > b ? w.sweep : b;
   if (s.hq != s.heads) w.dq = round256(steps * (size_t)s.kd);
   if (s.hk != s.heads) w.dk = round256(steps * (size_t)s.kd);
@@ -132,8 +132,8 @@ AttnSweep attn_sweep(const AttnSizes& s, const float* g, const uint8_t* starts, 
                      int vd, void* workspace, int k, int n, bool decay = false) {
   AttnSweep a{};
   const int blocks = decay ? attn_decay_blocks(vd) : attn_column_blocks(vd);
-  const AttnSplit sp = split_of(s, blocks, n);
-  const SweepBytes w = sweep_bytes(s, blocks, n, decay);
+  const AttnSplit sp = split_of(s, blocks, n, decay, dtype);
+  const SweepBytes w = sweep_bytes(s, blocks, n, decay, dtype);
   a.kd = kd;
   a.vd = vd;
   a.batch = s.batch;
@@ -197,7 +197,7 @@ extern "C" {
 size_t ssm_linear_attn_fwd_workspace_bytes(int batch, int64_t seqlen, int heads, int key_dim, int value_dim, int dtype) {
   const AttnSizes s{batch, seqlen, heads, 1, 1, 1, key_dim, value_dim};
   if (!dtype_ok(dtype) || !attn_shape_ok(s) || batch == 0 || heads == 0 || seqlen == 0) return 0;
-  return sweep_bytes(s, attn_column_blocks(value_dim), 1, false).all();
+  return sweep_bytes(s, attn_column_blocks(value_dim), 1, false, dtype).all();
 }
 
 int ssm_linear_attn_fwd(const void* q, const void* k, const void* v, const int64_t* strides, const float* log_decay,
@@ -222,7 +222,7 @@ int ssm_linear_attn_fwd(const void* q, const void* k, const void* v, const int64
       !aligned(lengths, 4) || !aligned(h0, 4) || !aligned(last_state, 4) || !aligned(workspace, 256))
     return SSM_ERR_ALIGN;
   if (none) return SSM_OK;
-  const size_t need = empty ? 0 : sweep_bytes(s, attn_column_blocks(value_dim), 1, false).all();
+  const size_t need = empty ? 0 : sweep_bytes(s, attn_column_blocks(value_dim), 1, false, dtype).all();
   if (need > 0 && (workspace == nullptr || workspace_bytes < need)) return SSM_ERR_WORKSPACE;
   const size_t rows = (size_t)batch * (size_t)seqlen;
   const size_t state = (size_t)batch * (size_t)heads * (size_t)key_dim * (size_t)value_dim * 4;
@@ -260,7 +260,7 @@ size_t ssm_linear_attn_bwd_workspace_bytes(int batch, int64_t seqlen, int heads,
                                            int key_dim, int value_dim, int dtype) {
   const AttnSizes s{batch, seqlen, heads, q_heads, k_heads, v_heads, key_dim, value_dim};
   if (!dtype_ok(dtype) || !attn_shape_ok(s) || batch == 0 || heads == 0 || seqlen == 0) return 0;
-  return bwd_bytes(s).all();
+  return bwd_bytes(s, dtype).all();
 }
 
 int ssm_linear_attn_bwd(const void* q, const void* k, const void* v, const int64_t* strides, const float* log_decay,
@@ -288,7 +288,7 @@ int ssm_linear_attn_bwd(const void* q, const void* k, const void* v, const int64
       !aligned(dlog_decay, 4) || !aligned(dh0, 4) || !aligned(workspace, 256))
     return SSM_ERR_ALIGN;
   if (heads == 0) return SSM_OK;
-  const BwdBytes w = empty ? BwdBytes{} : bwd_bytes(s);
+  const BwdBytes w = empty ? BwdBytes{} : bwd_bytes(s, dtype);
   const size_t need = w.all();
   if (need > 0 && (workspace == nullptr || workspace_bytes < need)) return SSM_ERR_WORKSPACE;
   const size_t rows = (size_t)batch * (size_t)seqlen;

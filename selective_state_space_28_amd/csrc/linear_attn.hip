@@ -1227,22 +1227,24 @@ int attn_column_blocks(int vd) { return (vd + 64 * column_tiles(vd) - 1) / (64 *
 int attn_decay_blocks(int vd) { return (vd + 63) / 64; }
 
 // Workgroups and segments.  A sweep of one chunk after another takes a time that a CU's
-// two workgroups share only in part (bf16, heads of 128, microseconds a chunk): 5.4 where
-// half the CUs have one, 6.3 with one on each, 8.9 with two.  Segments fill the CUs, and
-// cost the pass that finds their states (0.58 of the main one's time) with two more launches
-// and the states' traffic, some 20 us and more.  The least of these sums is taken, of
-// up to 64 segments of 4 chunks and more (batch 8, L 2048 bf16: 16 heads 173 us in one
-// piece, 133 in segments; 32 heads 202 and 244).
-AttnSplit attn_split(int64_t groups, int64_t seqlen, int64_t state_elements) {
+// two workgroups share only in part (bf16, heads of 128, microseconds for 64 steps): 5.4 where
+// half the CUs have one, 6.3 with one on each, 8.9 with two; float32, on its own matrix
+// cores, 2.4 times as much.  Segments fill the CUs, and cost the pass that finds their states
+// (0.58 of the main one's time) with two more launches and the states' traffic, some 20 us and
+// more.  The least of these sums is taken, of up to 64 segments (batch 8, L 2048 bf16: 16 heads
+// 173 us in one piece, 133 in segments; 32 heads 202 and 244; one row of 512 steps, 12 heads,
+// float32: 107 and 40).
+AttnSplit attn_split(int64_t groups, int64_t seqlen, int64_t state_elements, Dtype dtype) {
   const int64_t chunks = (seqlen + kAttnChunk - 1) / kAttnChunk;
-  const auto rounds = [](int64_t g) {
+  const double slower = dtype == Dtype::F32 ? 2.4 : 1.0;
+  const auto rounds = [&](int64_t g) {
     const int64_t left = g % 512;
-    return 8.9 * (double)(g / 512) + (left == 0 ? 0.0 : left <= 128 ? 5.4 : left <= 256 ? 6.3 : 8.9);
+    return slower * (8.9 * (double)(g / 512) + (left == 0 ? 0.0 : left <= 128 ? 5.4 : left <= 256 ? 6.3 : 8.9));
   };
   AttnSplit best{1, (chunks > 0 ? chunks : 1) * kAttnChunk};
   if (groups <= 0) return best;
   double least = (double)chunks * rounds(groups);
-  for (int64_t n = 2; n <= 64 && 4 * n <= chunks; ++n) {
+  for (int64_t n = 2; n <= 64 && n <= chunks; ++n) {
     const int64_t per = (chunks + n - 1) / n, nseg = (chunks + per - 1) / per;
     const double states = 16e-6 / 4.0 * (double)state_elements * (double)nseg;  // four passes of float32 at 4 TB/s
     const double t = (double)per * (rounds(groups * nseg) + 0.58 * rounds(groups * (nseg - 1))) + 20.0 + states;

@@ -62,7 +62,7 @@ struct AttnSplit {
   int nseg;
   int64_t seglen;
 };
-AttnSplit attn_split(int64_t groups, int64_t seqlen, int64_t state_elements);
+AttnSplit attn_split(int64_t groups, int64_t seqlen, int64_t state_elements, Dtype dtype);
 // Blocks of value columns, of a sweep and of the decay's gradient.
 int attn_column_blocks(int vd);
 int attn_decay_blocks(int vd);
