@@ -29,7 +29,8 @@
 // Roundings with bf16 storage.  P is rounded to bf16 once, as the operand that meets V; its
 // sums are float32.  The decayed v, whose products with k make the float32 state, goes
 // in three parts, which is exact; S as it meets q in two (2^-16): with one, and its 2^-9 in
-// every output, the kernel takes 295 us for 326, which was not taken.
+// every output, the kernel takes 295 us for 326, which was not taken.  The decay's
+// gradient, a float32 output, has P, S and R in three parts each.
 #include "linear_attn.hpp"
 #include "runs.hpp"
 #include "ssm_math.hpp"
@@ -424,16 +425,16 @@ __global__ __launch_bounds__(kThreads, KD <= 128 ? 2 : 1) void attn_sweep_kernel
   constexpr bool kDecay = MODE == kAttnDecay, kOut = !kSegments;
   constexpr bool kRate = kDecay || MODE == kAttnDecaySegments;  // R beside S
   constexpr int NU = sizeof(T) == 2 ? 3 : 1;  // parts of the decayed v, exact
-  constexpr int NS = sizeof(T) == 2 ? 2 : 1;  // parts of S as an operand, to 2^-16
+  constexpr int NS = sizeof(T) == 2 ? kDecay ? 3 : 2 : 1;  // parts of S as an operand, exact or to 2^-16
   constexpr int kTiles = IT * (IT + 1) / 2;   // of P, on and below the diagonal
   constexpr int kMyTiles = (kTiles + kWaves - 1) / kWaves;
-  constexpr bool kLow = kDecay && sizeof(T) == 2;  // P in two parts
+  constexpr bool kLow = kDecay && sizeof(T) == 2;  // P in three parts, exact: dg is float32
 
   __shared__ __attribute__((aligned(16))) T s_q[kOut ? C * KD : 1];
   __shared__ __attribute__((aligned(16))) T s_keys[2][C * KD];
   __shared__ __attribute__((aligned(16))) T s_v[C * NV];
   __shared__ __attribute__((aligned(16))) T s_p[kOut ? C * C : 1];
-  __shared__ __attribute__((aligned(16))) T s_p2[kLow ? C * C : 1];
+  __shared__ __attribute__((aligned(16))) T s_low[kLow ? 2 : 1][kLow ? C * C : 1];
   __shared__ __attribute__((aligned(16))) T s_dy[kDecay ? C * NV : 1];
   __shared__ float s_pw[C + 1];
   __shared__ __attribute__((aligned(16))) float s_enter[C], s_leave[C], s_left[kRate ? C : 1];
@@ -525,7 +526,7 @@ __global__ __launch_bounds__(kThreads, KD <= 128 ? 2 : 1) void attn_sweep_kernel
   if constexpr (kOut) {  // the masked halves of pairs of tiles stay zero
     for (int i = threadIdx.x; i < C * C; i += kThreads) {
       s_p[i] = (T)0;
-      if constexpr (kLow) s_p2[i] = (T)0;
+      if constexpr (kLow) s_low[0][i] = s_low[1][i] = (T)0;
     }
   }
   double dg = 0.0;
@@ -684,14 +685,19 @@ __global__ __launch_bounds__(kThreads, KD <= 128 ? 2 : 1) void attn_sweep_kernel
         const int dst = Tile<T, C>::at(i, 16 * jt + q4);
         if constexpr (sizeof(T) == 2) {
           if constexpr (kLow) {
-            float lo[4];
 #pragma unroll
-            for (int r = 0; r < 4; ++r) {
-              const float hi = cut16(p[r]);
-              lo[r] = p[r] - hi;
-              p[r] = hi;
+            for (int part = 0; part < 2; ++part) {
+              float lo[4];
+#pragma unroll
+              for (int r = 0; r < 4; ++r) {
+                lo[r] = p[r] - cut16(p[r]);
+                if (part == 0) lo[r] = cut16(lo[r]);
+                else lo[r] -= cut16(lo[r]);
+              }
+              *reinterpret_cast<uint2*>(s_low[part] + dst) = make_uint2(pack_bf16x2(lo[0], lo[1]), pack_bf16x2(lo[2], lo[3]));
             }
-            *reinterpret_cast<uint2*>(s_p2 + dst) = make_uint2(pack_bf16x2(lo[0], lo[1]), pack_bf16x2(lo[2], lo[3]));
+#pragma unroll
+            for (int r = 0; r < 4; ++r) p[r] = cut16(p[r]);
           }
           *reinterpret_cast<uint2*>(s_p + dst) = make_uint2(pack_bf16x2(p[0], p[1]), pack_bf16x2(p[2], p[3]));
         } else {
@@ -780,9 +786,12 @@ __global__ __launch_bounds__(kThreads, KD <= 128 ? 2 : 1) void attn_sweep_kernel
 #pragma unroll
               for (int ct = 0; ct < CT; ++ct) acc[ct][it] = M::mma(of(vf[ct][s]), fp, acc[ct][it]);
               if constexpr (kLow) {
-                const Frag fl = M::template row<C>(s_p2, p_now, 16 * it, CK * s);
 #pragma unroll
-                for (int ct = 0; ct < CT; ++ct) acc[ct][it] = M::mma(of(vf[ct][s]), fl, acc[ct][it]);
+                for (int part = 0; part < 2; ++part) {
+                  const Frag fl = M::template row<C>(s_low[part], p_now, 16 * it, CK * s);
+#pragma unroll
+                  for (int ct = 0; ct < CT; ++ct) acc[ct][it] = M::mma(of(vf[ct][s]), fl, acc[ct][it]);
+                }
               }
             }
         };

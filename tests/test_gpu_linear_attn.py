@@ -294,3 +294,21 @@ def test_same_bits_again(dev):
     a, b = check(p, "bf16", 300), check(p, "bf16", 300)
     for name in a:
         assert torch.equal(a[name], b[name]), name
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("apart", [1, 40, 65, 140])
+def test_decay_gradient_is_float32(dev, dtype, apart):
+    """One key and one query, `apart` steps from one another: the gradient is apart e^(g apart) scale q k v dy, a product
+    without a sum.  16 half steps of float32 for the decays of each 32 steps (as above), 16 for the products and the scale."""
+    import selective_state_space_28_amd as ssm
+    gen = torch.Generator().manual_seed(17 + apart)
+    heads, L = 64, apart + 1
+    q, k, v, dy = (torch.zeros(1, L, heads, 1, dtype=ref.TYPES[dtype]) for _ in range(4))
+    g = -0.05 * torch.rand(heads, generator=gen)
+    want = apart * 0.75 * torch.exp(apart * g.double())
+    for t, at in ((q, apart), (k, 0), (v, 0), (dy, apart)):
+        t[0, at, :, 0] = (1 + torch.rand(heads, generator=gen)).to(t.dtype)
+        want = want * t[0, at, :, 0].double()
+    got = ssm.ssm_linear_attn_bwd(*(t.to(dev) for t in (q, k, v)), g.to(dev), scale=0.75, dy=dy.to(dev))["dlog_decay"]
+    ref.within(got, want, (16 * (L // 32 + 1) + 16) * ref.EPS32 * want.abs(), "dlog_decay")
