@@ -37,7 +37,8 @@
  *    none).  NULL -> seqlen.
  *  - The state, the sums and the decays are held in float32; with bf16 storage the
  *    products q_t . k_s are rounded to bf16 once, after their decay, to meet v
- *    on the matrix cores, and the state meets q in two parts (2^-16).
+ *    on the matrix cores, and the state meets q in two parts (2^-16); in dlog_decay
+ *    both are exact.
  *  - log_decay is not checked for sign; a positive one grows.  -inf forgets all but
  *    the step itself.  A decay over many steps that underflows is held at the
  *    smallest normal float where log_decay > -87, so a state that is not finite
