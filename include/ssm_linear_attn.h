@@ -36,9 +36,8 @@
  *    there are 0, and last_state is that of the row's last step (h0 where it has
  *    none).  NULL -> seqlen.
  *  - The state, the sums and the decays are held in float32; with bf16 storage the
- *    products q_t . k_s are rounded to bf16 once, after their decay, to meet v
- *    on the matrix cores, and the state meets q in two parts (2^-16); in dlog_decay
- *    both are exact.
+ *    decayed products q_t . k_s as they meet v on the matrix cores, and the state as
+ *    it meets q, are two bf16 parts (2^-16 of each); in dlog_decay both are exact.
  *  - log_decay is not checked for sign; a positive one grows.  -inf forgets all but
  *    the step itself.  A decay over many steps that underflows is held at the
  *    smallest normal float where log_decay > -87, so a state that is not finite

@@ -26,10 +26,9 @@
 // decay of S), matrix cores 0.34, LDS 0.30.  8 waves of 16 columns, four to a SIMD, spill or
 // read LDS twice as often: 385 us for 327.
 //
-// Roundings with bf16 storage.  P is rounded to bf16 once, as the operand that meets V; its
-// sums are float32.  The decayed v, whose products with k make the float32 state, goes
-// in three parts, which is exact; S as it meets q in two (2^-16): with one, and its 2^-9 in
-// every output, the kernel takes 295 us for 326, which was not taken.  The decay's
+// Roundings with bf16 storage.  The decayed v, whose products with k make the float32
+// state, goes in three parts, which is exact.  P as it meets V, and S as it meets q, go in
+// two (2^-16): one part, rounded, would leave its 2^-9 in every output.  The decay's
 // gradient, a float32 output, has P, S and R in three parts each.
 #include "linear_attn.hpp"
 #include "runs.hpp"
@@ -244,6 +243,11 @@ __device__ __forceinline__ int step_of(int e, int q4) { return 16 * (e / 4) + q4
 // 2^-16.  (Of an infinite value the rest is NaN, and so is what it meets.)
 __device__ __forceinline__ float cut16(float v) { return __uint_as_float(__float_as_uint(v) & 0xffff0000u); }
 
+// the upper halves of both, a's below: one instruction
+__device__ __forceinline__ uint32_t upper_halves(float a, float b) {
+  return __builtin_amdgcn_perm(__float_as_uint(b), __float_as_uint(a), 0x07060302u);
+}
+
 template <typename T, int N>
 struct Parts {
   typename Mat<T>::Frag f[N];
@@ -258,8 +262,8 @@ __device__ __forceinline__ Parts<uint16_t, N> parts_of(const float (&x)[8]) {
 #pragma unroll
     for (int k = 0; k < N; ++k) {
       bf16x2 hi = {(__bf16)v0, (__bf16)v1};
-      if (k + 1 < N) {  // the upper halves of both, one instruction
-        hi = __builtin_bit_cast(bf16x2, __builtin_amdgcn_perm(__float_as_uint(v1), __float_as_uint(v0), 0x07060302u));
+      if (k + 1 < N) {
+        hi = __builtin_bit_cast(bf16x2, upper_halves(v0, v1));
         v0 -= cut16(v0);
         v1 -= cut16(v1);
       }
@@ -395,6 +399,23 @@ struct StateAt {
 
 }  // namespace
 
+// Where the parts of P lie in LDS, each a tile of 64 columns: of bf16 the upper two of four
+// blocks of 16 rows have 32 columns that are read, so two parts of them lie side by side, 32
+// rows high, and the lower two blocks' parts below those.  (12 KiB for two parts: a CU keeps two
+// workgroups at key and value heads of 128.)
+template <typename T, int PARTS>
+struct ScoreTiles {
+  static constexpr int C = Mat<T>::C;
+  static constexpr int kHalf = 32 * C, kUpper = (PARTS + 1) / 2;
+  static constexpr int kSize = sizeof(T) == 2 ? (kUpper + PARTS) * kHalf : C * C;
+  // the first row of a row block, and the first column
+  __device__ __forceinline__ static int rows(int part, int it) {
+    if (sizeof(T) == 4) return it * 16 * C;
+    return it < 2 ? part / 2 * kHalf + it * 16 * C : (kUpper + part) * kHalf + (it - 2) * 16 * C;
+  }
+  __device__ __forceinline__ static int column(int part, int it) { return sizeof(T) == 2 && it < 2 ? 32 * (part & 1) : 0; }
+};
+
 // Tiles of P on and below the diagonal, row by row: 2 bits of each one's row and column.
 __device__ __forceinline__ int tile_row(int tile) { return (0xffa94 >> (2 * tile)) & 3; }
 __device__ __forceinline__ int tile_col(int tile) { return (0xe4910 >> (2 * tile)) & 3; }
@@ -428,13 +449,13 @@ __global__ __launch_bounds__(kThreads, KD <= 128 ? 2 : 1) void attn_sweep_kernel
   constexpr int NS = sizeof(T) == 2 ? kDecay ? 3 : 2 : 1;  // parts of S as an operand, exact or to 2^-16
   constexpr int kTiles = IT * (IT + 1) / 2;   // of P, on and below the diagonal
   constexpr int kMyTiles = (kTiles + kWaves - 1) / kWaves;
-  constexpr bool kLow = kDecay && sizeof(T) == 2;  // P in three parts, exact: dg is float32
+  constexpr int NP = NS;                      // parts of P, as S's
+  using Scores = ScoreTiles<T, NP>;
 
   __shared__ __attribute__((aligned(16))) T s_q[kOut ? C * KD : 1];
   __shared__ __attribute__((aligned(16))) T s_keys[2][C * KD];
   __shared__ __attribute__((aligned(16))) T s_v[C * NV];
-  __shared__ __attribute__((aligned(16))) T s_p[kOut ? C * C : 1];
-  __shared__ __attribute__((aligned(16))) T s_low[kLow ? 2 : 1][kLow ? C * C : 1];
+  __shared__ __attribute__((aligned(16))) T s_p[kOut ? Scores::kSize : 1];
   __shared__ __attribute__((aligned(16))) T s_dy[kDecay ? C * NV : 1];
   __shared__ float s_pw[C + 1];
   __shared__ __attribute__((aligned(16))) float s_enter[C], s_leave[C], s_left[kRate ? C : 1];
@@ -524,10 +545,7 @@ __global__ __launch_bounds__(kThreads, KD <= 128 ? 2 : 1) void attn_sweep_kernel
         }
   }
   if constexpr (kOut) {  // the masked halves of pairs of tiles stay zero
-    for (int i = threadIdx.x; i < C * C; i += kThreads) {
-      s_p[i] = (T)0;
-      if constexpr (kLow) s_low[0][i] = s_low[1][i] = (T)0;
-    }
+    for (int i = threadIdx.x; i < Scores::kSize; i += kThreads) s_p[i] = (T)0;
   }
   double dg = 0.0;
   bool cut = false;
@@ -682,26 +700,20 @@ __global__ __launch_bounds__(kThreads, KD <= 128 ? 2 : 1) void attn_sweep_kernel
           if (PACKED && B != 0) kept = kept && seen(i) == seen(16 * jt + q4 + r);
           p[r] = kept ? acc[r] * wp[k][r] : 0.0f;
         }
-        const int dst = Tile<T, C>::at(i, 16 * jt + q4);
         if constexpr (sizeof(T) == 2) {
-          if constexpr (kLow) {
 #pragma unroll
-            for (int part = 0; part < 2; ++part) {
-              float lo[4];
+          for (int part = 0; part < NP; ++part) {
+            T* to = s_p + Scores::rows(part, it) + Tile<T, C>::at(m, Scores::column(part, it) + 16 * jt + q4);
+            uint2 w = make_uint2(pack_bf16x2(p[0], p[1]), pack_bf16x2(p[2], p[3]));
+            if (part + 1 < NP) {  // the upper halves, and what they leave
+              w = make_uint2(upper_halves(p[0], p[1]), upper_halves(p[2], p[3]));
 #pragma unroll
-              for (int r = 0; r < 4; ++r) {
-                lo[r] = p[r] - cut16(p[r]);
-                if (part == 0) lo[r] = cut16(lo[r]);
-                else lo[r] -= cut16(lo[r]);
-              }
-              *reinterpret_cast<uint2*>(s_low[part] + dst) = make_uint2(pack_bf16x2(lo[0], lo[1]), pack_bf16x2(lo[2], lo[3]));
+              for (int r = 0; r < 4; ++r) p[r] -= cut16(p[r]);
             }
-#pragma unroll
-            for (int r = 0; r < 4; ++r) p[r] = cut16(p[r]);
+            *reinterpret_cast<uint2*>(to) = w;
           }
-          *reinterpret_cast<uint2*>(s_p + dst) = make_uint2(pack_bf16x2(p[0], p[1]), pack_bf16x2(p[2], p[3]));
         } else {
-          *reinterpret_cast<f32x4*>(s_p + dst) = f32x4{p[0], p[1], p[2], p[3]};
+          *reinterpret_cast<f32x4*>(s_p + Tile<T, C>::at(i, 16 * jt + q4)) = f32x4{p[0], p[1], p[2], p[3]};
         }
       }
     }
@@ -782,16 +794,12 @@ __global__ __launch_bounds__(kThreads, KD <= 128 ? 2 : 1) void attn_sweep_kernel
 #pragma unroll
             for (int it = 0; it < IT; ++it) {
               if (CK * s >= 16 * (it + 1)) continue;
-              const Frag fp = M::template row<C>(s_p, p_now, 16 * it, CK * s);
 #pragma unroll
-              for (int ct = 0; ct < CT; ++ct) acc[ct][it] = M::mma(of(vf[ct][s]), fp, acc[ct][it]);
-              if constexpr (kLow) {
+              for (int part = 0; part < NP; ++part) {
+                const Frag fp =
+                    M::template row<C>(s_p + Scores::rows(part, it), p_now, 0, Scores::column(part, it) + CK * s);
 #pragma unroll
-                for (int part = 0; part < 2; ++part) {
-                  const Frag fl = M::template row<C>(s_low[part], p_now, 16 * it, CK * s);
-#pragma unroll
-                  for (int ct = 0; ct < CT; ++ct) acc[ct][it] = M::mma(of(vf[ct][s]), fl, acc[ct][it]);
-                }
+                for (int ct = 0; ct < CT; ++ct) acc[ct][it] = M::mma(of(vf[ct][s]), fp, acc[ct][it]);
               }
             }
         };
