@@ -39,13 +39,14 @@
  *    decayed products q_t . k_s as they meet v on the matrix cores, and the state as
  *    it meets q, are two bf16 parts (2^-16 of each); in dlog_decay both are exact.
  *  - log_decay is not checked for sign; a positive one grows.  -inf forgets all but
- *    the step itself.  A decay over many steps that underflows is held at the
- *    smallest normal float where log_decay > -87, so a state that is not finite
- *    stays so until the next start.
- *  - What a NaN or Inf reaches by the formula is NaN or Inf (which of them, where
- *    infinities of both signs meet, depends on the order of the sums); earlier
- *    steps, sequences of their own, other heads and, of v, other columns are what
- *    they were.
+ *    the step itself, of finite values.  A decay over many steps that underflows is
+ *    held at the smallest normal float where log_decay > -87; a state that is not
+ *    finite stays so until the next start, whatever the decay.
+ *  - What a NaN or Inf reaches by the formula is not finite.  An Inf may be NaN there:
+ *    the factors of a product are taken in parts, Inf - Inf one of them, and a value
+ *    that is not finite makes the later y of its chunk NaN.  Earlier steps, sequences of
+ *    their own, other heads and, of v, other columns are what they were.
+ *    (dlog_decay is a sum over its head's whole rows: any of them may make it NaN.)
  */
 #ifndef SSM_LINEAR_ATTN_H
 #define SSM_LINEAR_ATTN_H

@@ -220,13 +220,18 @@ struct Mat<float> {
   }
 };
 
-// A fragment's elements whose weights are not 0; the others are 0, NaN or not.
+// The weight of what does not reach is +0, and of what does, however small, another: -0 where
+// the product has underflowed.  (A NaN that such a decay meets stays one.)
+__device__ __forceinline__ float reaching(float w) { return w == 0.0f ? -0.0f : w; }
+__device__ __forceinline__ bool reaches(float w) { return __float_as_uint(w) != 0; }
+
+// A fragment's elements that reach; the others are 0, NaN or not.
 __device__ __forceinline__ uint4 weighed(const f32x4 (&w)[2]) {  // bf16: 8 halves
-  const auto two = [](float a, float b) { return (a != 0.0f ? 0xffffu : 0u) | (b != 0.0f ? 0xffff0000u : 0u); };
+  const auto two = [](float a, float b) { return (reaches(a) ? 0xffffu : 0u) | (reaches(b) ? 0xffff0000u : 0u); };
   return make_uint4(two(w[0][0], w[0][1]), two(w[0][2], w[0][3]), two(w[1][0], w[1][1]), two(w[1][2], w[1][3]));
 }
 __device__ __forceinline__ uint4 weighed(const f32x4 (&w)[1]) {
-  const auto one = [](float a) { return a != 0.0f ? 0xffffffffu : 0u; };
+  const auto one = [](float a) { return reaches(a) ? 0xffffffffu : 0u; };
   return make_uint4(one(w[0][0]), one(w[0][1]), one(w[0][2]), one(w[0][3]));
 }
 template <typename Frag>
@@ -420,6 +425,9 @@ struct ScoreTiles {
 __device__ __forceinline__ int tile_row(int tile) { return (0xffa94 >> (2 * tile)) & 3; }
 __device__ __forceinline__ int tile_col(int tile) { return (0xe4910 >> (2 * tile)) & 3; }
 
+// What a segment leaves of the state that enters it where a sequence starts in it: nothing.
+constexpr float kCut = -1.0f;
+
 enum AttnMode { kAttnOut = 0, kAttnSegments = 1, kAttnDecay = 2, kAttnDecaySegments = 3 };
 
 // One workgroup: kWaves waves, CT tiles of 16 value columns each.  kAttnSegments: only
@@ -596,8 +604,8 @@ __global__ __launch_bounds__(kThreads, KD <= 128 ? 2 : 1) void attn_sweep_kernel
       const int apart = 16 * (tile_row(tile) - tile_col(tile)) + m - q4;
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
-        wp[k][r] = apart >= r ? decay_pow(g, (float)(apart - r)) * a.scale_p : 0.0f;
-        if (kDecay) wp[k][r] *= (float)(apart - r);
+        const float n = (float)(apart - r);
+        wp[k][r] = apart >= (kDecay ? r + 1 : r) ? reaching(decay_pow(g, n) * a.scale_p * (kDecay ? n : 1.0f)) : 0.0f;
       }
     }
   }
@@ -642,8 +650,8 @@ __global__ __launch_bounds__(kThreads, KD <= 128 ? 2 : 1) void attn_sweep_kernel
     stage_k(u0 + C, turn);
     if (wave * 64 < C && own(threadIdx.x) < C) {  // the weights of the state that enters, and of each step in the one that leaves
       const int i = own(threadIdx.x), left = n - 1 - i;
-      if constexpr (kOut) s_enter[i] = B == 0 || seen(i) == 0 ? s_pw[i + 1 - sh] * a.scale_in : 0.0f;
-      const float w = left >= 0 && (B == 0 || seen(i) == total) ? s_pw[left + sh] * a.scale_upd : 0.0f;
+      if constexpr (kOut) s_enter[i] = B == 0 || seen(i) == 0 ? reaching(s_pw[i + 1 - sh] * a.scale_in) : 0.0f;
+      const float w = left >= 0 && (B == 0 || seen(i) == total) ? reaching(s_pw[left + sh] * a.scale_upd) : 0.0f;
       s_leave[i] = w;
       if constexpr (kRate) s_left[i] = w * (float)left;
     }
@@ -696,7 +704,7 @@ __global__ __launch_bounds__(kThreads, KD <= 128 ? 2 : 1) void attn_sweep_kernel
         float p[4];
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-          bool kept = wp[k][r] != 0.0f;
+          bool kept = reaches(wp[k][r]);
           if (PACKED && B != 0) kept = kept && seen(i) == seen(16 * jt + q4 + r);
           p[r] = kept ? acc[r] * wp[k][r] : 0.0f;
         }
@@ -782,7 +790,7 @@ __global__ __launch_bounds__(kThreads, KD <= 128 ? 2 : 1) void attn_sweep_kernel
             for (int r = 0; r < 4; ++r) {
               float o = acc[ct][it][r];
               if constexpr (kDecay) o = __builtin_fmaf(o, (float)(i + 1), acc_r[ct][it][r]);
-              acc[ct][it][r] = PACKED && w == 0.0f ? 0.0f : o * w;
+              acc[ct][it][r] = PACKED && !reaches(w) ? 0.0f : o * w;
             }
         }
         in_order();
@@ -980,7 +988,7 @@ __global__ __launch_bounds__(kThreads, KD <= 128 ? 2 : 1) void attn_sweep_kernel
   if constexpr (kSegments) {
     const int steps = min(max(len - u_begin, 0), u_end - u_begin);
     if (vb == 0 && threadIdx.x == 0) {
-      a.seg_through[head * a.nseg + seg] = cut ? 0.0f : decay_pow(g, (float)steps);
+      a.seg_through[head * a.nseg + seg] = cut ? kCut : decay_pow(g, (float)steps);
       if constexpr (kRate) a.seg_steps[head * a.nseg + seg] = (float)steps;
     }
   } else if constexpr (MODE == kAttnDecay) {
@@ -1068,10 +1076,10 @@ __global__ __launch_bounds__(256) void attn_carry_kernel(const AttnSweeps all, b
       if (k + 1 >= nseg) break;
       const float t = th[k];
       if (rate != nullptr) {
-        r = t == 0.0f ? more[u] : __builtin_fmaf(t, __builtin_fmaf(steps[head * nseg + k], s, r), more[u]);
+        r = t == kCut ? more[u] : __builtin_fmaf(t, __builtin_fmaf(steps[head * nseg + k], s, r), more[u]);
         rate[first + (int64_t)(k + 1) * mat] = r;
       }
-      s = t == 0.0f ? added[u] : __builtin_fmaf(t, s, added[u]);
+      s = t == kCut ? added[u] : __builtin_fmaf(t, s, added[u]);
       state[first + (int64_t)(k + 1) * mat] = s;
     }
   }

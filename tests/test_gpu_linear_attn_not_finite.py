@@ -1,0 +1,110 @@
+"""GPU tests of values that are not finite in the linear attention (include/ssm_linear_attn.h): what they reach by the
+recurrence is not finite, and nothing else is other than it was -- with starts and without, in rows of one piece and split
+ones, of every width's kernels, and where the decay of a step underflows."""
+import pytest
+import torch
+
+from tests import heads_ref as ref
+from tests.test_gpu_linear_attn import make, rows_of
+
+pytestmark = pytest.mark.gpu
+
+SHAPES = [(200, 20, 40), (200, 64, 64), (190, 128, 128), (130, 256, 200), (1300, 64, 64), (1300, 128, 128)]
+
+
+@pytest.fixture(scope="module")
+def dev():
+    assert torch.cuda.is_available(), "GPU tests need a GPU"
+    import selective_state_space_28_amd as ssm
+    ssm.load()
+    return torch.device("cuda:0")
+
+
+def inputs(dev, dtype, L, dk, dv, starts, g):
+    import selective_state_space_28_amd as ssm
+    p = make(dev, dtype, 1, L, 2, dk, dv, packed=starts, g=[0.5 * g, g], seed=31)
+    if starts:  # one, well behind the value
+        p["starts"].zero_()
+        p["starts"][0, L - 20] = 1
+    if L > 1000:
+        assert ssm.ssm_linear_attn_fwd_workspace_bytes(1, L, 2, dk, dv, p["q"].dtype) > 0  # split
+    return p
+
+
+def same(a, b, what):
+    assert torch.equal(a, b), what
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("L,dk,dv", SHAPES)
+@pytest.mark.parametrize("starts", [False, True])
+@pytest.mark.parametrize("g", [-0.02, -90.0, -200.0])
+def test_forward(dev, dtype, L, dk, dv, starts, g):
+    import selective_state_space_28_amd as ssm
+    p = inputs(dev, dtype, L, dk, dv, starts, g)
+    kw = dict(rows_of(p), return_last_state=True)
+    clean, clean_last = ssm.ssm_linear_attn_fwd(p["q"], p["k"], p["v"], p["g"], **kw)
+    at, c = 70, 3
+    for which in ("q", "k", "v", "h0"):
+        for value in (float("nan"), float("inf"), float("-inf")):
+            args = {n: p[n].clone() for n in ("q", "k", "v", "h0")}
+            args[which][(0, 1, c, c) if which == "h0" else (0, at, 1, c)] = value
+            y, last = ssm.ssm_linear_attn_fwd(args["q"], args["k"], args["v"], p["g"], **dict(kw, h0=args["h0"]))
+            want, want_last = ref.attn_steps(args["q"], args["k"], args["v"], p["g"], dk ** -0.5, starts=p["starts"],
+                                             h0=args["h0"])
+            what = f"{which} {value}"
+            assert torch.equal(torch.isfinite(y.cpu()), torch.isfinite(want)), what
+            assert torch.equal(torch.isfinite(last.cpu()), torch.isfinite(want_last)), what
+            reached = ~torch.isfinite(want).to(dev)
+            assert bool(reached.any()), what
+            same(torch.where(reached, 0, y), torch.where(reached, 0, clean), what)
+            reached = ~torch.isfinite(want_last).to(dev)
+            assert bool(reached.any()) == (not starts and which != "q"), what
+            same(torch.where(reached, 0, last), torch.where(reached, 0, clean_last), what)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("L,dk,dv", SHAPES)
+@pytest.mark.parametrize("starts", [False, True])
+@pytest.mark.parametrize("g", [-0.02, -90.0, -200.0])
+def test_gradients(dev, dtype, L, dk, dv, starts, g):
+    """A gradient of y at step t, column c, reaches dq of that step, dk and dv (of that column) of it and the ones before it,
+    and dh0."""
+    import selective_state_space_28_amd as ssm
+    p = inputs(dev, dtype, L, dk, dv, starts, g)
+    if starts:
+        p["starts"].zero_()
+        p["starts"][0, 30] = 1
+    args = (p["q"], p["k"], p["v"], p["g"])
+    kw = dict(rows_of(p), dlast_state=p["dlast"])
+    clean = ssm.ssm_linear_attn_bwd(*args, dy=p["dy"], **kw)
+    t, c, first = L - 40, 5, 30 if starts else 0
+    for value in (float("nan"), float("inf")):
+        dy = p["dy"].clone()
+        dy[0, t, 1, c] = value
+        got = ssm.ssm_linear_attn_bwd(*args, dy=dy, **kw)
+        reached = {name: torch.zeros_like(clean[name], dtype=torch.bool) for name in ("dq", "dk", "dv", "dh0")}
+        reached["dq"][0, t, 1] = True
+        reached["dk"][0, first:t + 1, 1] = True
+        reached["dv"][0, first:t + 1, 1, c] = True
+        if not starts:
+            reached["dh0"][0, 1, :, c] = True
+        for name, r in reached.items():
+            assert torch.equal(torch.isfinite(got[name]), ~r), f"{name} {value}"
+            same(torch.where(r, 0, got[name]), torch.where(r, 0, clean[name]), f"{name} {value}")
+        assert not bool(torch.isfinite(got["dlog_decay"][1])) and torch.equal(got["dlog_decay"][0], clean["dlog_decay"][0])
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("starts", [False, True])
+def test_no_scale(dev, dtype, starts):
+    """0 q_t S_t is no number where q_t or S_t is none."""
+    import selective_state_space_28_amd as ssm
+    p = inputs(dev, dtype, 200, 32, 48, starts, -0.02)
+    for which in "qkv":
+        args = {n: p[n].clone() for n in "qkv"}
+        args[which][0, 70, 1, 3] = float("nan")
+        y = ssm.ssm_linear_attn_fwd(args["q"], args["k"], args["v"], p["g"], **rows_of(p), scale=0.0)
+        want, _ = ref.attn_steps(args["q"], args["k"], args["v"], p["g"], 0.0, starts=p["starts"], h0=p["h0"])
+        assert torch.equal(torch.isfinite(y.cpu()), torch.isfinite(want)), which
+        assert not bool(torch.nan_to_num(y).any()), which
