@@ -425,8 +425,20 @@ struct ScoreTiles {
 __device__ __forceinline__ int tile_row(int tile) { return (0xffa94 >> (2 * tile)) & 3; }
 __device__ __forceinline__ int tile_col(int tile) { return (0xe4910 >> (2 * tile)) & 3; }
 
-// What a segment leaves of the state that enters it where a sequence starts in it: nothing.
+// What a segment leaves of the state that enters it: e^{g steps}; -1 (nothing) where a
+// sequence starts in it; and where a growing head's factor passes float32's range,
+// minus its fourth root, more than 1: a state of 0 stays 0, and a small one need not overflow.
+// (Four factors reach e^355: the smallest float passes the range before that.)
 constexpr float kCut = -1.0f;
+__device__ __forceinline__ float through_of(float g, int steps, bool cut) {
+  const float t = decay_pow(g, (float)steps);
+  return cut ? kCut : t == __builtin_inff() ? -decay_pow(g, 0.25f * (float)steps) : t;
+}
+__device__ __forceinline__ float carried(float t, float s, float added) {
+  if (t == kCut) return added;
+  if (t < kCut) return s == 0.0f ? added : __builtin_fmaf(s * t * t * t, t, added);
+  return __builtin_fmaf(t, s, added);
+}
 
 enum AttnMode { kAttnOut = 0, kAttnSegments = 1, kAttnDecay = 2, kAttnDecaySegments = 3 };
 
@@ -988,7 +1000,7 @@ __global__ __launch_bounds__(kThreads, KD <= 128 ? 2 : 1) void attn_sweep_kernel
   if constexpr (kSegments) {
     const int steps = min(max(len - u_begin, 0), u_end - u_begin);
     if (vb == 0 && threadIdx.x == 0) {
-      a.seg_through[head * a.nseg + seg] = cut ? kCut : decay_pow(g, (float)steps);
+      a.seg_through[head * a.nseg + seg] = through_of(g, steps, cut);
       if constexpr (kRate) a.seg_steps[head * a.nseg + seg] = (float)steps;
     }
   } else if constexpr (MODE == kAttnDecay) {
@@ -1076,10 +1088,10 @@ __global__ __launch_bounds__(256) void attn_carry_kernel(const AttnSweeps all, b
       if (k + 1 >= nseg) break;
       const float t = th[k];
       if (rate != nullptr) {
-        r = t == kCut ? more[u] : __builtin_fmaf(t, __builtin_fmaf(steps[head * nseg + k], s, r), more[u]);
+        r = carried(t, __builtin_fmaf(steps[head * nseg + k], s, r), more[u]);
         rate[first + (int64_t)(k + 1) * mat] = r;
       }
-      s = t == kCut ? added[u] : __builtin_fmaf(t, s, added[u]);
+      s = carried(t, s, added[u]);
       state[first + (int64_t)(k + 1) * mat] = s;
     }
   }

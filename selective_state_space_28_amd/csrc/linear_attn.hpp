@@ -41,7 +41,7 @@ struct AttnSweep {
   float* seg_state;   // (batch, heads, nseg, kd, vd): states entering the segments, when nseg > 1
   float* seg_rate;    // the decay's gradient only: its derivative by g, as seg_state
   float* seg_steps;   // and the steps of the segments, as seg_through
-  float* seg_through; // (batch, heads, nseg): what a segment leaves of the state that enters it; -1: a start cuts it off
+  float* seg_through; // (batch, heads, nseg): what a segment leaves of the state that enters it (through_of)
   int64_t seglen;     // steps of a segment, a multiple of kAttnChunk
   int nseg;
   double* part;       // decay's gradient: (heads, batch, column blocks, nseg)
