@@ -29,7 +29,9 @@
  *    Pointers need their element's alignment only.
  *  - Every sum is held in float32 or wider, the variance taken about the mean;
  *    outputs are rounded once.  A group of equal values has exactly that mean and
- *    variance 0: n is the bias (NaN where eps is 0 too).
+ *    variance 0: n is the bias (NaN where eps is 0 too).  Deviations may be of any
+ *    size, past float32's range too (a group partly at the type's lowest value):
+ *    rstd may then be subnormal, with its fewer bits, and the backward has these.
  *  - A NaN or Inf in one group makes that group NaN where the formula does and
  *    leaves the others alone.
  */

@@ -54,6 +54,13 @@ template <typename T>
 using GroupSum = typename std::conditional<sizeof(T) == 4, double, float>::type;
 constexpr float kSumScale = 1.0f / 65536;
 
+// Groups whose squares pass float32's range (a part of a group at the type's lowest value, as
+// masks have it) are taken again with deviations scaled by kFar: of up to 2^129, their squares
+// sum to less than 2^112; of those whose squares passed 2^128 some exceed 2^57, 2^-23 scaled.
+// The backward scales by kFarBack where rstd is below kFarRstd: deviations that pass the
+// range have one below 2^-121, which may be subnormal; its product with 1 / kFarBack is exact.
+constexpr float kFar = 0x1p-80f, kFarBack = 0x1p-24f, kFarRstd = 0x1p-100f, kMostFloat = 3.4028234664e38f;
+
 __device__ __forceinline__ void load_par(const float* p, int valid, float otherwise, float (&f)[kRun]) {
   if (p == nullptr) {
 #pragma unroll
@@ -158,18 +165,29 @@ __global__ __launch_bounds__(kBlockSpan) void group_norm_fwd_kernel(const GroupN
     }
     sum = group_sum<LR>(sum, s_mean);
     const float mean = sizeof(T) == 4 ? (float)(sum * rn) : (float)sum / n * (1.0f / kSumScale);
-    float sq = 0.0f;
+    // the sum of the squares of the deviations, formed again for each use: v * scale - m
+    float scale = 1.0f, m = mean;
+    const auto sum_of_squares = [&] {
+      float sq = 0.0f;
 #pragma unroll
-    for (int c = 0; c < K; ++c)
+      for (int c = 0; c < K; ++c)
 #pragma unroll
-      for (int k = 0; k < kRun; ++k) {
-        v[c][k] -= mean;
-        sq += k < valid[c] ? v[c][k] * v[c][k] : 0.0f;
-      }
-    const float rstd = 1.0f / __builtin_sqrtf(group_sum<LR>(sq, s_var) / n + a.eps);
+        for (int k = 0; k < kRun; ++k) {
+          const float d = __builtin_fmaf(v[c][k], scale, -m);
+          sq += k < valid[c] ? d * d : 0.0f;
+        }
+      return group_sum<LR>(sq, s_var);
+    };
+    float squares = sum_of_squares();
+    if (!(squares <= kMostFloat)) {  // (alike in all lanes of the group)
+      scale = kFar;
+      m = mean * kFar;
+      squares = sum_of_squares();
+    }
+    const float rstd = 1.0f / __builtin_sqrtf(squares / n + a.eps * scale * scale);  // of the scaled deviations
     if (p.lane == 0) {
       if (a.mean != nullptr) a.mean[t * a.groups + p.group] = mean;
-      if (a.rstd != nullptr) a.rstd[t * a.groups + p.group] = rstd;
+      if (a.rstd != nullptr) a.rstd[t * a.groups + p.group] = rstd * scale;
     }
 #pragma unroll
     for (int c = 0; c < K; ++c) {
@@ -177,7 +195,7 @@ __global__ __launch_bounds__(kBlockSpan) void group_norm_fwd_kernel(const GroupN
       if (z != nullptr) run_floats<T>(zw[c], f);
 #pragma unroll
       for (int k = 0; k < kRun; ++k) {
-        const float u = __builtin_fmaf(v[c][k] * rstd, w[c][k], bias[c][k]);
+        const float u = __builtin_fmaf(__builtin_fmaf(v[c][k], scale, -m) * rstd, w[c][k], bias[c][k]);
         f[k] = z != nullptr ? u * act_of(a.act, f[k], slope) : act_of(a.act, u, slope);
       }
       store_run<T, sizeof(T) == 2>(y + t * a.dim + at[c], valid[c], f);
@@ -213,6 +231,8 @@ __global__ __launch_bounds__(kBlockSpan) void group_norm_bwd_kernel(const GroupN
   for (int64_t t = p.token; t < a.tokens; t += p.step) {
     if (!p.live) break;
     const float mean = a.mean[t * a.groups + p.group], rstd = a.rstd[t * a.groups + p.group];
+    const bool far = rstd < kFarRstd;
+    const float scale = far ? kFarBack : 1.0f, m = mean * scale, r = far ? rstd * (1.0f / kFarBack) : rstd;
     float xh[K][kRun], d[K][kRun];
     float s1 = 0.0f, s2 = 0.0f;
 #pragma unroll
@@ -224,7 +244,7 @@ __global__ __launch_bounds__(kBlockSpan) void group_norm_bwd_kernel(const GroupN
 #pragma unroll
       for (int k = 0; k < kRun; ++k) {
         const bool in = k < valid[c];
-        xh[c][k] = in ? (xh[c][k] - mean) * rstd : 0.0f;
+        xh[c][k] = in ? __builtin_fmaf(xh[c][k], scale, -m) * r : 0.0f;
         const float u = __builtin_fmaf(xh[c][k], w[c][k], bias[c][k]);
         float slope, dn;
         if (z != nullptr) {
