@@ -112,3 +112,43 @@ def test_growing_heads_in_long_segments(dev, dtype, state, dk, dv):
             assert not bool(t[:, n:].any()), name
             t = t[:, :n]
         ref.within(t, want[name], b, name)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("dk,dv", [(64, 64), (128, 128), (128, 64), (64, 128), (100, 200), (200, 100), (256, 256), (256, 40)])
+@pytest.mark.parametrize("L,packed,lengths", [(1000, False, None), (1111, True, None), (1030, False, [700])])
+def test_split_rows_of_every_width(dev, dtype, dk, dv, L, packed, lengths):
+    """Rows in segments, through which a slow decay carries the states from end to end: in every width's kernels, with the
+    gradients' sweeps side by side (widths alike) and after one another."""
+    import selective_state_space_28_amd as ssm
+    p = make(dev, dtype, 1, L, 2, dk, dv, hk=1, packed=packed, lengths=lengths, g=[-0.002, -0.0005], seed=23)
+    state = 2 * dk * dv * 4  # of one segment
+    assert ssm.ssm_linear_attn_fwd_workspace_bytes(1, L, 2, dk, dv, p["q"].dtype) >= 2 * state
+    assert ssm.ssm_linear_attn_bwd_workspace_bytes(1, L, 2, 2, 1, 2, dk, dv, p["q"].dtype) >= 4 * state
+    near(p, dtype, L)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("L", [1, 64, 200, 900])
+def test_decay_gradient_of_a_state_is_float32(dev, dtype, L):
+    """A state of one element that meets one query at the last step, or only the last state's gradient: the decay's
+    gradient is L e^(g L) times a product without a sum.  16 half steps of float32 for the decays of each 32 steps, 16 for
+    the products and the scale."""
+    import selective_state_space_28_amd as ssm
+    gen = torch.Generator().manual_seed(19 + L)
+    heads = 64
+    g = -0.02 * torch.rand(heads, generator=gen)
+    h0 = 1 + torch.rand(1, heads, 1, 1, generator=gen)  # 24 bits of it
+    q, k, v, dy = (torch.zeros(1, L, heads, 1, dtype=ref.TYPES[dtype]) for _ in range(4))
+    q[0, -1], dy[0, -1] = ((1 + torch.rand(heads, 1, generator=gen)).to(q.dtype) for _ in range(2))
+    dlast = 1 + torch.rand(1, heads, 1, 1, generator=gen)
+    state = L * torch.exp(L * g.double()) * h0[0, :, 0, 0].double()
+    slack = (16 * (L // 32 + 1) + 16) * ref.EPS32
+    ops = [t.to(dev) for t in (q, k, v, g)]
+    got = ssm.ssm_linear_attn_bwd(*ops, scale=0.75, h0=h0.to(dev), dy=dy.to(dev))["dlog_decay"]
+    want = 0.75 * state * q[0, -1, :, 0].double() * dy[0, -1, :, 0].double()
+    ref.within(got, want, slack * want.abs(), "by a query")
+    got = ssm.ssm_linear_attn_bwd(*ops, scale=0.75, h0=h0.to(dev), dy=torch.zeros_like(dy).to(dev),
+                                  dlast_state=dlast.to(dev))["dlog_decay"]
+    want = state * dlast[0, :, 0, 0].double()
+    ref.within(got, want, slack * want.abs(), "by the last state")
