@@ -21,14 +21,15 @@
 // each of its waves.  S never leaves the matrix cores' accumulators.  16-bit operands use
 // v_mfma_f32_16x16x32_bf16, float32 v_mfma_f32_16x16x4_f32.  HBM sees q, k, v and y once
 // (and k and v once more where rows are split); batch 16, L 2048, 32 heads of 128, bf16:
-// 280 to 340 us by the clock, 3.2 to 3.8 TB/s.  What bounds it there is the chain of a chunk, with two
-// waves to a SIMD: VALUs busy 0.52 of the time (the parts of S and of the decayed v, the
-// decay of S), matrix cores 0.34, LDS 0.30.  8 waves of 16 columns, four to a SIMD, spill or
+// 290 to 335 us by the clock, 3.2 to 3.7 TB/s.  What bounds it there is the chain of a chunk, with two
+// waves to a SIMD: VALUs busy 0.51 of the time (the parts of S and of the decayed v, the
+// decay of S), matrix cores 0.34, LDS 0.33.  8 waves of 16 columns, four to a SIMD, spill or
 // read LDS twice as often: 385 us for 327.
 //
 // Roundings with bf16 storage.  The decayed v, whose products with k make the float32
 // state, goes in three parts, which is exact.  P as it meets V, and S as it meets q, go in
-// two (2^-16): one part, rounded, would leave its 2^-9 in every output.  The decay's
+// two (2^-16): one part, rounded, would leave its 2^-9 in every output, for 295 us in place of 326
+// (S) and 495 in place of 512 (P, batch 16, L 2048, 40 heads of 128).  The decay's
 // gradient, a float32 output, has P, S and R in three parts each.
 #include "linear_attn.hpp"
 #include "runs.hpp"
@@ -1201,8 +1202,8 @@ namespace {
 
 // Tiles of value columns of a wave: 128 columns to a workgroup, or 64 (heads of up to 64
 // values would leave half of them idle; of wider ones two tiles share what a wave reads
-// of Q, K and P: batch 16, L 2048, 32 heads of 128 bf16 take 327 us with two, as much work in
-// 64 heads of 64 values takes 490).
+// of Q, K and P: batch 16, L 2048, 32 heads of 128 bf16 take 330 us with two, as much work in
+// 64 heads of 64 values takes 410).
 int column_tiles(int vd) { return vd <= 64 ? 1 : 2; }
 
 template <typename T, int KD, int CT, int MODE>
@@ -1269,8 +1270,10 @@ int attn_decay_blocks(int vd) { return (vd + 63) / 64; }
 // cores, 2.4 times as much.  Segments fill the CUs, and cost the pass that finds their states
 // (0.58 of the main one's time) with two more launches and the states' traffic, some 20 us and
 // more.  The least of these sums is taken, of up to 64 segments (batch 8, L 2048 bf16: 16 heads
-// 173 us in one piece, 133 in segments; 32 heads 202 and 244; one row of 512 steps, 12 heads,
-// float32: 107 and 40).
+// 182 us in one piece, 137 in segments; 32 heads 203 and 244; one row of 512 steps, 12 heads,
+// float32: 112 and 45).  The same times are taken for the kernels that have one workgroup to a CU
+// (key heads above 128; the decay's gradient of bf16 key heads above 64), whose 257 to 512
+// workgroups are two rounds and are counted as one.
 AttnSplit attn_split(int64_t groups, int64_t seqlen, int64_t state_elements, Dtype dtype) {
   const int64_t chunks = (seqlen + kAttnChunk - 1) / kAttnChunk;
   const double slower = dtype == Dtype::F32 ? 2.4 : 1.0;

@@ -38,7 +38,7 @@ def same(a, b, what):
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 @pytest.mark.parametrize("L,dk,dv", SHAPES)
 @pytest.mark.parametrize("starts", [False, True])
-@pytest.mark.parametrize("g", [-0.02, -90.0, -200.0])
+@pytest.mark.parametrize("g", [-0.02, -90.0, -200.0, float("-inf")])
 def test_forward(dev, dtype, L, dk, dv, starts, g):
     import selective_state_space_28_amd as ssm
     p = inputs(dev, dtype, L, dk, dv, starts, g)
@@ -55,6 +55,9 @@ def test_forward(dev, dtype, L, dk, dv, starts, g):
             what = f"{which} {value}"
             assert torch.equal(torch.isfinite(y.cpu()), torch.isfinite(want)), what
             assert torch.equal(torch.isfinite(last.cpu()), torch.isfinite(want_last)), what
+            if value != value:
+                assert torch.equal(torch.isnan(y.cpu()), torch.isnan(want)), what
+                assert torch.equal(torch.isnan(last.cpu()), torch.isnan(want_last)), what
             reached = ~torch.isfinite(want).to(dev)
             assert bool(reached.any()), what
             same(torch.where(reached, 0, y), torch.where(reached, 0, clean), what)
