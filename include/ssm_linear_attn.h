@@ -39,12 +39,13 @@
  *    decayed products q_t . k_s as they meet v on the matrix cores, and the state as
  *    it meets q, are two bf16 parts (2^-16 of each, and what lies below 2^-126); in
  *    dlog_decay both are exact.
- *  - log_decay is not checked for sign; a positive one grows: of up to 1.38, so that
- *    e^(64 log_decay) is a float32 (above it results may be NaN where the formula's
- *    are finite).  -inf forgets all but the step itself, of finite values.  A decay
- *    over many steps that underflows is held at the smallest normal float where
- *    log_decay > -87; a state that is not finite stays so until the next start,
- *    whatever the decay.
+ *  - log_decay is not checked for sign; a positive one grows.  e^(64 log_decay), by
+ *    itself and times the values of v, dy and q.k, has to be a float32: log_decay is at
+ *    most 1.38, and 1.3 leaves room for values of 100 (above that, results may be NaN
+ *    where the formula's are finite).  -inf forgets all but the step itself, of finite
+ *    values.  A decay over many steps that underflows is held at the smallest normal
+ *    float where log_decay > -87; a state that is not finite stays so until the next
+ *    start, whatever the decay.
  *  - What a NaN or Inf reaches by the formula is not finite.  An Inf may be NaN there:
  *    the factors of a product are taken in parts, Inf - Inf one of them, and a value
  *    that is not finite makes the later y of its chunk NaN.  Earlier steps, sequences of

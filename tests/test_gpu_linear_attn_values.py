@@ -115,6 +115,16 @@ def test_growing_heads_in_long_segments(dev, dtype, state, dk, dv):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("packed", [False, True])
+@pytest.mark.parametrize("L", [1, 33, 64])
+def test_heads_that_grow_fast(dev, dtype, packed, L):
+    """e^1.3 a step, 1.4e36 over 64 of them: small keys, and no state, keep the formula's outputs in float32's range."""
+    p = make(dev, dtype, 2, L, 2, 32, 48, packed=packed, state=False, g=[1.3, 0.9], seed=24)
+    p["k"] *= 1e-30
+    near(p, dtype, L)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("dk,dv", [(64, 64), (128, 128), (128, 64), (64, 128), (100, 200), (200, 100), (256, 256), (256, 40)])
 @pytest.mark.parametrize("L,packed,lengths", [(1000, False, None), (1111, True, None), (1030, False, [700])])
 def test_split_rows_of_every_width(dev, dtype, dk, dv, L, packed, lengths):
